@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -19,6 +20,8 @@ __all__ = [
     "fp4_scale_max_workspace_bytes",
     "fp4_dequant", "fp4_gemm", "fp4_quantize_mxfp8", "fp4_mx_to_mxfp8", "fp4_mx_dequant_fp8", "fp4_gemm_w4a8", "fp4_fake_quant",
     "fp4_ste_backward", "fp4_kv_append_mx", "fp4_moe_grouped_gemm", "fp4_moe_workspace_bytes", "MoeDebug",
+    "fp4_qk_norm_rope", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
+    "fp4_kv_free", "fp4_kv_compact", "fp4_kv_copy_pages",
     "fp4_abi_version", "LIB_PATH",
 ]
 
@@ -35,6 +38,21 @@ class MoeDebug(_c.Structure):
     _fields_ = [("x_codes", _vp), ("x_scales", _vp), ("counts", _vp), ("offsets", _vp), ("perm", _vp), ("gate_up", _vp),
                 ("h_bf16", _vp), ("h_codes", _vp), ("h_scales", _vp), ("y", _vp),
                 ("gate_up_in", _vp), ("h_codes_in", _vp), ("h_scales_in", _vp), ("stage_events", _vp * 6)]
+
+
+class _KvCacheC(_c.Structure):
+    """Mirror of struct fp4_kv_cache."""
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp), ("num_pages", _i64),
+                ("d", _i64), ("page_size", _i64)]
+
+
+class _KvPagesC(_c.Structure):
+    """Mirror of struct fp4_kv_pages."""
+    _fields_ = [("page_table", _vp), ("page_counts", _vp), ("seq_lens", _vp), ("page_refs", _vp), ("batch", _i64),
+                ("max_pages", _i64), ("num_pages", _i64)]
+
+
+_cache_p, _pages_p = _c.POINTER(_KvCacheC), _c.POINTER(_KvPagesC)
 
 
 _SIGS = {
@@ -59,6 +77,14 @@ _SIGS = {
     "fp4_moe_grouped_gemm": (_i32, [_i32, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _vp,
                                      _vp, _vp, _vp, _vp, _vp, _vp, _sz, _c.POINTER(MoeDebug), _vp]),
     "fp4_moe_workspace_bytes": (_sz, [_i32, _i64, _i64, _i32, _i32, _i64]),
+    "fp4_qk_norm_rope": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _c.c_float, _vp, _i64, _i32,
+                                _i32, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "fp4_kv_reserve": (_i32, [_cache_p, _pages_p, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "fp4_kv_reserve_workspace_bytes": (_sz, [_i64, _i64]),
+    "fp4_kv_fork": (_i32, [_pages_p, _vp, _i64, _i64, _vp]),
+    "fp4_kv_free": (_i32, [_pages_p, _vp, _i64, _vp, _i64, _vp]),
+    "fp4_kv_compact": (_i32, [_cache_p, _pages_p, _vp, _i64, _vp, _vp]),
+    "fp4_kv_copy_pages": (_i32, [_cache_p, _cache_p, _vp, _vp, _i64, _vp]),
 }
 
 
@@ -130,6 +156,23 @@ class _Args:
         for name, t in self.items:
             if t.device.type != "cuda":
                 raise ValueError(f"{self.fn}: {name} must be on the GPU, got a {t.device.type} tensor")
+
+    def call(self, stream, *args):
+        """Checks that all tensors are on one GPU, then calls the C entry point
+        with args and the stream (that GPU's current one by default), with that
+        GPU as the current device."""
+        self.on_device()
+        dev = self.items[0][1].device
+        for name, t in self.items:
+            if t.device != dev:
+                raise ValueError(f"{self.fn}: {name} is on {t.device}, {self.items[0][0]} on {dev}")
+        f = getattr(lib, self.fn)
+        if torch.cuda.current_device() == dev.index:
+            status = f(*args, _stream(stream))
+        else:
+            with torch.cuda.device(dev):
+                status = f(*args, _stream(stream))
+        _check(self.fn, status)
 
 
 def _shape(fn, name, t, shape, rows_at_least=False):
@@ -422,3 +465,166 @@ def fp4_moe_grouped_gemm(fmt, x, topk_ids, topk_weights, num_experts, inter, w13
         fmt, _ptr(x), tokens, hidden, _ptr(topk_ids), _ptr(topk_weights), topk, num_experts, inter,
         _ptr(w13_codes), _ptr(w13_scales), _ptr(w13_tensor_scales), _ptr(w2_codes), _ptr(w2_scales),
         _ptr(w2_tensor_scales), _ptr(act_tensor_scales), _ptr(out), _ptr(workspace), wsb, dbg, _stream(stream)))
+
+
+def _heads(a, name, t):
+    """A bf16 [tokens, heads, head_dim] tensor whose heads lie one after another;
+    tokens may be any number of elements apart.  Returns its leading dimension."""
+    a(name, t, _BF16, dense=False)
+    if t.dim() != 3:
+        raise ValueError(f"{a.fn}: {name} must be [tokens, heads, head_dim], got shape {tuple(t.shape)}")
+    if t.numel() and t.size(1) > 1 and t.stride(1) != t.size(2):
+        raise ValueError(f"{a.fn}: the heads of {name} must be contiguous")
+    return t.stride(0) if t.size(0) > 1 else t.size(1) * t.size(2)
+
+
+def fp4_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, stream=None):
+    """q [tokens, q_heads, head_dim], k [tokens, kv_heads, head_dim]: their rms
+    norms and rotation into q_out and k_out (which may be q and k).  cos_sin:
+    fp32 [max_positions, rot_dim]; None: norms only."""
+    a = _Args("fp4_qk_norm_rope")
+    ld_q, ld_k = _heads(a, "q", q), _heads(a, "k", k)
+    ld_qo, ld_ko = _heads(a, "q_out", q_out), _heads(a, "k_out", k_out)
+    tokens, q_heads, head_dim = q.shape
+    kv_heads = k.shape[1]
+    if k.shape[0] != tokens or k.shape[2] != head_dim:
+        raise ValueError(f"{a.fn}: k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError(f"{a.fn}: q_out and k_out must have the shapes of q and k")
+    w_dtypes = _OUT if q_weight is None else (q_weight.dtype,) if k_weight is not None else _OUT
+    for nm, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        a(nm, w, _OUT if nm == "q_weight" else w_dtypes, optional=True)
+        if w is not None and tuple(w.shape) != (head_dim,):
+            raise ValueError(f"{a.fn}: {nm} has shape {tuple(w.shape)}, expected {(head_dim,)}")
+    weight = q_weight if q_weight is not None else k_weight
+    rot_dim = places = 0
+    if cos_sin is not None:
+        a("cos_sin", cos_sin, _F32)("positions", positions, _I32)
+        if cos_sin.dim() != 2 or tuple(positions.shape) != (tokens,):
+            raise ValueError(f"{a.fn}: cos_sin must be [max_positions, rot_dim] and positions [tokens]")
+        places, rot_dim = cos_sin.shape
+    a.call(stream, _ptr(q), _ptr(k), tokens, q_heads, kv_heads, head_dim, ld_q, ld_k, _ptr(q_weight), _ptr(k_weight),
+           DT_F32 if weight is not None and weight.dtype == torch.float32 else DT_BF16, eps, _ptr(cos_sin), places,
+           rot_dim, int(bool(interleaved)), _ptr(positions) if rot_dim else None, _ptr(q_out), ld_qo, _ptr(k_out), ld_ko)
+
+
+class KvCache(NamedTuple):
+    """A paged MXFP4 cache in fp4_kv_append_mx's layout: uint8 codes
+    [num_pages * page_size, d/2] and scales [num_pages * page_size, d/32] of the
+    keys and of the values (both None: a keys-only cache)."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor | None
+    v_scales: torch.Tensor | None
+    page_size: int
+
+
+class KvPages(NamedTuple):
+    """The pages that the sequences of a batch hold: int32 page_table
+    [batch, max_pages] (-1 = none), page_counts [batch], seq_lens [batch]
+    (committed tokens) and page_refs [num_pages] (holders; 0 = free)."""
+    page_table: torch.Tensor
+    page_counts: torch.Tensor
+    seq_lens: torch.Tensor
+    page_refs: torch.Tensor
+
+
+def _kv_cache(a, cache, name="cache"):
+    """Checks a KvCache's arrays and returns its C mirror."""
+    kc, ks, vc, vs, page_size = cache
+    fn = a.fn
+    a(f"{name}.k_codes", kc, _U8)(f"{name}.k_scales", ks, _U8)
+    a(f"{name}.v_codes", vc, _U8, optional=True)(f"{name}.v_scales", vs, _U8, optional=True)
+    if kc.dim() != 2 or page_size <= 0 or kc.shape[0] % page_size:
+        raise ValueError(f"{fn}: {name}.k_codes must be [num_pages * {page_size}, d/2], got {tuple(kc.shape)}")
+    rows, half = kc.shape
+    if ks.shape != (rows, half // 16):
+        raise ValueError(f"{fn}: {name}.k_scales has shape {tuple(ks.shape)}, expected {(rows, half // 16)}")
+    if (vc is None) != (vs is None):
+        raise ValueError(f"{fn}: {name}.v_codes and v_scales must both be given or both be None")
+    if vc is not None and (vc.shape != kc.shape or vs.shape != ks.shape):
+        raise ValueError(f"{fn}: the values of {name} must have the shapes of its keys")
+    return _KvCacheC(_ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), rows // page_size, 2 * half, page_size)
+
+
+def _kv_pages(a, pages):
+    """Checks a KvPages' arrays and returns its C mirror."""
+    table, counts, lens, refs = pages
+    a("page_table", table, _I32)("page_counts", counts, _I32)("seq_lens", lens, _I32)("page_refs", refs, _I32)
+    if table.dim() != 2 or counts.shape != table.shape[:1] or lens.shape != table.shape[:1] or refs.dim() != 1:
+        raise ValueError(f"{a.fn}: page_table must be [batch, max_pages], page_counts and seq_lens [batch], "
+                         "page_refs [num_pages]")
+    return _KvPagesC(_ptr(table), _ptr(counts), _ptr(lens), _ptr(refs), table.shape[0], table.shape[1], refs.shape[0])
+
+
+def _per_seq(a, name, t, n, optional=False):
+    a(name, t, _I32, optional=optional)
+    if t is not None and tuple(t.shape) != (n,):
+        raise ValueError(f"{a.fn}: {name} has shape {tuple(t.shape)}, expected {(n,)}")
+
+
+def fp4_kv_reserve_workspace_bytes(batch: int, num_pages: int) -> int:
+    return lib.fp4_kv_reserve_workspace_bytes(batch, num_pages)
+
+
+def fp4_kv_reserve(cache: KvCache, pages: KvPages, new_tokens, slots, n_short, workspace, stream=None):
+    """Room for new_tokens[b] tokens behind every sequence; their cache rows in
+    slots [batch, max_new] (None: not wanted), -1 past new_tokens[b]."""
+    a = _Args("fp4_kv_reserve")
+    c, p = _kv_cache(a, cache), _kv_pages(a, pages)
+    _per_seq(a, "new_tokens", new_tokens, p.batch)
+    a("slots", slots, _I32, optional=True)
+    if slots is not None and (slots.dim() != 2 or slots.shape[0] != p.batch):
+        raise ValueError(f"{a.fn}: slots has shape {tuple(slots.shape)}, expected [{p.batch}, max_new]")
+    _per_seq(a, "n_short", n_short, 1)
+    a("workspace", workspace, _U8)
+    a.call(stream, _c.byref(c), _c.byref(p), _ptr(new_tokens), _ptr(slots), 0 if slots is None else slots.shape[1],
+           _ptr(n_short), _ptr(workspace), workspace.numel())
+
+
+def fp4_kv_fork(pages: KvPages, pairs, page_size: int, stream=None):
+    """pairs int32 [n, 2]: (source, target) sequences."""
+    a = _Args("fp4_kv_fork")
+    p = _kv_pages(a, pages)
+    a("pairs", pairs, _I32)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError(f"{a.fn}: pairs has shape {tuple(pairs.shape)}, expected [n, 2]")
+    a.call(stream, _c.byref(p), _ptr(pairs), pairs.shape[0], page_size)
+
+
+def fp4_kv_free(pages: KvPages, seqs, page_size: int, keep_lens=None, stream=None):
+    """Cuts the sequences seqs int32 [n] back to keep_lens int32 [n] tokens (None: none)."""
+    a = _Args("fp4_kv_free")
+    p = _kv_pages(a, pages)
+    a("seqs", seqs, _I32)
+    if seqs.dim() != 1:
+        raise ValueError(f"{a.fn}: seqs has shape {tuple(seqs.shape)}, expected [n]")
+    _per_seq(a, "keep_lens", keep_lens, seqs.shape[0], optional=True)
+    a.call(stream, _c.byref(p), _ptr(seqs), seqs.shape[0], _ptr(keep_lens), page_size)
+
+
+def fp4_kv_compact(cache: KvCache, pages: KvPages, accepted, accepted_lens, stream=None):
+    """Commits the drafted tokens accepted[b, :accepted_lens[b]] (None: the first
+    accepted_lens[b] reserved ones) behind every sequence."""
+    a = _Args("fp4_kv_compact")
+    c, p = _kv_cache(a, cache), _kv_pages(a, pages)
+    a("accepted", accepted, _I32, optional=True)
+    if accepted is not None and (accepted.dim() != 2 or accepted.shape[0] != p.batch):
+        raise ValueError(f"{a.fn}: accepted has shape {tuple(accepted.shape)}, expected [{p.batch}, max_accepted]")
+    _per_seq(a, "accepted_lens", accepted_lens, p.batch)
+    if accepted is not None and accepted.shape[1] == 0:
+        return                                                        # nothing can be accepted
+    a.call(stream, _c.byref(c), _c.byref(p), _ptr(accepted), 0 if accepted is None else accepted.shape[1],
+           _ptr(accepted_lens))
+
+
+def fp4_kv_copy_pages(src: KvCache, dst: KvCache, src_pages, dst_pages, stream=None):
+    """Page src_pages[i] of src to page dst_pages[i] of dst (int32 [n] each)."""
+    a = _Args("fp4_kv_copy_pages")
+    s, d = _kv_cache(a, src, "src"), _kv_cache(a, dst, "dst")
+    a("src_pages", src_pages, _I32)
+    if src_pages.dim() != 1:
+        raise ValueError(f"{a.fn}: src_pages has shape {tuple(src_pages.shape)}, expected [n]")
+    _per_seq(a, "dst_pages", dst_pages, src_pages.shape[0])
+    a.call(stream, _c.byref(s), _c.byref(d), _ptr(src_pages), _ptr(dst_pages), src_pages.shape[0])

@@ -3,6 +3,7 @@
 // nothing; the library holds no state besides the per-thread error message.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -63,6 +64,72 @@ int check_scale_max_ws(const void* ws, size_t bytes, int64_t rows, int64_t k) {
     }
     const size_t need = fp4::scale_max_workspace_bytes(rows, k);
     FP4_REQUIRE(bytes >= need, FP4_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, bytes);
+    return FP4_OK;
+}
+
+// Whether two arrays of `rows` rows (row pitch and width in bytes) share a byte.
+// Rows of one pitch may interleave (columns of one fused array) without sharing any.
+bool rows_overlap(const void* a, int64_t pitch_a, int64_t width_a, const void* b, int64_t pitch_b, int64_t width_b,
+                  int64_t rows) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    const uintptr_t ea = pa + (uintptr_t)((rows - 1) * pitch_a + width_a);
+    const uintptr_t eb = pb + (uintptr_t)((rows - 1) * pitch_b + width_b);
+    if (pa >= eb || pb >= ea) return false;
+    if (rows == 1 || pitch_a != pitch_b) return true;
+    const uintptr_t pitch = (uintptr_t)pitch_a;
+    const uintptr_t off = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;   // of b in a's rows
+    return off < (uintptr_t)width_a || off + (uintptr_t)width_b > pitch;
+}
+
+constexpr int64_t kMaxList = (int64_t)1 << 20;    // sequences of a batch, entries of a list of ids
+
+int check_page_size(int64_t page_size) {
+    FP4_REQUIRE(page_size > 0, FP4_ERR_INVALID, "page_size=%lld", (long long)page_size);
+    FP4_REQUIRE(page_size % 16 == 0, FP4_ERR_SHAPE, "page_size=%lld is not a multiple of 16", (long long)page_size);
+    return FP4_OK;
+}
+
+// A cache's sizes and arrays; an empty cache needs no arrays.
+int check_cache(const fp4_kv_cache* cache, bool values_needed) {
+    FP4_REQUIRE(cache != nullptr, FP4_ERR_INVALID, "cache is NULL");
+    FP4_REQUIRE(cache->num_pages >= 0 && cache->d >= 0, FP4_ERR_INVALID, "negative size num_pages=%lld d=%lld",
+                (long long)cache->num_pages, (long long)cache->d);
+    if (int e = check_page_size(cache->page_size)) return e;
+    FP4_REQUIRE(cache->d % 32 == 0, FP4_ERR_SHAPE, "d=%lld is not a multiple of 32", (long long)cache->d);
+    FP4_REQUIRE(cache->d < (int64_t)1 << 31 && cache->num_pages < ((int64_t)1 << 31) / cache->page_size, FP4_ERR_SHAPE,
+                "the cache is too large: num_pages=%lld of %lld rows, d=%lld (rows and d must be below 2^31)",
+                (long long)cache->num_pages, (long long)cache->page_size, (long long)cache->d);
+    if (cache->num_pages == 0 || cache->d == 0) return FP4_OK;
+    FP4_PTR(cache->k_codes);
+    FP4_PTR(cache->k_scales);
+    FP4_REQUIRE((cache->v_codes == nullptr) == (cache->v_scales == nullptr), FP4_ERR_INVALID,
+                "v_codes and v_scales must both be given or both be NULL");
+    if (values_needed || cache->v_codes) {
+        FP4_PTR(cache->v_codes);
+        FP4_PTR(cache->v_scales);
+    }
+    return FP4_OK;
+}
+
+int check_pages(const fp4_kv_pages* pages) {
+    FP4_REQUIRE(pages != nullptr, FP4_ERR_INVALID, "pages is NULL");
+    FP4_REQUIRE(pages->batch >= 0 && pages->max_pages >= 0 && pages->num_pages >= 0, FP4_ERR_INVALID,
+                "negative size batch=%lld max_pages=%lld num_pages=%lld", (long long)pages->batch,
+                (long long)pages->max_pages, (long long)pages->num_pages);
+    FP4_REQUIRE(pages->batch < kMaxList, FP4_ERR_SHAPE, "batch=%lld too large", (long long)pages->batch);
+    FP4_REQUIRE(pages->max_pages < (int64_t)1 << 31 && pages->num_pages < (int64_t)1 << 31, FP4_ERR_SHAPE,
+                "max_pages=%lld num_pages=%lld too large", (long long)pages->max_pages, (long long)pages->num_pages);
+    if (pages->batch == 0) return FP4_OK;
+    if (pages->max_pages) { FP4_SCALAR_PTR(pages->page_table); }
+    FP4_SCALAR_PTR(pages->page_counts);
+    FP4_SCALAR_PTR(pages->seq_lens);
+    if (pages->num_pages) { FP4_SCALAR_PTR(pages->page_refs); }
+    return FP4_OK;
+}
+
+int check_same_pool(const fp4_kv_cache* cache, const fp4_kv_pages* pages) {
+    FP4_REQUIRE(cache->num_pages == pages->num_pages, FP4_ERR_INVALID, "the cache has %lld pages, page_refs %lld",
+                (long long)cache->num_pages, (long long)pages->num_pages);
     return FP4_OK;
 }
 
@@ -431,6 +498,165 @@ int fp4_moe_grouped_gemm(fp4_format fmt, const void* x_bf16, int64_t tokens, int
                     "h_codes_in and h_scales_in must be given together");
     }
     return hip_status(fp4::launch_moe(a, static_cast<hipStream_t>(stream)), "fp4_moe_grouped_gemm launch");
+}
+
+int fp4_qk_norm_rope(const void* q, const void* k, int64_t tokens, int q_heads, int kv_heads, int head_dim,
+                     int64_t ld_q, int64_t ld_k, const void* q_weight, const void* k_weight, fp4_dtype weight_dtype,
+                     float eps, const float* cos_sin, int64_t max_positions, int rot_dim, int interleaved,
+                     const int32_t* positions, void* q_out, int64_t ld_qo, void* k_out, int64_t ld_ko, void* stream) {
+    FP4_REQUIRE(tokens >= 0 && q_heads >= 0 && kv_heads >= 0, FP4_ERR_INVALID,
+                "negative size tokens=%lld q_heads=%d kv_heads=%d", (long long)tokens, q_heads, kv_heads);
+    FP4_REQUIRE(weight_dtype == FP4_DT_BF16 || weight_dtype == FP4_DT_F32, FP4_ERR_INVALID, "bad dtype %d",
+                (int)weight_dtype);
+    FP4_REQUIRE(eps >= 0.0f && std::isfinite(eps), FP4_ERR_INVALID, "eps=%g is negative or not finite", (double)eps);
+    FP4_REQUIRE(head_dim >= 16 && head_dim <= 256 && head_dim % 16 == 0, FP4_ERR_SHAPE,
+                "head_dim=%d is not a multiple of 16 in [16, 256]", head_dim);
+    FP4_REQUIRE(rot_dim >= 0 && rot_dim <= head_dim && rot_dim % 16 == 0, FP4_ERR_SHAPE,
+                "rot_dim=%d is not a multiple of 16 in [0, head_dim=%d]", rot_dim, head_dim);
+    FP4_REQUIRE(tokens < (int64_t)1 << 24, FP4_ERR_SHAPE, "tokens=%lld too large", (long long)tokens);
+    FP4_REQUIRE(q_heads <= 65536 && kv_heads <= 65536, FP4_ERR_SHAPE, "q_heads=%d kv_heads=%d too large", q_heads,
+                kv_heads);
+    if (tokens == 0 || q_heads + kv_heads == 0) return ok();
+    const int64_t wq = (int64_t)q_heads * head_dim, wk = (int64_t)kv_heads * head_dim;
+    if (q_heads) {
+        FP4_PTR(q);
+        FP4_PTR(q_out);
+        if (int e = check_ld(ld_q, wq, "ld_q")) return e;
+        if (int e = check_ld(ld_qo, wq, "ld_qo")) return e;
+    }
+    if (kv_heads) {
+        FP4_PTR(k);
+        FP4_PTR(k_out);
+        if (int e = check_ld(ld_k, wk, "ld_k")) return e;
+        if (int e = check_ld(ld_ko, wk, "ld_ko")) return e;
+    }
+    FP4_REQUIRE(aligned16(q_weight), FP4_ERR_ALIGN, "q_weight is not 16-byte aligned");
+    FP4_REQUIRE(aligned16(k_weight), FP4_ERR_ALIGN, "k_weight is not 16-byte aligned");
+    if (rot_dim) {
+        FP4_PTR(cos_sin);
+        FP4_SCALAR_PTR(positions);
+        FP4_REQUIRE(max_positions >= 0, FP4_ERR_INVALID, "negative max_positions=%lld", (long long)max_positions);
+    }
+    if (q_heads) {
+        FP4_REQUIRE((q_out == q && ld_qo == ld_q) || !rows_overlap(q_out, ld_qo * 2, wq * 2, q, ld_q * 2, wq * 2, tokens),
+                    FP4_ERR_INVALID, "q_out overlaps q without being q itself");
+    }
+    if (kv_heads) {
+        FP4_REQUIRE((k_out == k && ld_ko == ld_k) || !rows_overlap(k_out, ld_ko * 2, wk * 2, k, ld_k * 2, wk * 2, tokens),
+                    FP4_ERR_INVALID, "k_out overlaps k without being k itself");
+    }
+    if (q_heads && kv_heads) {
+        FP4_REQUIRE(!rows_overlap(q_out, ld_qo * 2, wq * 2, k, ld_k * 2, wk * 2, tokens), FP4_ERR_INVALID,
+                    "q_out overlaps k");
+        FP4_REQUIRE(!rows_overlap(k_out, ld_ko * 2, wk * 2, q, ld_q * 2, wq * 2, tokens), FP4_ERR_INVALID,
+                    "k_out overlaps q");
+        FP4_REQUIRE(!rows_overlap(q_out, ld_qo * 2, wq * 2, k_out, ld_ko * 2, wk * 2, tokens), FP4_ERR_INVALID,
+                    "q_out overlaps k_out");
+    }
+    fp4::QkNorm p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.tokens = tokens;
+    p.q_heads = q_heads;
+    p.kv_heads = kv_heads;
+    p.head_dim = head_dim;
+    p.ld_q = ld_q;
+    p.ld_k = ld_k;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.w_f32 = weight_dtype == FP4_DT_F32;
+    p.eps = eps;
+    p.cos_sin = cos_sin;
+    p.max_positions = max_positions;
+    p.rot_dim = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.positions = positions;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.ld_qo = ld_qo;
+    p.k_out = static_cast<uint16_t*>(k_out);
+    p.ld_ko = ld_ko;
+    return hip_status(fp4::launch_qk_norm_rope(p, static_cast<hipStream_t>(stream)), "fp4_qk_norm_rope launch");
+}
+
+size_t fp4_kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages) {
+    return batch > 0 && num_pages >= 0 ? fp4::kv_reserve_workspace_bytes(batch, num_pages) : 0;
+}
+
+int fp4_kv_reserve(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* new_tokens, int32_t* slots,
+                   int64_t max_new, int32_t* n_short, void* workspace, size_t workspace_bytes, void* stream) {
+    if (int e = check_cache(cache, false)) return e;
+    if (int e = check_pages(pages)) return e;
+    if (int e = check_same_pool(cache, pages)) return e;
+    FP4_REQUIRE(max_new >= 0, FP4_ERR_INVALID, "negative max_new=%lld", (long long)max_new);
+    if (pages->batch == 0) return ok();
+    FP4_SCALAR_PTR(new_tokens);
+    FP4_SCALAR_PTR(n_short);
+    if (max_new) { FP4_SCALAR_PTR(slots); }
+    const size_t need = fp4::kv_reserve_workspace_bytes(pages->batch, pages->num_pages);
+    FP4_REQUIRE(workspace != nullptr && workspace_bytes >= need, FP4_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu",
+                need, workspace ? workspace_bytes : (size_t)0);
+    FP4_REQUIRE(aligned16(workspace), FP4_ERR_ALIGN, "workspace is not 16-byte aligned");
+    return hip_status(fp4::launch_kv_reserve(*cache, *pages, new_tokens, slots, max_new, n_short, workspace,
+                                             static_cast<hipStream_t>(stream)),
+                      "fp4_kv_reserve launch");
+}
+
+int fp4_kv_fork(const fp4_kv_pages* pages, const int32_t* pairs, int64_t n, int64_t page_size, void* stream) {
+    if (int e = check_pages(pages)) return e;
+    if (int e = check_page_size(page_size)) return e;
+    FP4_REQUIRE(n >= 0, FP4_ERR_INVALID, "negative n=%lld", (long long)n);
+    FP4_REQUIRE(n < kMaxList, FP4_ERR_SHAPE, "n=%lld too large", (long long)n);
+    if (n == 0 || pages->batch == 0) return ok();
+    FP4_SCALAR_PTR(pairs);
+    return hip_status(fp4::launch_kv_fork(*pages, pairs, n, page_size, static_cast<hipStream_t>(stream)),
+                      "fp4_kv_fork launch");
+}
+
+int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const int32_t* keep_lens, int64_t page_size,
+                void* stream) {
+    if (int e = check_pages(pages)) return e;
+    if (int e = check_page_size(page_size)) return e;
+    FP4_REQUIRE(n >= 0, FP4_ERR_INVALID, "negative n=%lld", (long long)n);
+    FP4_REQUIRE(n < kMaxList, FP4_ERR_SHAPE, "n=%lld too large", (long long)n);
+    if (n == 0 || pages->batch == 0) return ok();
+    FP4_SCALAR_PTR(seqs);
+    if (keep_lens) { FP4_SCALAR_PTR(keep_lens); }
+    return hip_status(fp4::launch_kv_free(*pages, seqs, n, keep_lens, page_size, static_cast<hipStream_t>(stream)),
+                      "fp4_kv_free launch");
+}
+
+int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted, int64_t max_accepted,
+                   const int32_t* accepted_lens, void* stream) {
+    if (int e = check_cache(cache, false)) return e;
+    if (int e = check_pages(pages)) return e;
+    if (int e = check_same_pool(cache, pages)) return e;
+    FP4_REQUIRE(!accepted || (max_accepted >= 0 && max_accepted <= 64), FP4_ERR_INVALID,
+                "max_accepted=%lld outside [0, 64]", (long long)max_accepted);
+    if (pages->batch == 0 || cache->num_pages == 0 || cache->d == 0) return ok();
+    if (accepted) { FP4_SCALAR_PTR(accepted); }
+    FP4_SCALAR_PTR(accepted_lens);
+    return hip_status(fp4::launch_kv_compact(*cache, *pages, accepted, max_accepted, accepted_lens,
+                                             static_cast<hipStream_t>(stream)),
+                      "fp4_kv_compact launch");
+}
+
+int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const int32_t* src_pages,
+                      const int32_t* dst_pages, int64_t n, void* stream) {
+    if (int e = check_cache(src, false)) return e;
+    if (int e = check_cache(dst, false)) return e;
+    FP4_REQUIRE(src->d == dst->d && src->page_size == dst->page_size, FP4_ERR_INVALID,
+                "src has d=%lld page_size=%lld, dst d=%lld page_size=%lld", (long long)src->d, (long long)src->page_size,
+                (long long)dst->d, (long long)dst->page_size);
+    FP4_REQUIRE(n >= 0, FP4_ERR_INVALID, "negative n=%lld", (long long)n);
+    if (n == 0 || src->num_pages == 0 || dst->num_pages == 0 || src->d == 0) return ok();
+    FP4_REQUIRE((src->v_codes == nullptr) == (dst->v_codes == nullptr), FP4_ERR_INVALID,
+                "one of src and dst has no values");
+    FP4_REQUIRE(n < ((int64_t)1 << 24) / fp4::kv_copy_blocks(*src), FP4_ERR_SHAPE, "n=%lld pages too large for one call",
+                (long long)n);
+    FP4_SCALAR_PTR(src_pages);
+    FP4_SCALAR_PTR(dst_pages);
+    return hip_status(fp4::launch_kv_copy_pages(*src, *dst, src_pages, dst_pages, n, static_cast<hipStream_t>(stream)),
+                      "fp4_kv_copy_pages launch");
 }
 
 }  // extern "C"

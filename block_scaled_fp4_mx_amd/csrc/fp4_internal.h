@@ -132,4 +132,36 @@ size_t moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int topk, in
                            int64_t inter);
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s);
 
+struct QkNorm {
+    const uint16_t *q, *k;
+    int64_t tokens;
+    int q_heads, kv_heads, head_dim;
+    int64_t ld_q, ld_k;
+    const void *q_weight, *k_weight;
+    int w_f32;
+    float eps;
+    const float* cos_sin;
+    int64_t max_positions;
+    int rot_dim;
+    bool interleaved;
+    const int32_t* positions;
+    uint16_t* q_out;
+    int64_t ld_qo;
+    uint16_t* k_out;
+    int64_t ld_ko;
+};
+hipError_t launch_qk_norm_rope(const QkNorm& p, hipStream_t s);
+
+size_t kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages);
+hipError_t launch_kv_reserve(const fp4_kv_cache& c, const fp4_kv_pages& t, const int32_t* new_tokens, int32_t* slots,
+                             int64_t max_new, int32_t* n_short, void* ws, hipStream_t s);
+hipError_t launch_kv_fork(const fp4_kv_pages& t, const int32_t* pairs, int64_t n, int64_t page_size, hipStream_t s);
+hipError_t launch_kv_free(const fp4_kv_pages& t, const int32_t* seqs, int64_t n, const int32_t* keep_lens,
+                          int64_t page_size, hipStream_t s);
+hipError_t launch_kv_compact(const fp4_kv_cache& c, const fp4_kv_pages& t, const int32_t* accepted,
+                             int64_t max_accepted, const int32_t* accepted_lens, hipStream_t s);
+int64_t kv_copy_blocks(const fp4_kv_cache& c);
+hipError_t launch_kv_copy_pages(const fp4_kv_cache& src, const fp4_kv_cache& dst, const int32_t* src_pages,
+                                const int32_t* dst_pages, int64_t n, hipStream_t s);
+
 }  // namespace fp4

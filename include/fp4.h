@@ -384,6 +384,147 @@ int fp4_moe_grouped_gemm(fp4_format fmt, const void* x_bf16, int64_t tokens, int
 size_t fp4_moe_workspace_bytes(fp4_format fmt, int64_t tokens, int64_t hidden, int topk,
                                int num_experts, int64_t inter);
 
+/*
+ * Attention beside the MXFP4 cache.  The entry points below take a prompt or a
+ * step of (drafted) tokens from its projections to its attention: head norms
+ * and rotation, attention over the prompt itself, the pages of the cache that
+ * fp4_kv_append_mx fills, and attention of drafted tokens over that cache
+ * ("DeepSeek-V4 FP4 QAT" article, section 3.3: the KV cache is kept in MXFP4
+ * and dequantized where attention reads it).
+ *
+ * Head layout: a token's heads lie one after another, head h of token t at
+ * t * ld + h * head_dim elements, so q, k and v may be columns of one fused
+ * projection.  Grouped heads: query head h attends with key/value head
+ * h / (q_heads / kv_heads); q_heads is a multiple of kv_heads.
+ */
+
+/*
+ * Root-mean-square norm of every query and key head and the rotation by the
+ * token's position, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (over head_dim, fp32)
+ *   the first rot_dim values in pairs (a, b), pair i turned by the position's
+ *   angle i: (a cos - b sin, b cos + a sin); pairs are (i, i + rot_dim/2), or
+ *   (2i, 2i + 1) with interleaved != 0; the rest unturned; one rounding to bf16.
+ * cos_sin: fp32 [max_positions, rot_dim], cos of the rot_dim/2 angles, then sin
+ * (a table keeps far positions exact); positions: int32 [tokens].  A token whose
+ * position lies outside [0, max_positions) is padding: its output rows are left
+ * as they were.  rot_dim 0: norms only, cos_sin and positions ignored (may be NULL).
+ * q_weight, k_weight: [head_dim] of weight_dtype, NULL = ones.
+ * q [tokens, ld_q], k [tokens, ld_k], q_out [tokens, ld_qo], k_out [tokens,
+ * ld_ko]: bf16.  Either output may be its own input (same pointer and leading
+ * dimension); any other overlap of an output with an input or the other output
+ * is FP4_ERR_INVALID.  q_heads or kv_heads may be 0 (pointers then ignored).
+ * Errors: head_dim not a multiple of 16 in [16, 256], rot_dim not a multiple of
+ * 16 in [0, head_dim], 2^24 tokens or more -> FP4_ERR_SHAPE; eps negative or not finite -> FP4_ERR_INVALID.
+ */
+int fp4_qk_norm_rope(const void* q, const void* k, int64_t tokens, int q_heads, int kv_heads, int head_dim,
+                     int64_t ld_q, int64_t ld_k, const void* q_weight, const void* k_weight,
+                     fp4_dtype weight_dtype, float eps, const float* cos_sin, int64_t max_positions, int rot_dim,
+                     int interleaved, const int32_t* positions, void* q_out, int64_t ld_qo, void* k_out,
+                     int64_t ld_ko, void* stream);
+
+/*
+ * A paged MXFP4 cache of keys and values in fp4_kv_append_mx's layout: row
+ * page * page_size + i is token i of a page, d = kv_heads * head_dim values to
+ * a row: codes [num_pages * page_size, d/2], scales [.., d/32].  v_codes and
+ * v_scales may both be NULL (a keys-only cache) where no attention reads it.
+ * page_size is a multiple of 16 (so every page starts 16-byte aligned), d of 32,
+ * and num_pages * page_size is below 2^31 (rows are int32 slots).
+ */
+typedef struct fp4_kv_cache {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    int64_t num_pages;
+    int64_t d;
+    int64_t page_size;
+} fp4_kv_cache;
+
+/*
+ * Which pages the sequences of a batch hold (all device memory):
+ *   page_table  int32 [batch, max_pages]  page of tokens i*page_size.., -1 = none
+ *   page_counts int32 [batch]             entries of the row in use
+ *   seq_lens    int32 [batch]             tokens committed to the cache
+ *   page_refs   int32 [num_pages]         holders of each page; 0 = free
+ * Pages may be shared between sequences (after fp4_kv_fork) up to a sequence's
+ * committed length; a sequence writes only rows that fp4_kv_reserve gave it.
+ * Page ids outside [0, num_pages), counts outside [0, max_pages] and sequence
+ * ids outside [0, batch) are never followed.  Calls on one state are ordered by
+ * the caller (one stream).  batch and the lists of ids are shorter than 2^20.
+ */
+typedef struct fp4_kv_pages {
+    int32_t* page_table;
+    int32_t* page_counts;
+    int32_t* seq_lens;
+    int32_t* page_refs;
+    int64_t batch;
+    int64_t max_pages;
+    int64_t num_pages;
+} fp4_kv_pages;
+
+/*
+ * Makes room for new_tokens[b] (int32 [batch], negative = 0) more tokens behind
+ * the committed ones of every sequence: pages are taken free ones first by
+ * index, for the sequences in order, so the result does not depend on timing.
+ * A partly filled last page that other sequences hold too is copied first (its
+ * committed rows) and the copy takes its place: copy on write.
+ *   slots: int32 [batch, max_new], the cache row of new token j of sequence b
+ *   (position seq_lens[b] + j) for j < new_tokens[b], else -1: the slots of
+ *   fp4_kv_append_mx.  May be NULL with max_new 0.
+ *   *n_short: int32, 0, or how many pages the pool or the table rows lack; then
+ *   nothing is reserved for any sequence and every slot is -1.
+ * workspace: fp4_kv_reserve_workspace_bytes(batch, num_pages) bytes.
+ */
+int fp4_kv_reserve(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* new_tokens, int32_t* slots,
+                   int64_t max_new, int32_t* n_short, void* workspace, size_t workspace_bytes, void* stream);
+size_t fp4_kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages);
+
+/*
+ * Forks sequences: for each pair (source, target) of pairs (int32 [n, 2]) the
+ * target holds the source's committed tokens, sharing their pages; no row is
+ * copied until one of the holders writes (fp4_kv_reserve).  A pair is skipped
+ * when an id is outside [0, batch), the target still holds pages, an earlier
+ * pair names the same target, or the source is a target of this call.
+ */
+int fp4_kv_fork(const fp4_kv_pages* pages, const int32_t* pairs, int64_t n, int64_t page_size, void* stream);
+
+/*
+ * Cuts each listed sequence (int32 [n]) back to its first min(keep_lens[i],
+ * seq_lens) tokens (keep_lens int32 [n]; NULL = 0: the whole sequence) and lets
+ * go of every page behind them, reserved ones included.  A page that nobody
+ * holds any more is free.  Ids outside [0, batch) are skipped; of an id listed
+ * twice the first entry counts.
+ */
+int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const int32_t* keep_lens,
+                int64_t page_size, void* stream);
+
+/*
+ * Commits drafted tokens: for every sequence b the rows of its drafted tokens
+ * accepted[b, 0 .. accepted_lens[b]) (indices behind the committed length, in
+ * any order; reads come before writes, so rows may cross) move to the positions
+ * seq_lens[b], seq_lens[b] + 1, ..., and seq_lens[b] grows by that many.
+ * accepted: int32 [batch, max_accepted], max_accepted <= 64; accepted_lens:
+ * int32 [batch], taken as within [0, max_accepted].  accepted NULL: the first
+ * accepted_lens[b] reserved tokens are committed where they are (max_accepted
+ * ignored; the end of a prompt's append).  Rows move between pages that the
+ * sequence holds, onto pages that nobody else holds (fp4_kv_reserve saw to
+ * that), and the length never passes its pages; an accepted index that points
+ * elsewhere moves nothing.
+ */
+int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
+                   int64_t max_accepted, const int32_t* accepted_lens, void* stream);
+
+/*
+ * Copies whole pages: for i in [0, n), page src_pages[i] of src to page
+ * dst_pages[i] of dst (the same d and page_size; both with values or both
+ * without).  Pairs with an id outside its cache are skipped.  The in-range
+ * destinations must be distinct, and within one cache no page may be source and
+ * destination of the same call.
+ */
+int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const int32_t* src_pages,
+                      const int32_t* dst_pages, int64_t n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,161 @@
+"""Host-side refusals of the attention path's entry points: the documented
+status before any HIP call, and the binding's checks (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+import block_scaled_fp4_mx_amd as F
+
+OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, HIPERR = 0, -1, -2, -3, -4, -5, -6
+FAKE = 1 << 20          # 16-byte aligned, never dereferenced by rejected calls
+FAR = 1 << 40
+
+
+def _norm(q=FAKE, k=2 * FAKE, tokens=4, hq=4, hk=2, d=64, ld_q=256, ld_k=128, qw=None, kw=None, dt=0, eps=1e-6, table=FAKE,
+          places=100, rot=64, pos=FAKE, qo=3 * FAKE, ld_qo=256, ko=4 * FAKE, ld_ko=128):
+    return F.lib.fp4_qk_norm_rope(q, k, tokens, hq, hk, d, ld_q, ld_k, qw, kw, dt, eps, table, places, rot, 0, pos, qo,
+                                  ld_qo, ko, ld_ko, None)
+
+
+def test_norm_rope_rejections():
+    assert _norm(tokens=-1) == INVALID
+    assert _norm(d=24) == SHAPE and _norm(d=272) == SHAPE and _norm(d=0) == SHAPE
+    assert _norm(rot=80) == SHAPE and _norm(rot=24) == SHAPE and _norm(rot=-16) == SHAPE
+    assert _norm(dt=2) == INVALID
+    assert _norm(eps=-1.0) == INVALID and _norm(eps=float("nan")) == INVALID and _norm(eps=float("inf")) == INVALID
+    assert _norm(ld_q=248) == INVALID and _norm(ld_q=260) == ALIGN and _norm(ld_ko=120) == INVALID
+    assert _norm(q=None) == INVALID and _norm(ko=None) == INVALID and _norm(q=FAKE + 8) == ALIGN
+    assert _norm(qw=FAKE + 8) == ALIGN and _norm(table=None) == INVALID and _norm(pos=None) == INVALID
+    assert _norm(pos=FAKE + 2) == ALIGN and _norm(places=-1) == INVALID
+    assert _norm(tokens=1 << 24) == SHAPE
+    # overlaps: shifted in place, an output over the other input or output
+    assert _norm(qo=FAKE + 16) == INVALID and b"overlaps" in F.lib.fp4_last_error()
+    assert _norm(qo=FAKE, ld_qo=264) == INVALID
+    assert _norm(qo=2 * FAKE) == INVALID and _norm(ko=FAKE) == INVALID and _norm(ko=3 * FAKE) == INVALID
+    assert _norm(tokens=0, q=None, k=None, qo=None, ko=None) == OK
+    assert _norm(hq=0, hk=0, q=None, k=None, qo=None, ko=None) == OK
+
+
+def _cache(**kw):
+    v = dict(k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, num_pages=10, d=64, page_size=16) | kw
+    return ctypes.byref(F._KvCacheC(*(v[n] for n, _ in F._KvCacheC._fields_)))
+
+
+def _pages(**kw):
+    v = dict(page_table=FAKE, page_counts=FAKE, seq_lens=FAKE, page_refs=FAKE, batch=3, max_pages=4, num_pages=10) | kw
+    return ctypes.byref(F._KvPagesC(*(v[n] for n, _ in F._KvPagesC._fields_)))
+
+
+BAD_CACHES = [(dict(d=48), SHAPE), (dict(page_size=24), SHAPE), (dict(page_size=0), INVALID), (dict(num_pages=-1), INVALID),
+              (dict(k_codes=None), INVALID), (dict(k_scales=FAKE + 4), ALIGN), (dict(v_codes=None), INVALID),
+              (dict(v_scales=FAKE + 8), ALIGN), (dict(num_pages=1 << 28, page_size=16), SHAPE)]
+BAD_PAGES = [(dict(batch=-1), INVALID), (dict(page_table=None), INVALID), (dict(page_counts=FAKE + 2), ALIGN),
+             (dict(seq_lens=None), INVALID), (dict(page_refs=None), INVALID), (dict(batch=1 << 20), SHAPE),
+             (dict(num_pages=1 << 31), SHAPE), (dict(max_pages=-2), INVALID)]
+
+
+def test_page_operations_reject_bad_states():
+    lib, need = F.lib, F.lib.fp4_kv_reserve_workspace_bytes(3, 10)
+    for kw, status in BAD_CACHES:
+        assert lib.fp4_kv_reserve(_cache(**kw), _pages(), FAKE, FAKE, 4, FAKE, FAKE, need, None) == status, kw
+        assert lib.fp4_kv_compact(_cache(**kw), _pages(), FAKE, 4, FAKE, None) == status, kw
+        assert lib.fp4_kv_copy_pages(_cache(**kw), _cache(), FAKE, FAKE, 2, None) == status, kw
+        assert lib.fp4_kv_copy_pages(_cache(), _cache(**kw), FAKE, FAKE, 2, None) == status, kw
+    for kw, status in BAD_PAGES:
+        assert lib.fp4_kv_reserve(_cache(), _pages(**kw), FAKE, FAKE, 4, FAKE, FAKE, need, None) == status, kw
+        assert lib.fp4_kv_fork(_pages(**kw), FAKE, 2, 16, None) == status, kw
+        assert lib.fp4_kv_free(_pages(**kw), FAKE, 2, None, 16, None) == status, kw
+        assert lib.fp4_kv_compact(_cache(), _pages(**kw), FAKE, 4, FAKE, None) == status, kw
+
+
+def test_page_operations_reject_bad_arguments():
+    lib, need = F.lib, F.lib.fp4_kv_reserve_workspace_bytes(3, 10)
+    assert need == 16 + 3 * 16 + 10 * 4 and lib.fp4_kv_reserve_workspace_bytes(0, 10) == 0
+
+    def reserve(new=FAKE, slots=FAKE, max_new=4, short=FAKE, ws=FAKE, n=need, pages=None):
+        return lib.fp4_kv_reserve(_cache(), pages or _pages(), new, slots, max_new, short, ws, n, None)
+
+    assert reserve(new=None) == INVALID and reserve(slots=None) == INVALID and reserve(short=None) == INVALID
+    assert reserve(max_new=-1) == INVALID and reserve(short=FAKE + 1) == ALIGN
+    assert reserve(ws=None) == WORKSPACE and reserve(n=need - 1) == WORKSPACE and reserve(ws=FAKE + 4) == ALIGN
+    assert reserve(pages=_pages(num_pages=9)) == INVALID
+    assert reserve(pages=_pages(batch=0)) == OK
+    assert lib.fp4_kv_fork(_pages(), None, 2, 16, None) == INVALID
+    assert lib.fp4_kv_fork(_pages(), FAKE, -1, 16, None) == INVALID
+    assert lib.fp4_kv_fork(_pages(), FAKE, 2, 20, None) == SHAPE
+    assert lib.fp4_kv_fork(_pages(), FAKE, 1 << 20, 16, None) == SHAPE
+    assert lib.fp4_kv_fork(_pages(), None, 0, 16, None) == OK
+    assert lib.fp4_kv_free(_pages(), None, 2, None, 16, None) == INVALID
+    assert lib.fp4_kv_free(_pages(), FAKE, 2, FAKE + 2, 16, None) == ALIGN
+    assert lib.fp4_kv_free(_pages(), FAKE, 2, None, 0, None) == INVALID
+    assert lib.fp4_kv_free(_pages(), FAKE, 1 << 20, None, 16, None) == SHAPE
+    assert lib.fp4_kv_compact(_cache(), _pages(), FAKE, 65, FAKE, None) == INVALID
+    assert lib.fp4_kv_compact(_cache(), _pages(), FAKE, 4, None, None) == INVALID
+    assert lib.fp4_kv_compact(_cache(), _pages(num_pages=11), FAKE, 4, FAKE, None) == INVALID
+    copy = lib.fp4_kv_copy_pages
+    assert copy(_cache(), _cache(d=96), FAKE, FAKE, 2, None) == INVALID
+    assert copy(_cache(), _cache(page_size=32), FAKE, FAKE, 2, None) == INVALID
+    assert copy(_cache(), _cache(v_codes=None, v_scales=None), FAKE, FAKE, 2, None) == INVALID
+    assert copy(_cache(), _cache(), FAKE, None, 2, None) == INVALID
+    assert copy(_cache(), _cache(), FAKE, FAKE, -1, None) == INVALID
+    assert copy(_cache(), _cache(), FAKE, FAKE, 1 << 24, None) == SHAPE
+    assert copy(_cache(), _cache(), None, None, 0, None) == OK
+
+
+def _u8(*s):
+    return torch.zeros(s, dtype=torch.uint8)
+
+
+def _int(*s):
+    return torch.zeros(s, dtype=torch.int32)
+
+
+def test_binding_checks_the_attention_path():
+    x = torch.zeros((4, 6, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="bfloat16"):
+        F.fp4_qk_norm_rope(x.float(), x, x, x)
+    with pytest.raises(ValueError, match="tokens, heads"):
+        F.fp4_qk_norm_rope(x[0], x, x, x)
+    with pytest.raises(ValueError, match="heads of q"):
+        F.fp4_qk_norm_rope(x[:, ::2], x, x, x)
+    with pytest.raises(ValueError, match="k has shape"):
+        F.fp4_qk_norm_rope(x, x[:3], x, x[:3])
+    with pytest.raises(ValueError, match="q_out and k_out"):
+        F.fp4_qk_norm_rope(x, x, x[:, :2], x)
+    with pytest.raises(ValueError, match="q_weight"):
+        F.fp4_qk_norm_rope(x, x, x, x, q_weight=torch.ones(32))
+    with pytest.raises(TypeError, match="k_weight"):
+        F.fp4_qk_norm_rope(x, x, x, x, q_weight=torch.ones(64), k_weight=torch.ones(64, dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="positions"):
+        F.fp4_qk_norm_rope(x, x, x, x, torch.zeros(4, dtype=torch.int64), torch.zeros((8, 64)))
+    with pytest.raises(TypeError, match="positions"):
+        F.fp4_qk_norm_rope(x, x, x, x, None, torch.zeros((8, 64)))
+    with pytest.raises(ValueError, match="GPU"):
+        F.fp4_qk_norm_rope(x, x, x, x)
+    cache = F.KvCache(_u8(160, 32), _u8(160, 2), _u8(160, 32), _u8(160, 2), 16)
+    pages = F.KvPages(_int(3, 4), _int(3), _int(3), _int(10))
+    with pytest.raises(ValueError, match="k_scales"):
+        F.fp4_kv_compact(cache._replace(k_scales=_u8(160, 3)), pages, _int(3, 4), _int(3))
+    with pytest.raises(ValueError, match="both"):
+        F.fp4_kv_compact(cache._replace(v_codes=None), pages, _int(3, 4), _int(3))
+    with pytest.raises(ValueError, match="keys"):
+        F.fp4_kv_compact(cache._replace(v_codes=_u8(144, 32)), pages, _int(3, 4), _int(3))
+    with pytest.raises(ValueError, match="num_pages"):
+        F.fp4_kv_compact(cache._replace(page_size=48), pages, _int(3, 4), _int(3))
+    with pytest.raises(ValueError, match="page_table"):
+        F.fp4_kv_fork(pages._replace(page_counts=_int(2)), _int(1, 2), 16)
+    with pytest.raises(ValueError, match="pairs"):
+        F.fp4_kv_fork(pages, _int(2), 16)
+    with pytest.raises(ValueError, match="keep_lens"):
+        F.fp4_kv_free(pages, _int(3), 16, keep_lens=_int(2))
+    with pytest.raises(ValueError, match="accepted"):
+        F.fp4_kv_compact(cache, pages, _int(2, 4), _int(3))
+    with pytest.raises(ValueError, match="slots"):
+        F.fp4_kv_reserve(cache, pages, _int(3), _int(2, 4), _int(1), _u8(200))
+    with pytest.raises(TypeError, match="workspace"):
+        F.fp4_kv_reserve(cache, pages, _int(3), _int(3, 4), _int(1), _int(200))
+    with pytest.raises(ValueError, match="dst_pages"):
+        F.fp4_kv_copy_pages(cache, cache, _int(2), _int(3))
+    with pytest.raises(ValueError, match="GPU"):
+        F.fp4_kv_copy_pages(cache, cache, _int(2), _int(2))
