@@ -21,7 +21,7 @@ __all__ = [
     "fp4_dequant", "fp4_gemm", "fp4_quantize_mxfp8", "fp4_mx_to_mxfp8", "fp4_mx_dequant_fp8", "fp4_gemm_w4a8", "fp4_fake_quant",
     "fp4_ste_backward", "fp4_kv_append_mx", "fp4_moe_grouped_gemm", "fp4_moe_workspace_bytes", "MoeDebug",
     "fp4_qk_norm_rope", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
-    "fp4_kv_free", "fp4_kv_compact", "fp4_kv_copy_pages",
+    "fp4_kv_free", "fp4_kv_compact", "fp4_kv_copy_pages", "fp4_attn_tree_mx", "fp4_attn_tree_workspace_bytes",
     "fp4_abi_version", "LIB_PATH",
 ]
 
@@ -85,6 +85,9 @@ _SIGS = {
     "fp4_kv_free": (_i32, [_pages_p, _vp, _i64, _vp, _i64, _vp]),
     "fp4_kv_compact": (_i32, [_cache_p, _pages_p, _vp, _i64, _vp, _vp]),
     "fp4_kv_copy_pages": (_i32, [_cache_p, _cache_p, _vp, _vp, _i64, _vp]),
+    "fp4_attn_tree_mx": (_i32, [_vp, _i64, _cache_p, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _c.c_float, _vp,
+                                _i64, _vp, _sz, _vp]),
+    "fp4_attn_tree_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
 }
 
 
@@ -123,7 +126,7 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_U8, _I32, _F32, _BF16 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
+_U8, _I32, _I64, _F32, _BF16 = (torch.uint8,), (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
 _OUT = (torch.bfloat16, torch.float32)
 
 
@@ -628,3 +631,49 @@ def fp4_kv_copy_pages(src: KvCache, dst: KvCache, src_pages, dst_pages, stream=N
         raise ValueError(f"{a.fn}: src_pages has shape {tuple(src_pages.shape)}, expected [n]")
     _per_seq(a, "dst_pages", dst_pages, src_pages.shape[0])
     a.call(stream, _c.byref(s), _c.byref(d), _ptr(src_pages), _ptr(dst_pages), src_pages.shape[0])
+
+
+def fp4_attn_tree_workspace_bytes(batch: int, drafts: int, q_heads: int, head_dim: int, kv_heads: int) -> int:
+    return lib.fp4_attn_tree_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads)
+
+
+def _drafted(a, name, t):
+    """A bf16 [batch, drafts, q_heads, head_dim] tensor, tokens any one pitch apart; returns the pitch."""
+    a(name, t, _BF16, dense=False)
+    if t.dim() != 4:
+        raise ValueError(f"{a.fn}: {name} must be [batch, drafts, q_heads, head_dim], got shape {tuple(t.shape)}")
+    batch, drafts, heads, d = t.shape
+    if t.numel() and heads > 1 and t.stride(2) != d:
+        raise ValueError(f"{a.fn}: the heads of {name} must be contiguous")
+    ld = t.stride(1) if drafts > 1 else t.stride(0) if batch > 1 else heads * d
+    if batch > 1 and t.numel() and t.stride(0) != drafts * ld:
+        raise ValueError(f"{a.fn}: the tokens of {name} must be one pitch apart")
+    return ld
+
+
+def fp4_attn_tree_mx(q, cache: KvCache, page_table, seq_lens, out, workspace, draft_lens=None, tree_mask=None, scale=None,
+                     stream=None):
+    """q, out [batch, drafts, q_heads, head_dim]; tree_mask int64 [batch, drafts]
+    (bit j: sees drafted token j; None: tokens up to itself); scale None: head_dim ** -0.5."""
+    a = _Args("fp4_attn_tree_mx")
+    ld_q, ld_out = _drafted(a, "q", q), _drafted(a, "out", out)
+    if out.shape != q.shape:
+        raise ValueError(f"{a.fn}: out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    batch, drafts, q_heads, head_dim = q.shape
+    c = _kv_cache(a, cache)
+    if cache.v_codes is None:
+        raise ValueError(f"{a.fn}: the cache has no values")
+    if c.d % head_dim or not c.d:
+        raise ValueError(f"{a.fn}: the cache's rows hold {c.d} values, not a multiple of head_dim {head_dim}")
+    a("page_table", page_table, _I32)
+    if page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError(f"{a.fn}: page_table has shape {tuple(page_table.shape)}, expected [{batch}, max_pages]")
+    _per_seq(a, "seq_lens", seq_lens, batch)
+    _per_seq(a, "draft_lens", draft_lens, batch, optional=True)
+    a("tree_mask", tree_mask, _I64, optional=True)
+    if tree_mask is not None and tuple(tree_mask.shape) != (batch, drafts):
+        raise ValueError(f"{a.fn}: tree_mask has shape {tuple(tree_mask.shape)}, expected {(batch, drafts)}")
+    a("workspace", workspace, _U8)
+    a.call(stream, _ptr(q), ld_q, _c.byref(c), _ptr(page_table), page_table.shape[1], _ptr(seq_lens), _ptr(draft_lens),
+           _ptr(tree_mask), batch, drafts, q_heads, c.d // head_dim, head_dim,
+           head_dim ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(workspace), workspace.numel())

@@ -18,7 +18,8 @@ OUT = os.path.join(HERE, "libfp4.so")
 BUILD = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "moe.hip", "qk_norm.hip", "kv_pages.hip"]
+SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "moe.hip", "qk_norm.hip", "kv_pages.hip",
+           "attn_tree.hip"]
 PROBES = os.path.join(HERE, "probes")
 PROBE_OUT = os.path.join(PROBES, "libfp4_peak.so")
 FLAGS = [

@@ -133,6 +133,17 @@ int check_same_pool(const fp4_kv_cache* cache, const fp4_kv_pages* pages) {
     return FP4_OK;
 }
 
+// Head counts and head_dim of the attention entry points.
+int check_heads(int q_heads, int kv_heads, int head_dim) {
+    FP4_REQUIRE(q_heads > 0 && kv_heads > 0, FP4_ERR_INVALID, "q_heads=%d and kv_heads=%d must be positive", q_heads,
+                kv_heads);
+    FP4_REQUIRE(q_heads % kv_heads == 0 && q_heads <= 4096, FP4_ERR_SHAPE,
+                "q_heads=%d is not a multiple of kv_heads=%d (or above 4096)", q_heads, kv_heads);
+    FP4_REQUIRE(head_dim == 64 || head_dim == 128 || head_dim == 256, FP4_ERR_SHAPE, "head_dim=%d is not 64, 128 or 256",
+                head_dim);
+    return FP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -657,6 +668,62 @@ int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const in
     FP4_SCALAR_PTR(dst_pages);
     return hip_status(fp4::launch_kv_copy_pages(*src, *dst, src_pages, dst_pages, n, static_cast<hipStream_t>(stream)),
                       "fp4_kv_copy_pages launch");
+}
+
+size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
+    if (batch <= 0 || drafts < 1 || drafts > 64 || check_heads(q_heads, kv_heads, head_dim) != FP4_OK) return 0;
+    return fp4::attn_tree_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads);
+}
+
+int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                     const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* tree_mask, int64_t batch,
+                     int drafts, int q_heads, int kv_heads, int head_dim, float scale, void* out, int64_t ld_out,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    if (int e = check_heads(q_heads, kv_heads, head_dim)) return e;
+    if (int e = check_cache(cache, true)) return e;
+    const int64_t width = (int64_t)q_heads * head_dim;
+    FP4_REQUIRE(cache->d == (int64_t)kv_heads * head_dim, FP4_ERR_SHAPE, "the cache has d=%lld, kv_heads * head_dim is %lld",
+                (long long)cache->d, (long long)kv_heads * head_dim);
+    FP4_REQUIRE(drafts >= 1 && drafts <= 64, FP4_ERR_INVALID, "drafts=%d outside [1, 64]", drafts);
+    FP4_REQUIRE(batch >= 0 && max_pages >= 0, FP4_ERR_INVALID, "negative size batch=%lld max_pages=%lld", (long long)batch,
+                (long long)max_pages);
+    FP4_REQUIRE(batch < 65536 && max_pages < (int64_t)1 << 31, FP4_ERR_SHAPE, "batch=%lld or max_pages=%lld too large",
+                (long long)batch, (long long)max_pages);
+    FP4_REQUIRE(std::isfinite(scale), FP4_ERR_INVALID, "scale is not finite");
+    if (batch == 0) return ok();
+    FP4_PTR(q);
+    FP4_PTR(out);
+    if (int e = check_ld(ld_q, width, "ld_q")) return e;
+    if (int e = check_ld(ld_out, width, "ld_out")) return e;
+    if (max_pages) { FP4_SCALAR_PTR(page_table); }
+    FP4_SCALAR_PTR(seq_lens);
+    FP4_REQUIRE((reinterpret_cast<uintptr_t>(draft_lens) & 3u) == 0, FP4_ERR_ALIGN, "draft_lens is not 4-byte aligned");
+    FP4_REQUIRE((reinterpret_cast<uintptr_t>(tree_mask) & 7u) == 0, FP4_ERR_ALIGN, "tree_mask is not 8-byte aligned");
+    FP4_REQUIRE(!rows_overlap(out, ld_out * 2, width * 2, q, ld_q * 2, width * 2, batch * drafts), FP4_ERR_INVALID,
+                "out overlaps q");
+    const size_t need = fp4::attn_tree_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads);
+    FP4_REQUIRE(workspace != nullptr && workspace_bytes >= need, FP4_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu",
+                need, workspace ? workspace_bytes : (size_t)0);
+    FP4_REQUIRE(aligned16(workspace), FP4_ERR_ALIGN, "workspace is not 16-byte aligned");
+    fp4::AttnTree p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.ld_q = ld_q;
+    p.cache = *cache;
+    p.page_table = page_table;
+    p.max_pages = max_pages;
+    p.seq_lens = seq_lens;
+    p.draft_lens = draft_lens;
+    p.tree_mask = tree_mask;
+    p.batch = batch;
+    p.drafts = drafts;
+    p.q_heads = q_heads;
+    p.kv_heads = kv_heads;
+    p.head_dim = head_dim;
+    p.scale = scale;
+    p.out = static_cast<uint16_t*>(out);
+    p.ld_out = ld_out;
+    p.ws = workspace;
+    return hip_status(fp4::launch_attn_tree(p, static_cast<hipStream_t>(stream)), "fp4_attn_tree_mx launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,574 @@
+// Attention of drafted tokens over the paged MXFP4 cache.
+//
+//   o = sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m),  s_j = q . k_j,
+//   c = scale * log2(e), over the visible tokens j, in one pass: m is a running
+//   reference near the row's maximum, and o and the sum are scaled when it moves.
+//
+// Bound by HBM: a token's keys and values are 2 * (d/2 + d/32) bytes for all
+// its heads and are read once for all query rows of a sequence.  A wave takes
+// one key/value head and up to 16 * NR of the query rows that share it (drafts
+// times q_heads / kv_heads), and walks its tokens 32 at a time without LDS or
+// barriers: every operand is loaded in the layout the matrix core takes.
+//
+//   S^T = K Q^T on v_mfma_f32_16x16x32_bf16: lane (c = lane % 16, g = lane / 16)
+//   loads the quarter g of token c's row, one load for all K steps (the order of
+//   a row's values among the steps is free as long as Q is loaded alike), and
+//   widens it with its block scales (exact in bf16).
+//   The result leaves lane (c, g) with query row c and tokens 4g .. 4g+3, which
+//   is what the B operand of O^T = V^T P^T takes if the token order within a
+//   step is (g, tile, i): the weights never leave their lane.
+//   V^T needs 8 tokens of one value per lane: a lane loads the same d/16 values
+//   of its 8 tokens (16 lanes cover the row), widens each with its token's
+//   scale, and pairs tokens with byte permutes.
+//   O^T leaves lane (c, g) with d/4 consecutive values of row c.
+//
+// The reference m moves only when some score exceeds it by more than 2^8 (one
+// ballot); until then no lane exchange is needed.  Weights are rounded to bf16
+// for the second product (they enter it with V's 16-bit format); their sum is
+// kept in fp32 from the unrounded weights.
+//
+// Work split: the batch's tiles of 32 tokens are laid end to end and cut into
+// equal ranges, one per workgroup column, whatever the lengths; a sequence that
+// a cut goes through leaves partial (m, sum, o) in the workspace, at most two
+// per range, and a second kernel joins them in order.
+#include "fp4_internal.h"
+#include "mma_core.h"
+
+namespace fp4 {
+namespace {
+
+constexpr int kTile = 32;                  // tokens per step
+constexpr int kWaves = 4;                  // at most, per workgroup
+constexpr int kMinTiles = 4;               // tiles per range below which fewer ranges are used
+constexpr int kWorkgroups = 512;           // two per CU: two waves per SIMD
+constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
+constexpr float kNone = -__builtin_inff();
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+struct TreeArgs {
+    const uint16_t* q;
+    int64_t ld_q;
+    const uint8_t *kc, *ks, *vc, *vs;
+    int64_t num_pages;
+    int page_size;
+    int code_row, scale_row;               // bytes of a cache row
+    const int32_t* table;
+    int64_t max_pages;
+    const int32_t *seq_lens, *draft_lens;
+    const uint64_t* mask;
+    int batch, drafts, group, kv_heads, rows;   // rows = drafts * group: query rows of a key/value head
+    float scale2;                          // scale * log2(e)
+    uint16_t* out;
+    int64_t ld_out;
+    float* part;                           // [2 * ranges][kv_heads][rows][D] sums, then [..][2] (m, sum)
+    int ranges;
+};
+
+__device__ __forceinline__ int drafts_of(const TreeArgs& a, int b) {
+    return a.draft_lens ? min(max(a.draft_lens[b], 0), a.drafts) : a.drafts;
+}
+
+// Tokens of sequence b that can be seen at all: its committed and drafted ones,
+// as far as the table's row goes (none in an empty pool).
+__device__ __forceinline__ int64_t tokens_of(const TreeArgs& a, int b) {
+    const int64_t n = (int64_t)max(a.seq_lens[b], 0) + drafts_of(a, b);
+    return a.num_pages ? min(n, a.max_pages * a.page_size) : 0;
+}
+
+// Tiles of sequence b; a sequence with drafted tokens has at least one, so that
+// its rows are written.
+__device__ __forceinline__ int64_t tiles_of(const TreeArgs& a, int b) {
+    if (b >= a.batch || drafts_of(a, b) == 0) return 0;
+    return max((tokens_of(a, b) + kTile - 1) / kTile, (int64_t)1);
+}
+
+// A value equal in all lanes, as a scalar (so that what follows from it is one too).
+__device__ __forceinline__ int64_t scalar(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m, 64);
+    return scalar(v);
+}
+
+// All tiles of the batch, and the ranges they are cut into.
+__device__ __forceinline__ int64_t all_tiles(const TreeArgs& a, int lane) {
+    int64_t n = 0;
+    for (int b = lane; b < a.batch; b += 64) n += tiles_of(a, b);
+    return wave_sum(n);
+}
+__device__ __forceinline__ int64_t used_ranges(const TreeArgs& a, int64_t tiles) {
+    return min((int64_t)a.ranges, max((tiles + kMinTiles - 1) / kMinTiles, (int64_t)1));
+}
+
+// Tiles of the sequences before b (all lanes must call).
+__device__ __forceinline__ int64_t tiles_before(const TreeArgs& a, int b, int lane) {
+    int64_t n = 0;
+    for (int i = lane; i < b; i += 64) n += tiles_of(a, i);
+    return wave_sum(n);
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const bf16x2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Byte kByte of w (two E2M1 codes) times 2^(scale byte - 127), exact, as two bf16.
+template <int kByte>
+__device__ __forceinline__ uint32_t widen(uint32_t w, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, kByte));
+}
+__device__ __forceinline__ u32x4 widen8(uint32_t w, float scale) {
+    return u32x4{widen<0>(w, scale), widen<1>(w, scale), widen<2>(w, scale), widen<3>(w, scale)};
+}
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+template <int D>
+struct Raw {                               // one tile's bytes of one lane
+    static constexpr int kK = D / 32;      // dwords of a quarter row
+    static constexpr int kKS = D == 256 ? 2 : 1;
+    uint32_t k[2][kK];
+    uint8_t ks[2][kKS];
+    uint32_t v[8][D == 256 ? 2 : 1];       // D == 64: 4 codes in the low half
+    uint8_t vs[8];
+};
+
+// A tile's place: the first cache row of its two halves (-1: no page).
+struct Place {
+    int64_t row[2];
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(Raw<D>& r, const TreeArgs& a, const Place& p, int head, int c, int g) {
+    const int kofs = c * a.code_row + head * (D / 2) + g * (D / 8);
+    const int ksofs = c * a.scale_row + head * (D / 32) + (D == 64 ? g / 2 : D == 128 ? g : 2 * g);
+    const int vofs = 4 * g * a.code_row + head * (D / 2) + c * (D / 32);
+    const int vsofs = 4 * g * a.scale_row + head * (D / 32) + c * (D / 16) / 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t row = p.row[h] < 0 ? 0 : p.row[h];      // any row of the pool: masked later
+        const uint8_t* kc = a.kc + row * a.code_row;
+        const uint8_t* ks = a.ks + row * a.scale_row;
+        const uint8_t* vc = a.vc + row * a.code_row;
+        const uint8_t* vs = a.vs + row * a.scale_row;
+        if constexpr (D == 64) {
+            const uint2 x = *reinterpret_cast<const uint2*>(kc + kofs);
+            r.k[h][0] = x.x, r.k[h][1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(kc + kofs + 16 * i);
+                r.k[h][4 * i] = x.x, r.k[h][4 * i + 1] = x.y, r.k[h][4 * i + 2] = x.z, r.k[h][4 * i + 3] = x.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < Raw<D>::kKS; ++i) r.ks[h][i] = ks[ksofs + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint8_t* x = vc + vofs + j * a.code_row;
+            if constexpr (D == 64) {
+                r.v[4 * h + j][0] = *reinterpret_cast<const uint16_t*>(x);
+            } else if constexpr (D == 128) {
+                r.v[4 * h + j][0] = *reinterpret_cast<const uint32_t*>(x);
+            } else {
+                const uint2 y = *reinterpret_cast<const uint2*>(x);
+                r.v[4 * h + j][0] = y.x, r.v[4 * h + j][1] = y.y;
+            }
+            r.vs[4 * h + j] = vs[vsofs + j * a.scale_row];
+        }
+    }
+}
+
+// Low (or high) halves of a and b: two tokens of one value.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_perm(b, a, kHigh ? 0x07060302u : 0x05040100u);
+}
+
+template <int D, int NR>
+__global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a) {
+    constexpr int kSteps = D / 32, kOut = D / 16;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int row_groups = (a.rows + 16 * NR - 1) / (16 * NR);
+    const int unit = __builtin_amdgcn_readfirstlane(blockIdx.y * (blockDim.x >> 6) + (threadIdx.x >> 6));
+    if (unit >= a.kv_heads * row_groups) return;
+    const int head = unit % a.kv_heads, r0 = unit / a.kv_heads * 16 * NR;
+
+    const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
+    if ((int64_t)blockIdx.x >= ranges || total == 0) return;
+    const int64_t lo = blockIdx.x * total / ranges, hi = (blockIdx.x + 1) * total / ranges;
+
+    // The sequence that holds tile lo, and the tiles before it.
+    int b = 0;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        int64_t n = tiles_of(a, b0 + lane);
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int64_t o = __shfl_up(n, m, 64);
+            if (lane >= m) n += o;
+        }
+        const int64_t chunk = scalar(__shfl(n, 63, 64));
+        if (before + chunk > lo) {
+            const int k = __popcll(__ballot(before + n <= lo));       // sequences of this chunk that end by lo
+            if (k) before += scalar(__shfl(n, k - 1, 64));
+            b = b0 + k;
+            break;
+        }
+        before += chunk;
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+
+    for (int64_t at = lo; at < hi; ++b) {
+        const int64_t tiles = tiles_of(a, b);
+        if (tiles == 0) continue;
+        const int64_t t0 = at - before, t1 = min(hi - before, tiles);
+        const int64_t len = max(a.seq_lens[b], 0), seen = tokens_of(a, b);
+        const int nd = drafts_of(a, b);
+        const int32_t* table = a.table + (int64_t)b * a.max_pages;
+
+        u32x4 q[NR][kSteps];
+        uint64_t vis[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int row = r0 + 16 * n + c, t = row / a.group;
+            const bool live = t < nd;
+            const uint16_t* x = a.q + ((int64_t)b * a.drafts + (live ? t : 0)) * a.ld_q +
+                                ((int64_t)head * a.group + row % a.group) * D + g * (D / 4);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                q[n][s] = live ? *reinterpret_cast<const u32x4*>(x + 8 * s) : u32x4{0, 0, 0, 0};
+            vis[n] = 0;
+            if (live) {
+                vis[n] = a.mask ? a.mask[(int64_t)b * a.drafts + t] : ~0ull >> (63 - t);
+                if (nd < 64) vis[n] &= (1ull << nd) - 1;
+            }
+        }
+
+        v4f o[NR][kOut];
+        float m[NR], sum[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            m[n] = kNone, sum[n] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) o[n][i] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+
+        // Page of the next 16 tokens to place.
+        int64_t page_i = t0 * kTile / a.page_size;
+        int off = (int)(t0 * kTile - page_i * a.page_size);
+        auto place = [&]() {
+            Place p;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t page = page_i < a.max_pages ? table[page_i] : -1;
+                p.row[h] = page >= 0 && page < a.num_pages ? (int64_t)page * a.page_size + off : -1;
+                off += 16;
+                if (off == a.page_size) off = 0, ++page_i;
+            }
+            return p;
+        };
+        Raw<D> cur, next;
+        Place here = place(), ahead = place();
+        if (seen > 0) load_tile<D>(cur, a, here, head, c, g);
+        for (int64_t t = t0; t < t1 && seen > 0; ++t) {
+            if (t + 1 < t1) load_tile<D>(next, a, ahead, head, c, g);
+            const Place later = place();
+
+            const int64_t pos0 = t * kTile;
+            const bool edge = pos0 + kTile > len || here.row[0] < 0 || here.row[1] < 0;     // uniform
+            v4f s[NR][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) s[n][h] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const float sc = scale_of(cur.ks[h][D == 256 ? i / 4 : 0]);
+                    const bf16x8 k = __builtin_bit_cast(bf16x8, widen8(cur.k[h][i], sc));
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, q[n][i]), s[n][h],
+                                                                          0, 0, 0);
+                }
+            }
+            // V: bytes of 8 tokens widened, then tokens paired per value.
+            u32x4 v[kOut];
+            {
+                constexpr int kBytes = D / 32;               // of a token's values in this lane
+                uint32_t w[8][kBytes];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t byte = cur.vs[j];
+                    if (edge) {
+                        const int64_t pos = pos0 + 16 * (j / 4) + 4 * g + j % 4;
+                        if (pos >= seen || here.row[j / 4] < 0) byte = 127;      // whatever lies there, finite
+                    }
+                    const float sc = scale_of(byte);
+                    w[j][0] = widen<0>(cur.v[j][0], sc);
+                    w[j][1] = widen<1>(cur.v[j][0], sc);
+                    if constexpr (D >= 128) {
+                        w[j][2] = widen<2>(cur.v[j][0], sc);
+                        w[j][3] = widen<3>(cur.v[j][0], sc);
+                    }
+                    if constexpr (D == 256) {
+                        w[j][4] = widen<0>(cur.v[j][1], sc);
+                        w[j][5] = widen<1>(cur.v[j][1], sc);
+                        w[j][6] = widen<2>(cur.v[j][1], sc);
+                        w[j][7] = widen<3>(cur.v[j][1], sc);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kOut; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[i][j] = i & 1 ? pair<true>(w[2 * j][i / 2], w[2 * j + 1][i / 2])
+                                        : pair<false>(w[2 * j][i / 2], w[2 * j + 1][i / 2]);
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = s[n][j / 4][j % 4] * a.scale2;
+                if (edge) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int64_t pos = pos0 + 16 * (j / 4) + 4 * g + j % 4, d = pos - len;
+                        const bool see = pos < seen && here.row[j / 4] >= 0 && (d < 0 || ((vis[n] >> (d & 63)) & 1));
+                        x[j] = see ? x[j] : kNone;
+                    }
+                }
+                float top = x[0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+                if (__any(top > m[n] + kSlack)) {
+                    top = fmaxf(top, __shfl_xor(top, 16, 64));
+                    top = fmaxf(top, __shfl_xor(top, 32, 64));
+                    const float up = fmaxf(m[n], top);
+                    const float alpha = up == m[n] ? 1.0f : exp2_hw(m[n] - up);
+                    m[n] = up;
+                    sum[n] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < kOut; ++i) o[n][i] *= alpha;
+                }
+                const float ref = m[n] == kNone ? 0.0f : m[n];
+                u32x4 p;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p0 = exp2_hw(x[2 * j] - ref), p1 = exp2_hw(x[2 * j + 1] - ref);
+                    sum[n] += p0 + p1;
+                    p[j] = pack2(p0, p1);
+                }
+                const bf16x8 pb = __builtin_bit_cast(bf16x8, p);
+#pragma unroll
+                for (int i = 0; i < kOut; ++i)
+                    o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v[i]), pb, o[n][i], 0, 0, 0);
+            }
+            cur = next;
+            here = ahead;
+            ahead = later;
+        }
+
+        const bool whole = t0 == 0 && t1 == tiles;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float l = sum[n];
+            l += __shfl_xor(l, 16, 64);
+            l += __shfl_xor(l, 32, 64);
+            const int row = r0 + 16 * n + c, t = row / a.group;
+            if (t >= nd) continue;
+            if (whole) {
+                const float inv = l > 0.f ? 1.0f / l : 0.f;
+                uint16_t* y = a.out + ((int64_t)b * a.drafts + t) * a.ld_out +
+                              ((int64_t)head * a.group + row % a.group) * D + g * (D / 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                 // D/16 consecutive values each
+                    uint32_t w[kOut / 2];
+#pragma unroll
+                    for (int j = 0; j < kOut / 2; ++j) w[j] = pack2(o[n][2 * j][i] * inv, o[n][2 * j + 1][i] * inv);
+#pragma unroll
+                    for (int j = 0; j < kOut / 2; j += 2)
+                        *reinterpret_cast<uint2*>(y + i * kOut + 2 * j) = make_uint2(w[j], w[j + 1]);
+                }
+            } else {
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (at == lo ? 0 : 1);
+                const int64_t at_row = (slot * a.kv_heads + head) * a.rows + row;
+                float* y = a.part + at_row * D + g * (D / 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < kOut; j += 4)
+                        *reinterpret_cast<float4*>(y + i * kOut + j) =
+                            make_float4(o[n][j][i], o[n][j + 1][i], o[n][j + 2][i], o[n][j + 3][i]);
+                if (g == 0) {
+                    float* ml = a.part + 2 * (int64_t)a.ranges * a.kv_heads * a.rows * D + at_row * 2;
+                    ml[0] = m[n], ml[1] = l;
+                }
+            }
+        }
+        at += t1 - t0;
+        before += tiles;
+    }
+}
+
+// Joins the partial results of the sequences that were cut: kRowWaves waves to
+// a row, pieces dealt to them in turn, their sums joined in wave order.
+// Workgroup (x, y): sequence y, rows from x * (4 / kRowWaves) (or one) on.
+template <int D, int kRowWaves>
+__global__ __launch_bounds__(64 * (kRowWaves < 4 ? 4 : kRowWaves)) void attn_tree_join_kernel(const TreeArgs a) {
+    constexpr int kAll = kRowWaves < 4 ? 4 : kRowWaves, kRows = kAll / kRowWaves, kV = D / 64;
+    __shared__ float sums[kAll][D + 2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % kRowWaves;
+    const int b = blockIdx.y, nd = drafts_of(a, b);
+    const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total), tiles = tiles_of(a, b);
+    if (tiles == 0) return;
+    const int64_t before = tiles_before(a, b, lane);
+    const int64_t first = ((before + 1) * ranges - 1) / total, last = ((before + tiles) * ranges - 1) / total;
+    if (first == last) return;                                // one piece: written already
+    const int64_t r = (int64_t)blockIdx.x * kRows + wave / kRowWaves;   // row among kv_heads * rows
+    const bool live = r < (int64_t)a.kv_heads * a.rows && (int)(r % a.rows) / a.group < nd;
+    const int64_t stride = (int64_t)a.kv_heads * a.rows;
+    const float* ml = a.part + 2 * a.ranges * stride * D;
+    float m = kNone, l = 0.f, acc[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+    if (live) {
+        // The first piece is its range's second one unless the range starts with it.
+        const int64_t first_slot = 2 * first + (first * total / ranges == before ? 0 : 1);
+        constexpr int kBatch = 8;
+        for (int64_t x0 = first + w; x0 <= last; x0 += kBatch * kRowWaves) {
+            float pm[kBatch], pl[kBatch], po[kBatch][kV];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t x = x0 + k * kRowWaves;
+                pm[k] = kNone, pl[k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < kV; ++i) po[k][i] = 0.f;
+                if (x <= last) {
+                    const int64_t at = (x == first ? first_slot : 2 * x) * stride + r;
+                    pm[k] = ml[at * 2], pl[k] = ml[at * 2 + 1];
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) po[k][i] = a.part[at * D + lane * kV + i];
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, pm[k]);
+            const float ref = top == kNone ? 0.f : top;
+            const float keep = exp2_hw(m - ref);
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) acc[i] *= keep;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float e = exp2_hw(pm[k] - ref);
+                l += pl[k] * e;
+#pragma unroll
+                for (int i = 0; i < kV; ++i) acc[i] += po[k][i] * e;
+            }
+        }
+    }
+    if constexpr (kRowWaves > 1) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) sums[wave][lane * kV + i] = acc[i];
+        if (lane == 0) sums[wave][D] = m, sums[wave][D + 1] = l;
+        __syncthreads();
+        if (w != 0) return;
+        float top = kNone;
+        for (int k = 0; k < kRowWaves; ++k) top = fmaxf(top, sums[wave + k][D]);
+        const float ref = top == kNone ? 0.f : top;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+        for (int k = 0; k < kRowWaves; ++k) {
+            const float e = exp2_hw(sums[wave + k][D] - ref);
+            l += sums[wave + k][D + 1] * e;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) acc[i] += sums[wave + k][lane * kV + i] * e;
+        }
+    }
+    if (!live) return;
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const int row = (int)(r % a.rows), head = (int)(r / a.rows);
+    uint16_t* y = a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out + ((int64_t)head * a.group + row % a.group) * D +
+                  lane * kV;
+    if constexpr (kV == 1) {
+        *y = (uint16_t)pack2(acc[0] * inv, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; i += 2) reinterpret_cast<uint32_t*>(y)[i / 2] = pack2(acc[i] * inv, acc[i + 1] * inv);
+    }
+}
+
+// How the call is laid out, from its shapes alone.
+struct Layout {
+    int nr, waves, columns, ranges;        // row tiles per wave, waves per workgroup, workgroups per range
+};
+Layout layout_of(int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim) {
+    const int rows = drafts * (q_heads / kv_heads);
+    Layout l;
+    l.nr = rows > 16 && head_dim <= 128 ? 2 : 1;
+    const int units = kv_heads * ((rows + 16 * l.nr - 1) / (16 * l.nr));
+    l.waves = units < kWaves ? units : kWaves;
+    l.columns = (units + l.waves - 1) / l.waves;
+    int64_t ranges = (int64_t)kWorkgroups * kWaves / ((int64_t)l.columns * l.waves);
+    // a multiple of 8, so that a range's workgroups meet on one XCD
+    ranges = ranges / 8 * 8;
+    l.ranges = (int)(ranges < 8 ? 8 : ranges);
+    (void)batch;
+    return l;
+}
+
+template <int D, int NR>
+hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
+    attn_tree_kernel<D, NR><<<dim3((unsigned)l.ranges, (unsigned)l.columns), 64 * l.waves, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t rows = (int64_t)a.kv_heads * a.rows;
+    // Pieces per sequence on average decide how many waves share a row.
+    if (l.ranges / a.batch >= 32)
+        attn_tree_join_kernel<D, 16><<<dim3((unsigned)rows, (unsigned)a.batch), 1024, 0, s>>>(a);
+    else if (l.ranges / a.batch >= 8)
+        attn_tree_join_kernel<D, 4><<<dim3((unsigned)rows, (unsigned)a.batch), 256, 0, s>>>(a);
+    else
+        attn_tree_join_kernel<D, 1><<<dim3((unsigned)((rows + 3) / 4), (unsigned)a.batch), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
+    const Layout l = layout_of(batch, drafts, q_heads, kv_heads, head_dim);
+    return (size_t)2 * l.ranges * q_heads * drafts * (head_dim + 2) * sizeof(float);
+}
+
+hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
+    const Layout l = layout_of(p.batch, p.drafts, p.q_heads, p.kv_heads, p.head_dim);
+    TreeArgs a{};
+    a.q = p.q, a.ld_q = p.ld_q, a.out = p.out, a.ld_out = p.ld_out;
+    a.kc = p.cache.k_codes, a.ks = p.cache.k_scales, a.vc = p.cache.v_codes, a.vs = p.cache.v_scales;
+    a.num_pages = p.cache.num_pages, a.page_size = (int)p.cache.page_size;
+    a.code_row = (int)(p.cache.d / 2), a.scale_row = (int)(p.cache.d / 32);
+    a.table = p.page_table, a.max_pages = p.max_pages;
+    a.seq_lens = p.seq_lens, a.draft_lens = p.draft_lens, a.mask = p.tree_mask;
+    a.batch = (int)p.batch, a.drafts = p.drafts, a.group = p.q_heads / p.kv_heads, a.kv_heads = p.kv_heads;
+    a.rows = p.drafts * a.group;
+    a.scale2 = p.scale * 1.4426950408889634f;
+    a.part = static_cast<float*>(p.ws), a.ranges = l.ranges;
+    switch (p.head_dim) {
+        case 64: return l.nr == 2 ? launch<64, 2>(a, l, s) : launch<64, 1>(a, l, s);
+        case 128: return l.nr == 2 ? launch<128, 2>(a, l, s) : launch<128, 1>(a, l, s);
+        default: return launch<256, 1>(a, l, s);
+    }
+}
+
+}  // namespace fp4

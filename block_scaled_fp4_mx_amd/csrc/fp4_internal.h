@@ -164,4 +164,22 @@ int64_t kv_copy_blocks(const fp4_kv_cache& c);
 hipError_t launch_kv_copy_pages(const fp4_kv_cache& src, const fp4_kv_cache& dst, const int32_t* src_pages,
                                 const int32_t* dst_pages, int64_t n, hipStream_t s);
 
+struct AttnTree {
+    const uint16_t* q;
+    int64_t ld_q;
+    fp4_kv_cache cache;
+    const int32_t* page_table;
+    int64_t max_pages;
+    const int32_t *seq_lens, *draft_lens;
+    const uint64_t* tree_mask;
+    int64_t batch;
+    int drafts, q_heads, kv_heads, head_dim;
+    float scale;
+    uint16_t* out;
+    int64_t ld_out;
+    void* ws;
+};
+size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
+hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s);
+
 }  // namespace fp4

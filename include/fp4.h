@@ -525,6 +525,34 @@ int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const i
 int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const int32_t* src_pages,
                       const int32_t* dst_pages, int64_t n, void* stream);
 
+/*
+ * Attention of drafted tokens over the cache (speculative decoding; drafts = 1
+ * is an ordinary decode step).  Query row (b, i) sees the committed tokens
+ * [0, seq_lens[b]) of its sequence and drafted token j, whose key and value
+ * stand at position seq_lens[b] + j, where bit j of tree_mask[b, i] is set and
+ * j < draft_lens[b]:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j, softmax statistics and sums in
+ *   fp32, keys and values dequantized exactly, weights rounded to bf16.
+ * A row that sees nothing gives zeros.
+ * q: bf16 [batch * drafts, ld_q]; out: bf16 [batch * drafts, ld_out]; rows
+ * i >= draft_lens[b] are left as they were.  draft_lens: int32 [batch], NULL =
+ * drafts for all.  tree_mask: uint64 [batch, drafts], NULL = token i sees
+ * drafted tokens 0..i.  page_table: int32 [batch, max_pages]; seq_lens: int32
+ * [batch].  Positions behind the table's end or on a page id outside
+ * [0, num_pages) are not seen.
+ * workspace: fp4_attn_tree_workspace_bytes(...) bytes, for the partial results
+ * of contexts that are split over workgroups.  The order of the sums depends on
+ * the shapes and lengths alone, so equal calls give equal bits.
+ * Errors: head_dim not 64, 128 or 256, or cache->d != kv_heads * head_dim, or
+ * q_heads not a multiple of kv_heads -> FP4_ERR_SHAPE; drafts outside [1, 64] ->
+ * FP4_ERR_INVALID; scale not finite -> FP4_ERR_INVALID.
+ */
+int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table,
+                     int64_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                     const uint64_t* tree_mask, int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim,
+                     float scale, void* out, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
+
 #ifdef __cplusplus
 }
 #endif

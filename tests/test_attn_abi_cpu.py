@@ -159,3 +159,54 @@ def test_binding_checks_the_attention_path():
         F.fp4_kv_copy_pages(cache, cache, _int(2), _int(3))
     with pytest.raises(ValueError, match="GPU"):
         F.fp4_kv_copy_pages(cache, cache, _int(2), _int(2))
+
+
+def _tree(q=FAKE, ld_q=512, cache=None, table=FAKE, width=4, lens=FAKE, nd=None, mask=None, batch=2, drafts=4, hq=8, hk=1, d=64,
+          scale=0.1, out=FAR, ld_out=512, ws=FAKE, n=1 << 40):
+    return F.lib.fp4_attn_tree_mx(q, ld_q, cache or _cache(), table, width, lens, nd, mask, batch, drafts, hq, hk, d, scale, out,
+                                  ld_out, ws, n, None)
+
+
+def test_attn_tree_rejections():
+    for kw, status in BAD_CACHES:
+        assert _tree(cache=_cache(**kw)) == status, kw
+    assert _tree(cache=_cache(v_codes=None, v_scales=None)) == INVALID
+    assert _tree(d=96) == SHAPE and _tree(d=32) == SHAPE and _tree(hq=3, hk=2) == SHAPE and _tree(hk=2) == SHAPE
+    assert _tree(hq=0) == INVALID and _tree(hk=0) == INVALID and _tree(hq=8192) == SHAPE
+    assert _tree(drafts=0) == INVALID and _tree(drafts=65) == INVALID and _tree(batch=-1) == INVALID
+    assert _tree(batch=65536) == SHAPE and _tree(width=-1) == INVALID
+    assert _tree(scale=float("nan")) == INVALID and _tree(scale=float("inf")) == INVALID
+    assert _tree(q=None) == INVALID and _tree(out=None) == INVALID and _tree(table=None) == INVALID
+    assert _tree(lens=None) == INVALID and _tree(q=FAKE + 8) == ALIGN and _tree(nd=FAKE + 2) == ALIGN
+    assert _tree(mask=FAKE + 4) == ALIGN and _tree(ld_q=508) == INVALID and _tree(ld_out=516) == ALIGN
+    assert _tree(out=FAKE) == INVALID and b"overlaps" in F.lib.fp4_last_error()
+    need = F.lib.fp4_attn_tree_workspace_bytes(2, 4, 8, 64, 1)
+    assert need > 0 and _tree(n=need - 1) == WORKSPACE and _tree(ws=None) == WORKSPACE and _tree(ws=FAKE + 4) == ALIGN
+    assert F.lib.fp4_attn_tree_workspace_bytes(2, 4, 8, 96, 1) == 0
+    assert F.lib.fp4_attn_tree_workspace_bytes(0, 4, 8, 64, 1) == 0
+    assert _tree(batch=0, q=None, out=None) == OK
+
+
+def test_binding_checks_the_tree_attention():
+    cache = F.KvCache(_u8(160, 64), _u8(160, 4), _u8(160, 64), _u8(160, 4), 16)
+    q = torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16)
+    args = dict(q=q, cache=cache, page_table=_int(2, 5), seq_lens=_int(2), out=torch.zeros_like(q), workspace=_u8(16))
+
+    def refuses(match, error=ValueError, **kw):
+        with pytest.raises(error, match=match):
+            F.fp4_attn_tree_mx(**args | kw)
+
+    refuses("bfloat16", TypeError, q=q.float())
+    refuses("batch, drafts", q=q[0])
+    refuses("heads of q", q=q[:, :, ::2])
+    refuses("one pitch", q=torch.zeros((4, 3, 4, 64), dtype=torch.bfloat16)[::2])
+    refuses("out has shape", out=q[:1])
+    refuses("no values", cache=cache._replace(v_codes=None, v_scales=None))
+    refuses("head_dim", cache=F.KvCache(_u8(160, 48), _u8(160, 3), _u8(160, 48), _u8(160, 3), 16))
+    refuses("page_table", page_table=_int(3, 5))
+    refuses("page_table", TypeError, page_table=_int(2, 5).long())
+    refuses("seq_lens", seq_lens=_int(3))
+    refuses("draft_lens", draft_lens=_int(3))
+    refuses("tree_mask", TypeError, tree_mask=_int(2, 3))
+    refuses("tree_mask", tree_mask=_int(2, 4).long())
+    refuses("GPU")
