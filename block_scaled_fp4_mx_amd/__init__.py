@@ -22,6 +22,7 @@ __all__ = [
     "fp4_ste_backward", "fp4_kv_append_mx", "fp4_moe_grouped_gemm", "fp4_moe_workspace_bytes", "MoeDebug",
     "fp4_qk_norm_rope", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
     "fp4_kv_free", "fp4_kv_compact", "fp4_kv_copy_pages", "fp4_attn_tree_mx", "fp4_attn_tree_workspace_bytes",
+    "fp4_attn_prompt",
     "fp4_abi_version", "LIB_PATH",
 ]
 
@@ -88,6 +89,8 @@ _SIGS = {
     "fp4_attn_tree_mx": (_i32, [_vp, _i64, _cache_p, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _c.c_float, _vp,
                                 _i64, _vp, _sz, _vp]),
     "fp4_attn_tree_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "fp4_attn_prompt": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _c.c_float, _vp, _i64,
+                               _vp]),
 }
 
 
@@ -677,3 +680,21 @@ def fp4_attn_tree_mx(q, cache: KvCache, page_table, seq_lens, out, workspace, dr
     a.call(stream, _ptr(q), ld_q, _c.byref(c), _ptr(page_table), page_table.shape[1], _ptr(seq_lens), _ptr(draft_lens),
            _ptr(tree_mask), batch, drafts, q_heads, c.d // head_dim, head_dim,
            head_dim ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(workspace), workspace.numel())
+
+
+def fp4_attn_prompt(q, k, v, cu_seqlens, out, scale=None, stream=None):
+    """q, out [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim]:
+    causal attention inside each sequence [cu_seqlens[s], cu_seqlens[s + 1])
+    (int32 [seqs + 1]); scale None: head_dim ** -0.5."""
+    a = _Args("fp4_attn_prompt")
+    ld_q, ld_k, ld_v, ld_out = _heads(a, "q", q), _heads(a, "k", k), _heads(a, "v", v), _heads(a, "out", out)
+    tokens, q_heads, head_dim = q.shape
+    if k.shape[0] != tokens or k.shape[2] != head_dim or v.shape != k.shape:
+        raise ValueError(f"{a.fn}: k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}, q {tuple(q.shape)}")
+    if out.shape != q.shape:
+        raise ValueError(f"{a.fn}: out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    a("cu_seqlens", cu_seqlens, _I32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError(f"{a.fn}: cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected [seqs + 1]")
+    a.call(stream, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), cu_seqlens.shape[0] - 1, tokens, q_heads, k.shape[1],
+           head_dim, ld_q, ld_k, ld_v, head_dim ** -0.5 if scale is None else scale, _ptr(out), ld_out)

@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "moe.hip", "qk_norm.hip", "kv_pages.hip",
-           "attn_tree.hip"]
+           "attn_tree.hip", "attn_prompt.hip"]
 PROBES = os.path.join(HERE, "probes")
 PROBE_OUT = os.path.join(PROBES, "libfp4_peak.so")
 FLAGS = [

@@ -726,4 +726,49 @@ int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, con
     return hip_status(fp4::launch_attn_tree(p, static_cast<hipStream_t>(stream)), "fp4_attn_tree_mx launch");
 }
 
+int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int64_t seqs, int64_t tokens,
+                    int q_heads, int kv_heads, int head_dim, int64_t ld_q, int64_t ld_k, int64_t ld_v, float scale,
+                    void* out, int64_t ld_out, void* stream) {
+    if (int e = check_heads(q_heads, kv_heads, head_dim)) return e;
+    FP4_REQUIRE(seqs >= 0 && tokens >= 0, FP4_ERR_INVALID, "negative size seqs=%lld tokens=%lld", (long long)seqs,
+                (long long)tokens);
+    FP4_REQUIRE(tokens < (int64_t)1 << 31 && seqs < kMaxList, FP4_ERR_SHAPE, "tokens=%lld or seqs=%lld too large",
+                (long long)tokens, (long long)seqs);
+    FP4_REQUIRE(fp4::attn_prompt_tiles(seqs, tokens) < ((int64_t)1 << 24) / q_heads, FP4_ERR_SHAPE,
+                "tokens=%lld, seqs=%lld and q_heads=%d give too many row tiles (2^24)", (long long)tokens, (long long)seqs,
+                q_heads);
+    FP4_REQUIRE(std::isfinite(scale), FP4_ERR_INVALID, "scale is not finite");
+    if (seqs == 0 || tokens == 0) return ok();
+    const int64_t wq = (int64_t)q_heads * head_dim, wk = (int64_t)kv_heads * head_dim;
+    FP4_PTR(q);
+    FP4_PTR(k);
+    FP4_PTR(v);
+    FP4_PTR(out);
+    FP4_SCALAR_PTR(cu_seqlens);
+    if (int e = check_ld(ld_q, wq, "ld_q")) return e;
+    if (int e = check_ld(ld_k, wk, "ld_k")) return e;
+    if (int e = check_ld(ld_v, wk, "ld_v")) return e;
+    if (int e = check_ld(ld_out, wq, "ld_out")) return e;
+    FP4_REQUIRE(!rows_overlap(out, ld_out * 2, wq * 2, q, ld_q * 2, wq * 2, tokens), FP4_ERR_INVALID, "out overlaps q");
+    FP4_REQUIRE(!rows_overlap(out, ld_out * 2, wq * 2, k, ld_k * 2, wk * 2, tokens), FP4_ERR_INVALID, "out overlaps k");
+    FP4_REQUIRE(!rows_overlap(out, ld_out * 2, wq * 2, v, ld_v * 2, wk * 2, tokens), FP4_ERR_INVALID, "out overlaps v");
+    fp4::AttnPrompt p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.cu_seqlens = cu_seqlens;
+    p.seqs = seqs;
+    p.tokens = tokens;
+    p.q_heads = q_heads;
+    p.kv_heads = kv_heads;
+    p.head_dim = head_dim;
+    p.ld_q = ld_q;
+    p.ld_k = ld_k;
+    p.ld_v = ld_v;
+    p.scale = scale;
+    p.out = static_cast<uint16_t*>(out);
+    p.ld_out = ld_out;
+    return hip_status(fp4::launch_attn_prompt(p, static_cast<hipStream_t>(stream)), "fp4_attn_prompt launch");
+}
+
 }  // extern "C"

@@ -182,4 +182,17 @@ struct AttnTree {
 size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
 hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s);
 
+struct AttnPrompt {
+    const uint16_t *q, *k, *v;
+    const int32_t* cu_seqlens;
+    int64_t seqs, tokens;
+    int q_heads, kv_heads, head_dim;
+    int64_t ld_q, ld_k, ld_v;
+    float scale;
+    uint16_t* out;
+    int64_t ld_out;
+};
+int64_t attn_prompt_tiles(int64_t seqs, int64_t tokens);
+hipError_t launch_attn_prompt(const AttnPrompt& p, hipStream_t s);
+
 }  // namespace fp4

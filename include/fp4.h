@@ -553,6 +553,22 @@ int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, con
                      float scale, void* out, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
 size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
 
+/*
+ * Causal attention over whole prompts, packed one after another:
+ *   out_i = sum_{j <= i, j in i's sequence} softmax_j(scale * q_i . k_j) v_j,
+ * softmax statistics and sums in fp32, weights rounded to bf16.
+ * cu_seqlens: int32 [seqs + 1], ascending: sequence s has the rows
+ * [cu_seqlens[s], cu_seqlens[s + 1]); empty sequences are fine, values are taken
+ * as within [0, tokens], and rows outside every sequence are left as they were.
+ * q [tokens, ld_q], k [tokens, ld_k], v [tokens, ld_v], out [tokens, ld_out]: bf16.
+ * out may not overlap q, k or v.
+ * Errors: head_dim not 64, 128 or 256, or q_heads not a multiple of kv_heads ->
+ * FP4_ERR_SHAPE; scale not finite -> FP4_ERR_INVALID.
+ */
+int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int64_t seqs,
+                    int64_t tokens, int q_heads, int kv_heads, int head_dim, int64_t ld_q, int64_t ld_k,
+                    int64_t ld_v, float scale, void* out, int64_t ld_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -210,3 +210,43 @@ def test_binding_checks_the_tree_attention():
     refuses("tree_mask", TypeError, tree_mask=_int(2, 3))
     refuses("tree_mask", tree_mask=_int(2, 4).long())
     refuses("GPU")
+
+
+def _prompt(q=FAKE, k=2 * FAKE, v=3 * FAKE, cu=FAKE, seqs=2, tokens=8, hq=4, hk=2, d=64, ld_q=256, ld_k=128, ld_v=128,
+            scale=0.1, out=4 * FAKE, ld_out=256):
+    return F.lib.fp4_attn_prompt(q, k, v, cu, seqs, tokens, hq, hk, d, ld_q, ld_k, ld_v, scale, out, ld_out, None)
+
+
+def test_attn_prompt_rejections():
+    assert _prompt(d=80) == SHAPE and _prompt(hq=3) == SHAPE and _prompt(hk=0) == INVALID
+    assert _prompt(tokens=-1) == INVALID and _prompt(seqs=-1) == INVALID
+    assert _prompt(tokens=1 << 31) == SHAPE and _prompt(seqs=1 << 20) == SHAPE
+    assert _prompt(tokens=1 << 30, hq=64, hk=2, ld_q=4096, ld_out=4096) == SHAPE
+    assert _prompt(scale=float("nan")) == INVALID and _prompt(scale=float("-inf")) == INVALID
+    assert _prompt(q=None) == INVALID and _prompt(k=None) == INVALID and _prompt(v=None) == INVALID
+    assert _prompt(cu=None) == INVALID and _prompt(out=None) == INVALID
+    assert _prompt(q=FAKE + 8) == ALIGN and _prompt(cu=FAKE + 2) == ALIGN
+    assert _prompt(ld_q=248) == INVALID and _prompt(ld_k=132) == ALIGN and _prompt(ld_v=120) == INVALID
+    assert _prompt(ld_out=255) == INVALID
+    for kw in (dict(out=FAKE), dict(out=2 * FAKE), dict(out=3 * FAKE), dict(out=FAKE + 64)):
+        assert _prompt(**kw) == INVALID and b"overlaps" in F.lib.fp4_last_error()
+    # columns of one array: outputs beside the inputs in the same rows do not overlap them
+    assert _prompt(tokens=0, q=None) == OK and _prompt(seqs=0, q=None) == OK
+
+
+def test_binding_checks_the_prompt_attention():
+    x = torch.zeros((8, 4, 64), dtype=torch.bfloat16)
+    args = dict(q=x, k=x[:, :2], v=x[:, :2], cu_seqlens=_int(3), out=x.clone())
+
+    def refuses(match, error=ValueError, **kw):
+        with pytest.raises(error, match=match):
+            F.fp4_attn_prompt(**args | kw)
+
+    refuses("bfloat16", TypeError, v=x.half())
+    refuses("heads of k", k=x[:, ::2])
+    refuses("k and v", k=x[:7, :2])
+    refuses("k and v", v=x[:, :1])
+    refuses("out has shape", out=x[:, :2])
+    refuses("cu_seqlens", TypeError, cu_seqlens=_int(3).long())
+    refuses("cu_seqlens", cu_seqlens=_int(0))
+    refuses("GPU")
