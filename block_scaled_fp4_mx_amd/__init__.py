@@ -122,9 +122,7 @@ class Fp4Error(RuntimeError):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -140,6 +138,8 @@ class _Args:
     leading-dimension parameter), then a tensor not on the GPU.  Dtype and
     layout are checked for every argument before any device check."""
 
+    __slots__ = ("fn", "items")
+
     def __init__(self, fn):
         self.fn, self.items = fn, []
 
@@ -151,10 +151,11 @@ class _Args:
             raise TypeError(f"{fn}: {name} must be a torch tensor, got {type(t).__name__}")
         if t.dtype not in dtypes:
             raise TypeError(f"{fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-        if t.numel() and t.dim() and t.size(-1) > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{fn}: {name} must be contiguous along its last axis")
-        if dense and t.numel() and not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be contiguous")
+        if not t.is_contiguous() and t.numel():
+            if t.dim() and t.size(-1) > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{fn}: {name} must be contiguous along its last axis")
+            if dense:
+                raise ValueError(f"{fn}: {name} must be contiguous")
         self.items.append((name, t))
         return self
 
@@ -167,18 +168,28 @@ class _Args:
         """Checks that all tensors are on one GPU, then calls the C entry point
         with args and the stream (that GPU's current one by default), with that
         GPU as the current device."""
-        self.on_device()
-        dev = self.items[0][1].device
+        dev = self.items[0][1].get_device()
         for name, t in self.items:
-            if t.device != dev:
-                raise ValueError(f"{self.fn}: {name} is on {t.device}, {self.items[0][0]} on {dev}")
+            if t.get_device() != dev or dev < 0:
+                self.on_device()
+                raise ValueError(f"{self.fn}: {name} is on {t.device}, {self.items[0][0]} on {self.items[0][1].device}")
         f = getattr(lib, self.fn)
-        if torch.cuda.current_device() == dev.index:
-            status = f(*args, _stream(stream))
+        if stream is None:
+            stream = _raw_stream(dev)
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
+        if torch.cuda.current_device() == dev:
+            status = f(*args, stream)
         else:
             with torch.cuda.device(dev):
-                status = f(*args, _stream(stream))
-        _check(self.fn, status)
+                status = f(*args, stream)
+        if status:
+            raise Fp4Error(self.fn, status)
+
+
+# The current stream's handle of a GPU by index, without a Stream object where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _shape(fn, name, t, shape, rows_at_least=False):
@@ -195,7 +206,7 @@ def _shape(fn, name, t, shape, rows_at_least=False):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        return _raw_stream(torch.cuda.current_device()) if torch.cuda.is_initialized() else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -326,15 +337,12 @@ def fp4_kv_append_mx(x, slots, cache_codes, cache_scales, tokens=None, d=None, l
     tokens = x.shape[0] if tokens is None else tokens
     d = x.shape[1] if d is None else d
     ld_x = x.stride(0) if ld_x is None else ld_x
-    fn = "fp4_kv_append_mx"
-    a = _Args(fn)
+    a = _Args("fp4_kv_append_mx")
     a("x", x, _BF16, dense=False)
     a("slots", slots, _I32)
     a("cache_codes", cache_codes, _U8)
     a("cache_scales", cache_scales, _U8)
-    a.on_device()
-    _check("fp4_kv_append_mx", lib.fp4_kv_append_mx(_ptr(x), tokens, d, ld_x, _ptr(slots), _ptr(cache_codes),
-                                                    _ptr(cache_scales), cache_codes.shape[0], _stream(stream)))
+    a.call(stream, _ptr(x), tokens, d, ld_x, _ptr(slots), _ptr(cache_codes), _ptr(cache_scales), cache_codes.shape[0])
 
 
 def fp4_fake_quant(fmt, x, out, tensor_scale=None, tensor_scale_is_input=False, workspace=None, rows=None, k=None,
@@ -477,11 +485,14 @@ def _heads(a, name, t):
     """A bf16 [tokens, heads, head_dim] tensor whose heads lie one after another;
     tokens may be any number of elements apart.  Returns its leading dimension."""
     a(name, t, _BF16, dense=False)
-    if t.dim() != 3:
-        raise ValueError(f"{a.fn}: {name} must be [tokens, heads, head_dim], got shape {tuple(t.shape)}")
-    if t.numel() and t.size(1) > 1 and t.stride(1) != t.size(2):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{a.fn}: {name} must be [tokens, heads, head_dim], got shape {tuple(shape)}")
+    tokens, heads, d = shape
+    ld, head, _ = t.stride()
+    if head != d and heads > 1 and tokens and d:
         raise ValueError(f"{a.fn}: the heads of {name} must be contiguous")
-    return t.stride(0) if t.size(0) > 1 else t.size(1) * t.size(2)
+    return ld if tokens > 1 else heads * d
 
 
 def fp4_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -492,26 +503,27 @@ def fp4_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=
     a = _Args("fp4_qk_norm_rope")
     ld_q, ld_k = _heads(a, "q", q), _heads(a, "k", k)
     ld_qo, ld_ko = _heads(a, "q_out", q_out), _heads(a, "k_out", k_out)
-    tokens, q_heads, head_dim = q.shape
-    kv_heads = k.shape[1]
-    if k.shape[0] != tokens or k.shape[2] != head_dim:
-        raise ValueError(f"{a.fn}: k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    tokens, q_heads, head_dim = shape = q.shape
+    k_tokens, kv_heads, k_dim = k_shape = k.shape
+    if k_tokens != tokens or k_dim != head_dim:
+        raise ValueError(f"{a.fn}: k has shape {tuple(k_shape)}, q {tuple(shape)}")
+    if q_out.shape != shape or k_out.shape != k_shape:
         raise ValueError(f"{a.fn}: q_out and k_out must have the shapes of q and k")
-    w_dtypes = _OUT if q_weight is None else (q_weight.dtype,) if k_weight is not None else _OUT
+    dtypes = _OUT
     for nm, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        a(nm, w, _OUT if nm == "q_weight" else w_dtypes, optional=True)
-        if w is not None and tuple(w.shape) != (head_dim,):
-            raise ValueError(f"{a.fn}: {nm} has shape {tuple(w.shape)}, expected {(head_dim,)}")
-    weight = q_weight if q_weight is not None else k_weight
+        if w is not None:
+            a(nm, w, dtypes)
+            dtypes = (w.dtype,)                                       # both of one dtype
+            if w.shape != (head_dim,):
+                raise ValueError(f"{a.fn}: {nm} has shape {tuple(w.shape)}, expected {(head_dim,)}")
     rot_dim = places = 0
     if cos_sin is not None:
         a("cos_sin", cos_sin, _F32)("positions", positions, _I32)
-        if cos_sin.dim() != 2 or tuple(positions.shape) != (tokens,):
+        if cos_sin.dim() != 2 or positions.shape != (tokens,):
             raise ValueError(f"{a.fn}: cos_sin must be [max_positions, rot_dim] and positions [tokens]")
         places, rot_dim = cos_sin.shape
     a.call(stream, _ptr(q), _ptr(k), tokens, q_heads, kv_heads, head_dim, ld_q, ld_k, _ptr(q_weight), _ptr(k_weight),
-           DT_F32 if weight is not None and weight.dtype == torch.float32 else DT_BF16, eps, _ptr(cos_sin), places,
+           DT_F32 if dtypes == _F32 else DT_BF16, eps, _ptr(cos_sin), places,
            rot_dim, int(bool(interleaved)), _ptr(positions) if rot_dim else None, _ptr(q_out), ld_qo, _ptr(k_out), ld_ko)
 
 
@@ -539,34 +551,37 @@ class KvPages(NamedTuple):
 def _kv_cache(a, cache, name="cache"):
     """Checks a KvCache's arrays and returns its C mirror."""
     kc, ks, vc, vs, page_size = cache
-    fn = a.fn
-    a(f"{name}.k_codes", kc, _U8)(f"{name}.k_scales", ks, _U8)
-    a(f"{name}.v_codes", vc, _U8, optional=True)(f"{name}.v_scales", vs, _U8, optional=True)
-    if kc.dim() != 2 or page_size <= 0 or kc.shape[0] % page_size:
-        raise ValueError(f"{fn}: {name}.k_codes must be [num_pages * {page_size}, d/2], got {tuple(kc.shape)}")
-    rows, half = kc.shape
+    a(name + ".k_codes", kc, _U8)(name + ".k_scales", ks, _U8)
+    if vc is not None and vs is not None:
+        a(name + ".v_codes", vc, _U8)(name + ".v_scales", vs, _U8)
+    elif vc is not vs:
+        raise ValueError(f"{a.fn}: {name}.v_codes and v_scales must both be given or both be None")
+    if kc.dim() != 2 or page_size <= 0 or len(kc) % page_size:
+        raise ValueError(f"{a.fn}: {name}.k_codes must be [num_pages * {page_size}, d/2], got {tuple(kc.shape)}")
+    rows, half = shape = kc.shape
     if ks.shape != (rows, half // 16):
-        raise ValueError(f"{fn}: {name}.k_scales has shape {tuple(ks.shape)}, expected {(rows, half // 16)}")
-    if (vc is None) != (vs is None):
-        raise ValueError(f"{fn}: {name}.v_codes and v_scales must both be given or both be None")
-    if vc is not None and (vc.shape != kc.shape or vs.shape != ks.shape):
-        raise ValueError(f"{fn}: the values of {name} must have the shapes of its keys")
-    return _KvCacheC(_ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), rows // page_size, 2 * half, page_size)
+        raise ValueError(f"{a.fn}: {name}.k_scales has shape {tuple(ks.shape)}, expected {(rows, half // 16)}")
+    if vc is None:
+        return _KvCacheC(kc.data_ptr(), ks.data_ptr(), None, None, rows // page_size, 2 * half, page_size)
+    if vc.shape != shape or vs.shape != ks.shape:
+        raise ValueError(f"{a.fn}: the values of {name} must have the shapes of its keys")
+    return _KvCacheC(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), rows // page_size, 2 * half, page_size)
 
 
 def _kv_pages(a, pages):
     """Checks a KvPages' arrays and returns its C mirror."""
     table, counts, lens, refs = pages
     a("page_table", table, _I32)("page_counts", counts, _I32)("seq_lens", lens, _I32)("page_refs", refs, _I32)
-    if table.dim() != 2 or counts.shape != table.shape[:1] or lens.shape != table.shape[:1] or refs.dim() != 1:
+    shape = table.shape
+    if len(shape) != 2 or counts.shape != shape[:1] or lens.shape != shape[:1] or refs.dim() != 1:
         raise ValueError(f"{a.fn}: page_table must be [batch, max_pages], page_counts and seq_lens [batch], "
                          "page_refs [num_pages]")
-    return _KvPagesC(_ptr(table), _ptr(counts), _ptr(lens), _ptr(refs), table.shape[0], table.shape[1], refs.shape[0])
+    return _KvPagesC(table.data_ptr(), counts.data_ptr(), lens.data_ptr(), refs.data_ptr(), *shape, len(refs))
 
 
 def _per_seq(a, name, t, n, optional=False):
     a(name, t, _I32, optional=optional)
-    if t is not None and tuple(t.shape) != (n,):
+    if t is not None and t.shape != (n,):
         raise ValueError(f"{a.fn}: {name} has shape {tuple(t.shape)}, expected {(n,)}")
 
 
