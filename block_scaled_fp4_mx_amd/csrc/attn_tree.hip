@@ -31,6 +31,8 @@
 // equal ranges, one per workgroup column, whatever the lengths; a sequence that
 // a cut goes through leaves partial (m, sum, o) in the workspace, at most two
 // per range, and a second kernel joins them in order.
+#include <type_traits>
+
 #include "fp4_internal.h"
 #include "mma_core.h"
 
@@ -45,6 +47,7 @@ constexpr float kSlack = 8.0f;             // scores may exceed the reference by
 constexpr float kNone = -__builtin_inff();
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 struct TreeArgs {
@@ -59,7 +62,8 @@ struct TreeArgs {
     const int32_t *seq_lens, *draft_lens;
     const uint64_t* mask;
     int batch, drafts, group, kv_heads, rows;   // rows = drafts * group: query rows of a key/value head
-    float scale2;                          // scale * log2(e)
+    float scale2;                          // |scale| * log2(e), positive
+    uint32_t flip;                         // sign bits of Q, set for a negative scale
     uint16_t* out;
     int64_t ld_out;
     float* part;                           // [2 * ranges][kv_heads][rows][D] sums, then [..][2] (m, sum)
@@ -71,17 +75,18 @@ __device__ __forceinline__ int drafts_of(const TreeArgs& a, int b) {
 }
 
 // Tokens of sequence b that can be seen at all: its committed and drafted ones,
-// as far as the table's row goes (none in an empty pool).
-__device__ __forceinline__ int64_t tokens_of(const TreeArgs& a, int b) {
+// as far as the table's row goes (none in an empty pool).  Positions of a tile
+// stay below 2^31.
+__device__ __forceinline__ int tokens_of(const TreeArgs& a, int b) {
     const int64_t n = (int64_t)max(a.seq_lens[b], 0) + drafts_of(a, b);
-    return a.num_pages ? min(n, a.max_pages * a.page_size) : 0;
+    return a.num_pages ? (int)min(min(n, a.max_pages * a.page_size), (int64_t)0x7FFFFFC0) : 0;
 }
 
 // Tiles of sequence b; a sequence with drafted tokens has at least one, so that
 // its rows are written.
-__device__ __forceinline__ int64_t tiles_of(const TreeArgs& a, int b) {
+__device__ __forceinline__ int tiles_of(const TreeArgs& a, int b) {
     if (b >= a.batch || drafts_of(a, b) == 0) return 0;
-    return max((tokens_of(a, b) + kTile - 1) / kTile, (int64_t)1);
+    return max((tokens_of(a, b) + kTile - 1) / kTile, 1);
 }
 
 // A value equal in all lanes, as a scalar (so that what follows from it is one too).
@@ -131,58 +136,90 @@ __device__ __forceinline__ u32x4 widen8(uint32_t w, float scale) {
 }
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 template <int D>
 struct Raw {                               // one tile's bytes of one lane
     static constexpr int kK = D / 32;      // dwords of a quarter row
     static constexpr int kKS = D == 256 ? 2 : 1;
     uint32_t k[2][kK];
-    uint8_t ks[2][kKS];
+    uint32_t ks[2][kKS];
     uint32_t v[8][D == 256 ? 2 : 1];       // D == 64: 4 codes in the low half
-    uint8_t vs[8];
+    uint32_t vs[8];
 };
 
 // A tile's place: the first cache row of its two halves (-1: no page).
 struct Place {
-    int64_t row[2];
+    int row[2];
 };
 
+// Byte offsets of a lane's loads within 16 cache rows; unsigned, so that a load
+// is a scalar base and this offset without address arithmetic.
+struct Offsets {
+    uint32_t k, ks, v[4], vs[4];
+};
 template <int D>
-__device__ __forceinline__ void load_tile(Raw<D>& r, const TreeArgs& a, const Place& p, int head, int c, int g) {
-    const int kofs = c * a.code_row + head * (D / 2) + g * (D / 8);
-    const int ksofs = c * a.scale_row + head * (D / 32) + (D == 64 ? g / 2 : D == 128 ? g : 2 * g);
-    const int vofs = 4 * g * a.code_row + head * (D / 2) + c * (D / 32);
-    const int vsofs = 4 * g * a.scale_row + head * (D / 32) + c * (D / 16) / 32;
+__device__ __forceinline__ Offsets offsets_of(const TreeArgs& a, int head, int c, int g) {
+    Offsets o;
+    o.k = c * a.code_row + head * (D / 2) + g * (D / 8);
+    o.ks = c * a.scale_row + head * (D / 32) + (D == 64 ? g / 2 : D == 128 ? g : 2 * g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        o.v[j] = (4 * g + j) * a.code_row + head * (D / 2) + c * (D / 32);
+        o.vs[j] = (4 * g + j) * a.scale_row + head * (D / 32) + c * (D / 16) / 32;
+    }
+    return o;
+}
+
+// Global memory at a uniform address, kept in scalar registers: else its sum with
+// a lane's offset is formed per lane and load, in 64-bit vector arithmetic.
+#define FP4_GLOBAL __attribute__((address_space(1)))
+typedef const FP4_GLOBAL uint8_t* gbytes;
+__device__ __forceinline__ gbytes scalar_base(const uint8_t* p) {
+    gbytes g = (gbytes)p;
+    asm("" : "+s"(g));
+    return g;
+}
+// One load at base + offset + imm.  The offset is renewed here so that its widening
+// to 64 bits stays beside the load, where the load takes it as a 32-bit register.
+template <typename T>
+__device__ __forceinline__ T load_at(gbytes base, uint32_t offset, int imm = 0) {
+    asm volatile("" : "+v"(offset));
+    return *(const FP4_GLOBAL T*)(base + offset + imm);
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(Raw<D>& r, const TreeArgs& a, const Place& p, const Offsets& o) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int64_t row = p.row[h] < 0 ? 0 : p.row[h];      // any row of the pool: masked later
-        const uint8_t* kc = a.kc + row * a.code_row;
-        const uint8_t* ks = a.ks + row * a.scale_row;
-        const uint8_t* vc = a.vc + row * a.code_row;
-        const uint8_t* vs = a.vs + row * a.scale_row;
+        const int64_t row = max(p.row[h], 0);                 // any row of the pool: masked later
+        const gbytes kc = scalar_base(a.kc + row * a.code_row), ks = scalar_base(a.ks + row * a.scale_row);
+        const gbytes vc = scalar_base(a.vc + row * a.code_row), vs = scalar_base(a.vs + row * a.scale_row);
         if constexpr (D == 64) {
-            const uint2 x = *reinterpret_cast<const uint2*>(kc + kofs);
-            r.k[h][0] = x.x, r.k[h][1] = x.y;
+            const u32x2 x = load_at<u32x2>(kc, o.k);
+            r.k[h][0] = x[0], r.k[h][1] = x[1];
         } else {
 #pragma unroll
             for (int i = 0; i < D / 128; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4*>(kc + kofs + 16 * i);
-                r.k[h][4 * i] = x.x, r.k[h][4 * i + 1] = x.y, r.k[h][4 * i + 2] = x.z, r.k[h][4 * i + 3] = x.w;
+                const u32x4 x = load_at<u32x4>(kc, o.k, 16 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r.k[h][4 * i + j] = x[j];
             }
         }
 #pragma unroll
-        for (int i = 0; i < Raw<D>::kKS; ++i) r.ks[h][i] = ks[ksofs + i];
+        for (int i = 0; i < Raw<D>::kKS; ++i) r.ks[h][i] = load_at<uint8_t>(ks, o.ks, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint8_t* x = vc + vofs + j * a.code_row;
             if constexpr (D == 64) {
-                r.v[4 * h + j][0] = *reinterpret_cast<const uint16_t*>(x);
+                r.v[4 * h + j][0] = load_at<uint16_t>(vc, o.v[j]);
             } else if constexpr (D == 128) {
-                r.v[4 * h + j][0] = *reinterpret_cast<const uint32_t*>(x);
+                r.v[4 * h + j][0] = load_at<uint32_t>(vc, o.v[j]);
             } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(x);
-                r.v[4 * h + j][0] = y.x, r.v[4 * h + j][1] = y.y;
+                const u32x2 y = load_at<u32x2>(vc, o.v[j]);
+                r.v[4 * h + j][0] = y[0], r.v[4 * h + j][1] = y[1];
             }
-            r.vs[4 * h + j] = vs[vsofs + j * a.scale_row];
+            r.vs[4 * h + j] = load_at<uint8_t>(vs, o.vs[j]);
         }
     }
 }
@@ -194,17 +231,19 @@ __device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
 }
 
 template <int D, int NR>
-__global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a) {
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
     constexpr int kSteps = D / 32, kOut = D / 16;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int row_groups = (a.rows + 16 * NR - 1) / (16 * NR);
     const int unit = __builtin_amdgcn_readfirstlane(blockIdx.y * (blockDim.x >> 6) + (threadIdx.x >> 6));
     if (unit >= a.kv_heads * row_groups) return;
-    const int head = unit % a.kv_heads, r0 = unit / a.kv_heads * 16 * NR;
+    const int head = __builtin_amdgcn_readfirstlane(unit % a.kv_heads);
+    const int r0 = __builtin_amdgcn_readfirstlane(unit / a.kv_heads) * 16 * NR;
 
+    const Offsets offsets = offsets_of<D>(a, head, c, g);
     const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
     if ((int64_t)blockIdx.x >= ranges || total == 0) return;
-    const int64_t lo = blockIdx.x * total / ranges, hi = (blockIdx.x + 1) * total / ranges;
+    const int64_t lo = scalar(blockIdx.x * total / ranges), hi = scalar((blockIdx.x + 1) * total / ranges);
 
     // The sequence that holds tile lo, and the tiles before it.
     int b = 0;
@@ -228,11 +267,12 @@ __global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a
     b = __builtin_amdgcn_readfirstlane(b);
 
     for (int64_t at = lo; at < hi; ++b) {
-        const int64_t tiles = tiles_of(a, b);
+        const int tiles = __builtin_amdgcn_readfirstlane(tiles_of(a, b));
         if (tiles == 0) continue;
-        const int64_t t0 = at - before, t1 = min(hi - before, tiles);
-        const int64_t len = max(a.seq_lens[b], 0), seen = tokens_of(a, b);
-        const int nd = drafts_of(a, b);
+        const int t0 = (int)(at - before), t1 = (int)min(hi - before, (int64_t)tiles);
+        const int len = __builtin_amdgcn_readfirstlane(max(a.seq_lens[b], 0));
+        const int seen = __builtin_amdgcn_readfirstlane(tokens_of(a, b));
+        const int nd = __builtin_amdgcn_readfirstlane(drafts_of(a, b));
         const int32_t* table = a.table + (int64_t)b * a.max_pages;
 
         u32x4 q[NR][kSteps];
@@ -245,7 +285,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a
                                 ((int64_t)head * a.group + row % a.group) * D + g * (D / 4);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
-                q[n][s] = live ? *reinterpret_cast<const u32x4*>(x + 8 * s) : u32x4{0, 0, 0, 0};
+                q[n][s] = live ? *reinterpret_cast<const u32x4*>(x + 8 * s) ^ a.flip : u32x4{0, 0, 0, 0};
             vis[n] = 0;
             if (live) {
                 vis[n] = a.mask ? a.mask[(int64_t)b * a.drafts + t] : ~0ull >> (63 - t);
@@ -262,29 +302,43 @@ __global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a
             for (int i = 0; i < kOut; ++i) o[n][i] = v4f{0.f, 0.f, 0.f, 0.f};
         }
 
-        // Page of the next 16 tokens to place.
-        int64_t page_i = t0 * kTile / a.page_size;
-        int off = (int)(t0 * kTile - page_i * a.page_size);
+        // Places the next 16 tokens at a time.  The lanes hold 64 page ids of the
+        // row (one load per 64 pages), read by lane when their turn comes.
+        int page_i = __builtin_amdgcn_readfirstlane(t0 * (kTile / 16) / (a.page_size / 16));
+        int off = t0 * kTile - page_i * a.page_size;
+        int pages = 0, first_page = page_i - 64;
+        const int width = (int)a.max_pages;
+        const uint32_t pool = (uint32_t)a.num_pages;
         auto place = [&]() {
             Place p;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int32_t page = page_i < a.max_pages ? table[page_i] : -1;
-                p.row[h] = page >= 0 && page < a.num_pages ? (int64_t)page * a.page_size + off : -1;
+                if (page_i >= first_page + 64) {
+                    first_page = page_i;
+                    const int i = page_i + lane;
+                    pages = table[min(i, width - 1)];
+                    if (i >= width) pages = -1;
+                }
+                const int page = __builtin_amdgcn_readlane(pages, page_i - first_page);
+                p.row[h] = (uint32_t)page < pool ? page * a.page_size + off : -1;
                 off += 16;
-                if (off == a.page_size) off = 0, ++page_i;
+                const int wrap = off == a.page_size;
+                off = wrap ? 0 : off;
+                page_i += wrap;
             }
             return p;
         };
-        Raw<D> cur, next;
-        Place here = place(), ahead = place();
-        if (seen > 0) load_tile<D>(cur, a, here, head, c, g);
-        for (int64_t t = t0; t < t1 && seen > 0; ++t) {
-            if (t + 1 < t1) load_tile<D>(next, a, ahead, head, c, g);
+        Raw<D> raw[2];                                        // of this tile and the next, in turn
+        Place here{}, ahead{};
+        if (seen > 0) {
+            here = place(), ahead = place();
+            load_tile<D>(raw[0], a, here, offsets);
+        }
+        auto step = [&](int t, Raw<D>& cur, Raw<D>& next) {
+            if (t + 1 < t1) load_tile<D>(next, a, ahead, offsets);
             const Place later = place();
-
-            const int64_t pos0 = t * kTile;
-            const bool edge = pos0 + kTile > len || here.row[0] < 0 || here.row[1] < 0;     // uniform
+            const int pos0 = t * kTile;
+            const bool edge = pos0 + kTile > len || here.row[0] < 0 || here.row[1] < 0;     // some token is hidden
             v4f s[NR][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -300,55 +354,29 @@ __global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a
                                                                           0, 0, 0);
                 }
             }
-            // V: bytes of 8 tokens widened, then tokens paired per value.
-            u32x4 v[kOut];
-            {
-                constexpr int kBytes = D / 32;               // of a token's values in this lane
-                uint32_t w[8][kBytes];
+            if (edge) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    uint32_t byte = cur.vs[j];
-                    if (edge) {
-                        const int64_t pos = pos0 + 16 * (j / 4) + 4 * g + j % 4;
-                        if (pos >= seen || here.row[j / 4] < 0) byte = 127;      // whatever lies there, finite
-                    }
-                    const float sc = scale_of(byte);
-                    w[j][0] = widen<0>(cur.v[j][0], sc);
-                    w[j][1] = widen<1>(cur.v[j][0], sc);
-                    if constexpr (D >= 128) {
-                        w[j][2] = widen<2>(cur.v[j][0], sc);
-                        w[j][3] = widen<3>(cur.v[j][0], sc);
-                    }
-                    if constexpr (D == 256) {
-                        w[j][4] = widen<0>(cur.v[j][1], sc);
-                        w[j][5] = widen<1>(cur.v[j][1], sc);
-                        w[j][6] = widen<2>(cur.v[j][1], sc);
-                        w[j][7] = widen<3>(cur.v[j][1], sc);
+                    const int pos = pos0 + 16 * (j / 4) + 4 * g + j % 4, d = pos - len;
+                    const bool there = (pos < seen) & (here.row[j / 4] >= 0);
+                    cur.vs[j] = there ? cur.vs[j] : 127;          // whatever lies there, finite
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const bool see = there & ((d < 0) | ((uint32_t)(vis[n] >> (d & 63)) & 1u));
+                        s[n][j / 4][j % 4] = see ? s[n][j / 4][j % 4] : kNone;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < kOut; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[i][j] = i & 1 ? pair<true>(w[2 * j][i / 2], w[2 * j + 1][i / 2])
-                                        : pair<false>(w[2 * j][i / 2], w[2 * j + 1][i / 2]);
             }
+            bf16x8 p[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 float x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = s[n][j / 4][j % 4] * a.scale2;
-                if (edge) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int64_t pos = pos0 + 16 * (j / 4) + 4 * g + j % 4, d = pos - len;
-                        const bool see = pos < seen && here.row[j / 4] >= 0 && (d < 0 || ((vis[n] >> (d & 63)) & 1));
-                        x[j] = see ? x[j] : kNone;
-                    }
-                }
+                for (int j = 0; j < 8; ++j) x[j] = s[n][j / 4][j % 4];
                 float top = x[0];
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+                top *= a.scale2;
                 if (__any(top > m[n] + kSlack)) {
                     top = fmaxf(top, __shfl_xor(top, 16, 64));
                     top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -360,21 +388,39 @@ __global__ __launch_bounds__(64 * kWaves) void attn_tree_kernel(const TreeArgs a
                     for (int i = 0; i < kOut; ++i) o[n][i] *= alpha;
                 }
                 const float ref = m[n] == kNone ? 0.0f : m[n];
-                u32x4 p;
+                u32x4 w;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float p0 = exp2_hw(x[2 * j] - ref), p1 = exp2_hw(x[2 * j + 1] - ref);
+                    const float p0 = exp2_hw(fmaf(x[2 * j], a.scale2, -ref)), p1 = exp2_hw(fmaf(x[2 * j + 1], a.scale2, -ref));
                     sum[n] += p0 + p1;
-                    p[j] = pack2(p0, p1);
+                    w[j] = pack2(p0, p1);
                 }
-                const bf16x8 pb = __builtin_bit_cast(bf16x8, p);
-#pragma unroll
-                for (int i = 0; i < kOut; ++i)
-                    o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v[i]), pb, o[n][i], 0, 0, 0);
+                p[n] = __builtin_bit_cast(bf16x8, w);
             }
-            cur = next;
+            // V, a byte (two values) of the lane's 8 tokens at a time: widened, then
+            // tokens paired per value.
+            auto values = [&](auto byte_tag) {
+                constexpr int kB = decltype(byte_tag)::value;
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = widen<kB % 4>(cur.v[j][kB / 4], scale_of(cur.vs[j]));
+                const u32x4 lo = {pair<false>(w[0], w[1]), pair<false>(w[2], w[3]), pair<false>(w[4], w[5]), pair<false>(w[6], w[7])};
+                const u32x4 hi = {pair<true>(w[0], w[1]), pair<true>(w[2], w[3]), pair<true>(w[4], w[5]), pair<true>(w[6], w[7])};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    o[n][2 * kB] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lo), p[n], o[n][2 * kB], 0, 0, 0);
+                    o[n][2 * kB + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, hi), p[n], o[n][2 * kB + 1], 0, 0, 0);
+                }
+            };
+            values(Int<0>()), values(Int<1>());
+            if constexpr (D >= 128) values(Int<2>()), values(Int<3>());
+            if constexpr (D == 256) values(Int<4>()), values(Int<5>()), values(Int<6>()), values(Int<7>());
             here = ahead;
             ahead = later;
+        };
+        for (int t = t0; t < t1 && seen > 0; t += 2) {
+            step(t, raw[0], raw[1]);
+            if (t + 1 < t1) step(t + 1, raw[1], raw[0]);
         }
 
         const bool whole = t0 == 0 && t1 == tiles;
@@ -562,7 +608,9 @@ hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
     a.seq_lens = p.seq_lens, a.draft_lens = p.draft_lens, a.mask = p.tree_mask;
     a.batch = (int)p.batch, a.drafts = p.drafts, a.group = p.q_heads / p.kv_heads, a.kv_heads = p.kv_heads;
     a.rows = p.drafts * a.group;
-    a.scale2 = p.scale * 1.4426950408889634f;
+    // Never 0: a hidden score is -inf and has to stay that when scaled.
+    a.scale2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
+    a.flip = p.scale < 0 ? 0x80008000u : 0u;
     a.part = static_cast<float*>(p.ws), a.ranges = l.ranges;
     switch (p.head_dim) {
         case 64: return l.nr == 2 ? launch<64, 2>(a, l, s) : launch<64, 1>(a, l, s);
