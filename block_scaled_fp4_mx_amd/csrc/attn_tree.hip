@@ -465,94 +465,97 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
     }
 }
 
-// Joins the partial results of the sequences that were cut: kRowWaves waves to
-// a row, pieces dealt to them in turn, their sums joined in wave order.
-// Workgroup (x, y): sequence y, rows from x * (4 / kRowWaves) (or one) on.
-template <int D, int kRowWaves>
-__global__ __launch_bounds__(64 * (kRowWaves < 4 ? 4 : kRowWaves)) void attn_tree_join_kernel(const TreeArgs a) {
-    constexpr int kAll = kRowWaves < 4 ? 4 : kRowWaves, kRows = kAll / kRowWaves, kV = D / 64;
-    __shared__ float sums[kAll][D + 2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % kRowWaves;
-    const int b = blockIdx.y, nd = drafts_of(a, b);
-    const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total), tiles = tiles_of(a, b);
+// Joins the partial results of the sequences that were cut.  A team of D/4 lanes
+// takes a row (16 bytes a lane); kTeams of them share one, pieces dealt to them in
+// turn, and their sums are joined through LDS in team order.  Workgroups of
+// sequence y stride over its rows, so what the pieces are is found once for many.
+template <int D, int kTeams, int kBlock>
+__global__ __launch_bounds__(kBlock) void attn_tree_join_kernel(const TreeArgs a) {
+    constexpr int kLanes = D / 4, kRows = kBlock / kLanes / kTeams, kBatch = 8;
+    __shared__ float4 sums[kTeams > 1 ? kBlock : 1];
+    __shared__ float2 stats[kTeams > 1 ? kBlock / kLanes : 1];
+    const int lane = threadIdx.x & 63, b = blockIdx.y;
+    const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
+    const int tiles = __builtin_amdgcn_readfirstlane(tiles_of(a, b)), nd = drafts_of(a, b);
     if (tiles == 0) return;
     const int64_t before = tiles_before(a, b, lane);
-    const int64_t first = ((before + 1) * ranges - 1) / total, last = ((before + tiles) * ranges - 1) / total;
+    const int first = (int)scalar(((before + 1) * ranges - 1) / total);
+    const int last = (int)scalar(((before + tiles) * ranges - 1) / total);
     if (first == last) return;                                // one piece: written already
-    const int64_t r = (int64_t)blockIdx.x * kRows + wave / kRowWaves;   // row among kv_heads * rows
-    const bool live = r < (int64_t)a.kv_heads * a.rows && (int)(r % a.rows) / a.group < nd;
-    const int64_t stride = (int64_t)a.kv_heads * a.rows;
-    const float* ml = a.part + 2 * a.ranges * stride * D;
-    float m = kNone, l = 0.f, acc[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-    if (live) {
-        // The first piece is its range's second one unless the range starts with it.
-        const int64_t first_slot = 2 * first + (first * total / ranges == before ? 0 : 1);
-        constexpr int kBatch = 8;
-        for (int64_t x0 = first + w; x0 <= last; x0 += kBatch * kRowWaves) {
-            float pm[kBatch], pl[kBatch], po[kBatch][kV];
+    // The first piece is its range's second one unless the range starts with it.
+    const int first_slot = 2 * first + (scalar(first * total / ranges) == before ? 0 : 1);
+    const int all_rows = a.kv_heads * a.rows;
+    const float* ml = a.part + 2 * (int64_t)a.ranges * all_rows * D;
+    const int team = threadIdx.x / kLanes, part = team % kTeams, l4 = threadIdx.x % kLanes * 4;
+    for (int r0 = blockIdx.x * kRows; r0 < all_rows; r0 += gridDim.x * kRows) {
+        const int r = r0 + team / kTeams;
+        const bool live = r < all_rows && r % a.rows / a.group < nd;
+        float m = kNone, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int x0 = first + part; live && x0 <= last; x0 += kBatch * kTeams) {
+            float2 s[kBatch];
+            float4 o[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int64_t x = x0 + k * kRowWaves;
-                pm[k] = kNone, pl[k] = 0.f;
-#pragma unroll
-                for (int i = 0; i < kV; ++i) po[k][i] = 0.f;
+                const int x = x0 + k * kTeams;
+                s[k] = make_float2(kNone, 0.f);
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (x <= last) {
-                    const int64_t at = (x == first ? first_slot : 2 * x) * stride + r;
-                    pm[k] = ml[at * 2], pl[k] = ml[at * 2 + 1];
-#pragma unroll
-                    for (int i = 0; i < kV; ++i) po[k][i] = a.part[at * D + lane * kV + i];
+                    const int64_t at = (int64_t)(x == first ? first_slot : 2 * x) * all_rows + r;
+                    s[k] = *reinterpret_cast<const float2*>(ml + at * 2);
+                    o[k] = *reinterpret_cast<const float4*>(a.part + at * D + l4);
                 }
             }
             float top = m;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, pm[k]);
-            const float ref = top == kNone ? 0.f : top;
-            const float keep = exp2_hw(m - ref);
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
+            const float ref = top == kNone ? 0.f : top, keep = exp2_hw(m - ref);
             m = top;
             l *= keep;
 #pragma unroll
-            for (int i = 0; i < kV; ++i) acc[i] *= keep;
+            for (int i = 0; i < 4; ++i) acc[i] *= keep;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const float e = exp2_hw(pm[k] - ref);
-                l += pl[k] * e;
-#pragma unroll
-                for (int i = 0; i < kV; ++i) acc[i] += po[k][i] * e;
+                const float e = exp2_hw(s[k].x - ref);
+                l += s[k].y * e;
+                acc[0] += o[k].x * e, acc[1] += o[k].y * e, acc[2] += o[k].z * e, acc[3] += o[k].w * e;
             }
         }
-    }
-    if constexpr (kRowWaves > 1) {
+        if constexpr (kTeams > 1) {
+            sums[threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (l4 == 0) stats[team] = make_float2(m, l);
+            __syncthreads();
+            if (part == 0) {
+                float top = kNone;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sums[wave][lane * kV + i] = acc[i];
-        if (lane == 0) sums[wave][D] = m, sums[wave][D + 1] = l;
-        __syncthreads();
-        if (w != 0) return;
-        float top = kNone;
-        for (int k = 0; k < kRowWaves; ++k) top = fmaxf(top, sums[wave + k][D]);
-        const float ref = top == kNone ? 0.f : top;
-        l = 0.f;
+                for (int k = 0; k < kTeams; ++k) top = fmaxf(top, stats[team + k].x);
+                const float ref = top == kNone ? 0.f : top;
+                l = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-        for (int k = 0; k < kRowWaves; ++k) {
-            const float e = exp2_hw(sums[wave + k][D] - ref);
-            l += sums[wave + k][D + 1] * e;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) acc[i] += sums[wave + k][lane * kV + i] * e;
+                for (int k = 0; k < kTeams; ++k) {
+                    const float e = exp2_hw(stats[team + k].x - ref);
+                    const float4 o = sums[threadIdx.x + k * kLanes];
+                    l += stats[team + k].y * e;
+                    acc[0] += o.x * e, acc[1] += o.y * e, acc[2] += o.z * e, acc[3] += o.w * e;
+                }
+            }
+            __syncthreads();                                  // sums free for the next rows
+        }
+        if (live && part == 0) {
+            const float inv = l > 0.f ? 1.0f / l : 0.f;
+            const int row = r % a.rows, head = r / a.rows;
+            uint16_t* y = a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out +
+                          ((int64_t)head * a.group + row % a.group) * D + l4;
+            *reinterpret_cast<uint2*>(y) = make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
         }
     }
-    if (!live) return;
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    const int row = (int)(r % a.rows), head = (int)(r / a.rows);
-    uint16_t* y = a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out + ((int64_t)head * a.group + row % a.group) * D +
-                  lane * kV;
-    if constexpr (kV == 1) {
-        *y = (uint16_t)pack2(acc[0] * inv, 0.f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kV; i += 2) reinterpret_cast<uint32_t*>(y)[i / 2] = pack2(acc[i] * inv, acc[i + 1] * inv);
-    }
+}
+
+template <int D, int kTeams, int kBlock>
+void launch_join(const TreeArgs& a, hipStream_t s) {
+    constexpr int kRows = kBlock / (D / 4) / kTeams;
+    const int64_t need = ((int64_t)a.kv_heads * a.rows + kRows - 1) / kRows, most = 2048 * 256 / kBlock / a.batch;
+    const unsigned x = (unsigned)(need < most ? need : most < 1 ? 1 : most);
+    attn_tree_join_kernel<D, kTeams, kBlock><<<dim3(x, (unsigned)a.batch), kBlock, 0, s>>>(a);
 }
 
 // How the call is laid out, from its shapes alone.
@@ -579,14 +582,13 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
     attn_tree_kernel<D, NR><<<dim3((unsigned)l.ranges, (unsigned)l.columns), 64 * l.waves, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t rows = (int64_t)a.kv_heads * a.rows;
-    // Pieces per sequence on average decide how many waves share a row.
-    if (l.ranges / a.batch >= 32)
-        attn_tree_join_kernel<D, 16><<<dim3((unsigned)rows, (unsigned)a.batch), 1024, 0, s>>>(a);
-    else if (l.ranges / a.batch >= 8)
-        attn_tree_join_kernel<D, 4><<<dim3((unsigned)rows, (unsigned)a.batch), 256, 0, s>>>(a);
+    // Pieces of a sequence on average: how many teams share a row.
+    if (l.ranges >= 32 * a.batch)
+        launch_join<D, 16, 1024>(a, s);
+    else if (l.ranges >= 8 * a.batch)
+        launch_join<D, 4, 256>(a, s);
     else
-        attn_tree_join_kernel<D, 1><<<dim3((unsigned)((rows + 3) / 4), (unsigned)a.batch), 256, 0, s>>>(a);
+        launch_join<D, 1, 256>(a, s);
     return hipGetLastError();
 }
 
