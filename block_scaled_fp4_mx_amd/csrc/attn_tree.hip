@@ -44,9 +44,11 @@ constexpr int kWaves = 4;                  // at most, per workgroup
 constexpr int kMinTiles = 4;               // tiles per range below which fewer ranges are used
 constexpr int kWorkgroups = 512;           // two per CU: two waves per SIMD
 constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
-constexpr float kNone = -__builtin_inff();
+constexpr float kNone = -__builtin_inff();   // score of a hidden token
+constexpr float kFloor = -3e38f;           // reference of a row that has seen nothing
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) uint8_t* lds_bytes;
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
@@ -134,92 +136,144 @@ __device__ __forceinline__ uint32_t widen(uint32_t w, float scale) {
 __device__ __forceinline__ u32x4 widen8(uint32_t w, float scale) {
     return u32x4{widen<0>(w, scale), widen<1>(w, scale), widen<2>(w, scale), widen<3>(w, scale)};
 }
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+// A block's scale from the aligned word that holds its byte: rotated so that the
+// byte stands in the exponent's bits; widen looks at no others.
+__device__ __forceinline__ float scale_of(uint32_t word, uint32_t turn) {
+    return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
+}
+constexpr uint32_t kOnes = 0x7F7F7F7Fu;    // scales of 1
 
 template <int N>
 using Int = std::integral_constant<int, N>;
-
-template <int D>
-struct Raw {                               // one tile's bytes of one lane
-    static constexpr int kK = D / 32;      // dwords of a quarter row
-    static constexpr int kKS = D == 256 ? 2 : 1;
-    uint32_t k[2][kK];
-    uint32_t ks[2][kKS];
-    uint32_t v[8][D == 256 ? 2 : 1];       // D == 64: 4 codes in the low half
-    uint32_t vs[8];
-};
 
 // A tile's place: the first cache row of its two halves (-1: no page).
 struct Place {
     int row[2];
 };
 
-// Byte offsets of a lane's loads within 16 cache rows; unsigned, so that a load
-// is a scalar base and this offset without address arithmetic.
-struct Offsets {
-    uint32_t k, ks, v[4], vs[4];
+// One wave's staging of a tile in LDS.  Rows are read from global memory in
+// 16-byte chunks, neighbouring lanes in neighbouring chunks of a row, straight
+// into LDS: the vector memory pipe is bound by requests, and loads in the matrix
+// core's layout (a lane its own row) would cost it several times as many.
+//   keys    32 rows of kChunks chunks; chunk x of row r at x ^ swizzle(r), so that
+//           the 16 lanes that read one chunk of 16 rows meet different banks
+//   values  8 runs of 64 lane shares (D/32 bytes): run 4h + i has, lane by lane,
+//           what lane (c, g) needs of token 16h + 4g + i
+//   scales  the aligned words with a token's scale bytes: 32 of the keys, 32 of
+//           the values (twice for D = 256, whose heads have two words)
+template <int D>
+struct Stage {
+    static constexpr int kChunks = D / 32;
+    static constexpr int kKeys = 16 * D, kValues = 16 * D, kWords = D == 256 ? 2 : 1;
+    static constexpr int kBytes = kKeys + kValues + kWords * 256;
+    static constexpr int kCopies = D == 64 ? 3 : D == 128 ? 5 : 10;      // instructions to fill it
+    __device__ static constexpr int swizzle(int row) { return (row * kChunks / 16) & (kChunks - 1); }
+};
+constexpr int kStages = 3;                 // two tiles in flight behind the one in use
+
+// Until at most kLeft of the wave's copies are outstanding.
+template <int kLeft>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
+}
+// LDS reads issued so far have returned: their stage may be copied into.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// A lane's part in the copies and in the reads.
+template <int D>
+struct Lane {
+    uint32_t key[D == 256 ? 2 : 1], value;                // offsets of its chunks within 16 rows
+    const uint8_t* scale;                                 // its token's first scale word, in row 0
+    uint32_t read_key, read_value, read_ks, read_vs;      // LDS offsets
+    uint32_t kturn, vturn[4];                             // turns that bring a scale byte into place
 };
 template <int D>
-__device__ __forceinline__ Offsets offsets_of(const TreeArgs& a, int head, int c, int g) {
-    Offsets o;
-    o.k = c * a.code_row + head * (D / 2) + g * (D / 8);
-    o.ks = c * a.scale_row + head * (D / 32) + (D == 64 ? g / 2 : D == 128 ? g : 2 * g);
+__device__ __forceinline__ Lane<D> lane_of(const TreeArgs& a, int head, int lane) {
+    using S = Stage<D>;
+    constexpr int kC = S::kChunks;
+    const int c = lane & 15, g = lane >> 4, col = head * (D / 2), scol = head * (D / 32);
+    Lane<D> o;
+#pragma unroll
+    for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
+        const int row = (i * 64 + lane) / kC % 16;
+        o.key[i] = row * a.code_row + col + ((lane % kC) ^ S::swizzle(row)) * 16;
+    }
+    {
+        const int share = lane * 16 / (D / 32);           // the lane whose share this chunk starts with
+        const int run = share / 64, of = share % 64;      // run 4h + i; D = 64: also h
+        o.value = (4 * (of / 16) + run % 4) * a.code_row + col + of % 16 * (D / 32);
+    }
+    const int first = c * a.scale_row + scol;
+    o.scale = (lane < 32 ? a.ks : a.vs) + (first & ~3);
+    o.read_key = D == 64 ? (c * kC + ((g / 2) ^ S::swizzle(c))) * 16 + g % 2 * 8
+                         : (c * kC + ((D == 128 ? g : 2 * g) ^ S::swizzle(c))) * 16;
+    o.read_value = S::kKeys + lane * (D / 32);
+    o.read_ks = S::kKeys + S::kValues + (D == 256 ? g / 2 * 256 : 0) + c * 4;
+    o.read_vs = S::kKeys + S::kValues + (D == 256 ? c / 8 * 256 : 0) + 128 + 4 * g * 4;
+    const int kblock = D == 64 ? g / 2 : D == 128 ? g : 2 * g;
+    o.kturn = (8 * ((first + kblock) & 3) + 9) & 31;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        o.v[j] = (4 * g + j) * a.code_row + head * (D / 2) + c * (D / 32);
-        o.vs[j] = (4 * g + j) * a.scale_row + head * (D / 32) + c * (D / 16) / 32;
+        const int byte = (4 * g + j) * a.scale_row + scol + c * (D / 16) / 32;
+        // Rows of 4 bytes or more a head keep the byte's place in its word.
+        o.vturn[j] = D >= 128 && j ? o.vturn[0] : (8 * (byte & 3) + 9) & 31;
     }
     return o;
 }
 
-// Global memory at a uniform address, kept in scalar registers: else its sum with
-// a lane's offset is formed per lane and load, in 64-bit vector arithmetic.
-#define FP4_GLOBAL __attribute__((address_space(1)))
-typedef const FP4_GLOBAL uint8_t* gbytes;
-__device__ __forceinline__ gbytes scalar_base(const uint8_t* p) {
-    gbytes g = (gbytes)p;
-    asm("" : "+s"(g));
-    return g;
-}
-// One load at base + offset + imm.  The offset is renewed here so that its widening
-// to 64 bits stays beside the load, where the load takes it as a 32-bit register.
-template <typename T>
-__device__ __forceinline__ T load_at(gbytes base, uint32_t offset, int imm = 0) {
-    asm volatile("" : "+v"(offset));
-    return *(const FP4_GLOBAL T*)(base + offset + imm);
-}
-
+// Starts the copies of a tile into the stage at lds (global memory to LDS, lane
+// l's 16 or 4 bytes to M0 + offset + l * size); awaited by wait_copies.  Halves
+// without a page read row 0 on (a row of the pool; hidden later).  The copies of a
+// tile are one asm block behind one write of M0 (which needs a wait state); the
+// instruction's offset, -4096 to 4095, counts on the global side as well, so each
+// address is given less it.
 template <int D>
-__device__ __forceinline__ void load_tile(Raw<D>& r, const TreeArgs& a, const Place& p, const Offsets& o) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t row = max(p.row[h], 0);                 // any row of the pool: masked later
-        const gbytes kc = scalar_base(a.kc + row * a.code_row), ks = scalar_base(a.ks + row * a.scale_row);
-        const gbytes vc = scalar_base(a.vc + row * a.code_row), vs = scalar_base(a.vs + row * a.scale_row);
-        if constexpr (D == 64) {
-            const u32x2 x = load_at<u32x2>(kc, o.k);
-            r.k[h][0] = x[0], r.k[h][1] = x[1];
+__device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, const Lane<D>& o, int lane, uint32_t lds) {
+    const int row0 = max(p.row[0], 0), row1 = max(p.row[1], 0);
+    const uint8_t* scale = o.scale + (uint64_t)(uint32_t)(lane & 16 ? row1 : row0) * (uint32_t)a.scale_row;
+    if constexpr (D == 64) {                              // both halves in one instruction
+        const uint64_t at = (uint64_t)(uint32_t)(lane & 32 ? row1 : row0) * (uint32_t)a.code_row;
+        asm volatile(
+            "s_waitcnt lgkmcnt(0)\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %0, off\n\t"
+            "global_load_lds_dwordx4 %1, off offset:1024\n\t"
+            "global_load_lds_dword %2, off offset:2048" ::"v"(a.kc + at + o.key[0]),
+            "v"(a.vc + at + o.value - 1024), "v"(scale - 2048), "s"(lds)
+            : "memory", "m0");
+    } else {
+        const int64_t at0 = (int64_t)row0 * a.code_row, at1 = (int64_t)row1 * a.code_row;
+        if constexpr (D == 128) {
+            asm volatile(
+                "s_waitcnt lgkmcnt(0)\n\ts_mov_b32 m0, %7\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, %2 offset:-1024\n\t"
+                "global_load_lds_dwordx4 %0, %3\n\t"
+                "global_load_lds_dwordx4 %1, %4 offset:1024\n\t"
+                "global_load_lds_dwordx4 %1, %5 offset:2048\n\t"
+                "global_load_lds_dword %6, off offset:3072" ::"v"(o.key[0]),
+                "v"(o.value), "s"(a.kc + at0 + 1024), "s"(a.kc + at1), "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048),
+                "v"(scale - 3072), "s"(lds + 1024)
+                : "memory", "m0");
         } else {
-#pragma unroll
-            for (int i = 0; i < D / 128; ++i) {
-                const u32x4 x = load_at<u32x4>(kc, o.k, 16 * i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) r.k[h][4 * i + j] = x[j];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < Raw<D>::kKS; ++i) r.ks[h][i] = load_at<uint8_t>(ks, o.ks, i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (D == 64) {
-                r.v[4 * h + j][0] = load_at<uint16_t>(vc, o.v[j]);
-            } else if constexpr (D == 128) {
-                r.v[4 * h + j][0] = load_at<uint32_t>(vc, o.v[j]);
-            } else {
-                const u32x2 y = load_at<u32x2>(vc, o.v[j]);
-                r.v[4 * h + j][0] = y[0], r.v[4 * h + j][1] = y[1];
-            }
-            r.vs[4 * h + j] = load_at<uint8_t>(vs, o.vs[j]);
+            const int64_t two = 2 * (int64_t)a.code_row;
+            asm volatile(
+                "s_waitcnt lgkmcnt(0)\n\ts_mov_b32 m0, %6\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, %2\n\t"
+                "global_load_lds_dwordx4 %1, %3 offset:1024\n\t"
+                "global_load_lds_dwordx4 %0, %4 offset:2048\n\t"
+                "global_load_lds_dwordx4 %1, %5 offset:3072" ::"v"(o.key[0]),
+                "v"(o.key[1]), "s"(a.kc + at0), "s"(a.kc + at0 - 1024), "s"(a.kc + at1 - 2048), "s"(a.kc + at1 - 3072), "s"(lds)
+                : "memory", "m0");
+            asm volatile(
+                "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, %1 offset:-4096\n\t"
+                "global_load_lds_dwordx4 %0, %2 offset:-3072\n\t"
+                "global_load_lds_dwordx4 %0, %3 offset:-2048\n\t"
+                "global_load_lds_dwordx4 %0, %4 offset:-1024\n\t"
+                "global_load_lds_dword %5, off\n\t"
+                "global_load_lds_dword %7, off offset:256" ::"v"(o.value),
+                "s"(a.vc + at0 + 4096), "s"(a.vc + at0 + two + 3072), "s"(a.vc + at1 + 2048), "s"(a.vc + at1 + two + 1024),
+                "v"(scale), "s"(lds + 8192), "v"(scale + 4 - 256)
+                : "memory", "m0");
         }
     }
 }
@@ -240,7 +294,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
     const int head = __builtin_amdgcn_readfirstlane(unit % a.kv_heads);
     const int r0 = __builtin_amdgcn_readfirstlane(unit / a.kv_heads) * 16 * NR;
 
-    const Offsets offsets = offsets_of<D>(a, head, c, g);
+    using S = Stage<D>;
+    __shared__ __attribute__((aligned(16))) uint8_t staging[kWaves][kStages * S::kBytes];
+    const uint8_t* mine = staging[threadIdx.x >> 6];
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)mine);
+    const Lane<D> own = lane_of<D>(a, head, lane);
     const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
     if ((int64_t)blockIdx.x >= ranges || total == 0) return;
     const int64_t lo = scalar(blockIdx.x * total / ranges), hi = scalar((blockIdx.x + 1) * total / ranges);
@@ -294,10 +352,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
         }
 
         v4f o[NR][kOut];
-        float m[NR], sum[NR];
+        float m[NR];
+        v4f sum[NR];                                          // of the rounded weights, all four alike
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            m[n] = kNone, sum[n] = 0.f;
+            m[n] = kFloor, sum[n] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kOut; ++i) o[n][i] = v4f{0.f, 0.f, 0.f, 0.f};
         }
@@ -309,34 +368,56 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
         int pages = 0, first_page = page_i - 64;
         const int width = (int)a.max_pages;
         const uint32_t pool = (uint32_t)a.num_pages;
+        const bool paired = a.page_size % kTile == 0;         // a tile's halves lie on one page
+        auto row_of = [&]() {
+            if (page_i >= first_page + 64) {
+                first_page = page_i;
+                const int i = page_i + lane;
+                pages = table[min(i, width - 1)];
+                if (i >= width) pages = -1;
+            }
+            const int page = __builtin_amdgcn_readlane(pages, page_i - first_page);
+            return (uint32_t)page < pool ? page * a.page_size + off : -1;
+        };
+        auto advance = [&](int by) {
+            off += by;
+            const int wrap = off == a.page_size;
+            off = wrap ? 0 : off;
+            page_i += wrap;
+        };
         auto place = [&]() {
             Place p;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (page_i >= first_page + 64) {
-                    first_page = page_i;
-                    const int i = page_i + lane;
-                    pages = table[min(i, width - 1)];
-                    if (i >= width) pages = -1;
-                }
-                const int page = __builtin_amdgcn_readlane(pages, page_i - first_page);
-                p.row[h] = (uint32_t)page < pool ? page * a.page_size + off : -1;
-                off += 16;
-                const int wrap = off == a.page_size;
-                off = wrap ? 0 : off;
-                page_i += wrap;
+            p.row[0] = row_of();
+            if (paired) {
+                p.row[1] = p.row[0] < 0 ? -1 : p.row[0] + 16;
+                advance(32);
+            } else {
+                advance(16);
+                p.row[1] = row_of();
+                advance(16);
             }
             return p;
         };
-        Raw<D> raw[2];                                        // of this tile and the next, in turn
-        Place here{}, ahead{};
-        if (seen > 0) {
-            here = place(), ahead = place();
-            load_tile<D>(raw[0], a, here, offsets);
-        }
-        auto step = [&](int t, Raw<D>& cur, Raw<D>& next) {
-            if (t + 1 < t1) load_tile<D>(next, a, ahead, offsets);
-            const Place later = place();
+        const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+        auto compute = [&](int t, const Place& here, uint32_t stage) {
+            const uint8_t* lk = mine + stage + own.read_key;
+            uint32_t kw[2][D / 32], kscale[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (D == 64) {
+                    const u32x2 x = *reinterpret_cast<const u32x2*>(lk + h * 16 * S::kChunks * 16);
+                    kw[h][0] = x[0], kw[h][1] = x[1];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const uint32_t at = i ? (own.read_key ^ 16) - own.read_key : 0;     // chunk 2g + 1 beside 2g
+                        const u32x4 x = *reinterpret_cast<const u32x4*>(lk + (int32_t)at + h * 16 * S::kChunks * 16);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) kw[h][4 * i + w] = x[w];
+                    }
+                }
+                kscale[h] = *reinterpret_cast<const uint32_t*>(mine + stage + own.read_ks + 64 * h);
+            }
             const int pos0 = t * kTile;
             const bool edge = pos0 + kTile > len || here.row[0] < 0 || here.row[1] < 0;     // some token is hidden
             v4f s[NR][2];
@@ -346,20 +427,23 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
                 for (int n = 0; n < NR; ++n) s[n][h] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    const float sc = scale_of(cur.ks[h][D == 256 ? i / 4 : 0]);
-                    const bf16x8 k = __builtin_bit_cast(bf16x8, widen8(cur.k[h][i], sc));
+                    const float sc = scale_of(kscale[h], own.kturn + (D == 256 ? 8 * (i / 4) : 0));
+                    const bf16x8 k = __builtin_bit_cast(bf16x8, widen8(kw[h][i], sc));
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
                         s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, q[n][i]), s[n][h],
                                                                           0, 0, 0);
                 }
             }
+            u32x4 vscale[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vscale[h] = *reinterpret_cast<const u32x4*>(mine + stage + own.read_vs + 64 * h);
             if (edge) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int pos = pos0 + 16 * (j / 4) + 4 * g + j % 4, d = pos - len;
                     const bool there = (pos < seen) & (here.row[j / 4] >= 0);
-                    cur.vs[j] = there ? cur.vs[j] : 127;          // whatever lies there, finite
+                    vscale[j / 4][j % 4] = there ? vscale[j / 4][j % 4] : kOnes;      // whatever lies there, finite
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         const bool see = there & ((d < 0) | ((uint32_t)(vis[n] >> (d & 63)) & 1u));
@@ -367,43 +451,61 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
                     }
                 }
             }
-            bf16x8 p[NR];
+            float top[NR];
+            bool rises = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                float x[8];
+                top[n] = s[n][0][0];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = s[n][j / 4][j % 4];
-                float top = x[0];
+                for (int j = 1; j < 8; ++j) top[n] = fmaxf(top[n], s[n][j / 4][j % 4]);
+                rises |= top[n] * a.scale2 > m[n] + kSlack;
+            }
+            if (__any(rises)) {
 #pragma unroll
-                for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-                top *= a.scale2;
-                if (__any(top > m[n] + kSlack)) {
-                    top = fmaxf(top, __shfl_xor(top, 16, 64));
-                    top = fmaxf(top, __shfl_xor(top, 32, 64));
-                    const float up = fmaxf(m[n], top);
-                    const float alpha = up == m[n] ? 1.0f : exp2_hw(m[n] - up);
+                for (int n = 0; n < NR; ++n) {
+                    float x = top[n] * a.scale2;
+                    x = fmaxf(x, __shfl_xor(x, 16, 64));
+                    x = fmaxf(x, __shfl_xor(x, 32, 64));
+                    const float up = fmaxf(m[n], x), alpha = exp2_hw(m[n] - up);
                     m[n] = up;
                     sum[n] *= alpha;
 #pragma unroll
                     for (int i = 0; i < kOut; ++i) o[n][i] *= alpha;
                 }
-                const float ref = m[n] == kNone ? 0.0f : m[n];
+            }
+            bf16x8 p[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
                 u32x4 w;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p0 = exp2_hw(fmaf(x[2 * j], a.scale2, -ref)), p1 = exp2_hw(fmaf(x[2 * j + 1], a.scale2, -ref));
-                    sum[n] += p0 + p1;
-                    w[j] = pack2(p0, p1);
-                }
+                for (int j = 0; j < 4; ++j)
+                    w[j] = pack2(exp2_hw(fmaf(s[n][j / 2][2 * j % 4], a.scale2, -m[n])),
+                                 exp2_hw(fmaf(s[n][j / 2][2 * j % 4 + 1], a.scale2, -m[n])));
                 p[n] = __builtin_bit_cast(bf16x8, w);
+                sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n], sum[n], 0, 0, 0);
             }
             // V, a byte (two values) of the lane's 8 tokens at a time: widened, then
             // tokens paired per value.
+            float scale[8];
+            uint32_t vw[8][D == 256 ? 2 : 1];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                scale[j] = scale_of(vscale[j / 4][j % 4], own.vturn[j % 4]);
+                const uint8_t* x = mine + stage + own.read_value + j * 2 * D;
+                if constexpr (D == 64) {
+                    vw[j][0] = *reinterpret_cast<const uint16_t*>(x);
+                } else if constexpr (D == 128) {
+                    vw[j][0] = *reinterpret_cast<const uint32_t*>(x);
+                } else {
+                    const u32x2 y = *reinterpret_cast<const u32x2*>(x);
+                    vw[j][0] = y[0], vw[j][1] = y[1];
+                }
+            }
             auto values = [&](auto byte_tag) {
                 constexpr int kB = decltype(byte_tag)::value;
                 uint32_t w[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = widen<kB % 4>(cur.v[j][kB / 4], scale_of(cur.vs[j]));
+                for (int j = 0; j < 8; ++j) w[j] = widen<kB % 4>(vw[j][kB / 4], scale[j]);
                 const u32x4 lo = {pair<false>(w[0], w[1]), pair<false>(w[2], w[3]), pair<false>(w[4], w[5]), pair<false>(w[6], w[7])};
                 const u32x4 hi = {pair<true>(w[0], w[1]), pair<true>(w[2], w[3]), pair<true>(w[4], w[5]), pair<true>(w[6], w[7])};
 #pragma unroll
@@ -415,20 +517,40 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
             values(Int<0>()), values(Int<1>());
             if constexpr (D >= 128) values(Int<2>()), values(Int<3>());
             if constexpr (D == 256) values(Int<4>()), values(Int<5>()), values(Int<6>()), values(Int<7>());
-            here = ahead;
-            ahead = later;
         };
-        for (int t = t0; t < t1 && seen > 0; t += 2) {
-            step(t, raw[0], raw[1]);
-            if (t + 1 < t1) step(t + 1, raw[1], raw[0]);
+        if (seen > 0) {
+            // Three stages and the places of their tiles take turns, by unrolling.
+            Place at_stage[kStages];
+            auto start = [&](int k) {
+                at_stage[k] = place();
+                copy_tile<D>(a, at_stage[k], own, lane, lds + k * S::kBytes);
+            };
+            auto turn = [&](int t, auto tag) {
+                constexpr int k = decltype(tag)::value;
+                if (t + 2 < t1) {
+                    start((k + 2) % kStages);
+                    wait_copies<2 * S::kCopies>();
+                } else if (t + 1 < t1) {
+                    wait_copies<S::kCopies>();
+                } else {
+                    wait_copies<0>();
+                }
+                compute(t, at_stage[k], k * S::kBytes);
+            };
+            start(0);
+            if (t0 + 1 < t1) start(1);
+            for (int t = t0; t < t1; t += 3) {
+                turn(t, Int<0>());
+                if (t + 1 < t1) turn(t + 1, Int<1>());
+                if (t + 2 < t1) turn(t + 2, Int<2>());
+            }
+            wait_lds();                                       // before the next sequence's copies
         }
 
         const bool whole = t0 == 0 && t1 == tiles;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            float l = sum[n];
-            l += __shfl_xor(l, 16, 64);
-            l += __shfl_xor(l, 32, 64);
+            const float l = sum[n][0];
             const int row = r0 + 16 * n + c, t = row / a.group;
             if (t >= nd) continue;
             if (whole) {
@@ -490,14 +612,14 @@ __global__ __launch_bounds__(kBlock) void attn_tree_join_kernel(const TreeArgs a
     for (int r0 = blockIdx.x * kRows; r0 < all_rows; r0 += gridDim.x * kRows) {
         const int r = r0 + team / kTeams;
         const bool live = r < all_rows && r % a.rows / a.group < nd;
-        float m = kNone, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float m = kFloor, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         for (int x0 = first + part; live && x0 <= last; x0 += kBatch * kTeams) {
             float2 s[kBatch];
             float4 o[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int x = x0 + k * kTeams;
-                s[k] = make_float2(kNone, 0.f);
+                s[k] = make_float2(kFloor, 0.f);
                 o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (x <= last) {
                     const int64_t at = (int64_t)(x == first ? first_slot : 2 * x) * all_rows + r;
@@ -508,14 +630,14 @@ __global__ __launch_bounds__(kBlock) void attn_tree_join_kernel(const TreeArgs a
             float top = m;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
-            const float ref = top == kNone ? 0.f : top, keep = exp2_hw(m - ref);
+            const float keep = exp2_hw(m - top);
             m = top;
             l *= keep;
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] *= keep;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const float e = exp2_hw(s[k].x - ref);
+                const float e = exp2_hw(s[k].x - top);
                 l += s[k].y * e;
                 acc[0] += o[k].x * e, acc[1] += o[k].y * e, acc[2] += o[k].z * e, acc[3] += o[k].w * e;
             }
@@ -525,14 +647,13 @@ __global__ __launch_bounds__(kBlock) void attn_tree_join_kernel(const TreeArgs a
             if (l4 == 0) stats[team] = make_float2(m, l);
             __syncthreads();
             if (part == 0) {
-                float top = kNone;
+                float top = kFloor;
 #pragma unroll
                 for (int k = 0; k < kTeams; ++k) top = fmaxf(top, stats[team + k].x);
-                const float ref = top == kNone ? 0.f : top;
                 l = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
 #pragma unroll
                 for (int k = 0; k < kTeams; ++k) {
-                    const float e = exp2_hw(stats[team + k].x - ref);
+                    const float e = exp2_hw(stats[team + k].x - top);
                     const float4 o = sums[threadIdx.x + k * kLanes];
                     l += stats[team + k].y * e;
                     acc[0] += o.x * e, acc[1] += o.y * e, acc[2] += o.z * e, acc[3] += o.w * e;

@@ -3,7 +3,9 @@
 A value o = sum p v with the total magnitude S = sum p |v| (p the softmax
 weights) is off by at most
   2^-8 |o|        its rounding to bf16,
-  2^-8 S          every weight's rounding to bf16 before the second product,
+  2^-8 (S + |o|)  every weight's rounding to bf16 before the second product; the
+                  same rounded weights are summed for the division, so a weight
+                  off by d_j (at most 2^-8 of it) gives sum p_j d_j (v_j - o),
   2 e S           the scores' error e, in the weights and in their sum: a score
                   is a sum of d products of magnitude at most |q| |k| (Cauchy) in
                   fp32, scaled by one product: e = (d + 4) 2^-24 scale |q| |k|,
@@ -26,7 +28,7 @@ from oracle import formats as FM
 
 def tolerance(ref, size, d, n, scale, q_norm, k_norm, v_max):
     e = (d + 4) * 2.0 ** -24 * abs(scale) * q_norm * k_norm + 2.0 ** -22
-    return 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e + (n / 8 + 64) * 2.0 ** -24) * size + n * 2.0 ** -118 * v_max
+    return 2.0 ** -7 * np.abs(ref) + (2.0 ** -8 + 2 * e + (n / 8 + 64) * 2.0 ** -24) * size + n * 2.0 ** -118 * v_max
 
 
 def check(out, ref, size, d, n, scale, q_norm, k_norm, v_max):
