@@ -40,9 +40,8 @@ namespace fp4 {
 namespace {
 
 constexpr int kTile = 32;                  // tokens per step
-constexpr int kWaves = 4;                  // at most, per workgroup
 constexpr int kMinTiles = 4;               // tiles per range below which fewer ranges are used
-constexpr int kWorkgroups = 512;           // two per CU: two waves per SIMD
+constexpr int kGridWaves = 2048;           // two per SIMD
 constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
 constexpr float kNone = -__builtin_inff();   // score of a hidden token
 constexpr float kFloor = -3e38f;           // reference of a row that has seen nothing
@@ -151,23 +150,31 @@ struct Place {
     int row[2];
 };
 
-// One wave's staging of a tile in LDS.  Rows are read from global memory in
-// 16-byte chunks, neighbouring lanes in neighbouring chunks of a row, straight
-// into LDS: the vector memory pipe is bound by requests, and loads in the matrix
-// core's layout (a lane its own row) would cost it several times as many.
-//   keys    32 rows of kChunks chunks; chunk x of row r at x ^ swizzle(r), so that
-//           the 16 lanes that read one chunk of 16 rows meet different banks
-//   values  8 runs of 64 lane shares (D/32 bytes): run 4h + i has, lane by lane,
-//           what lane (c, g) needs of token 16h + 4g + i
-//   scales  the aligned words with a token's scale bytes: 32 of the keys, 32 of
-//           the values (twice for D = 256, whose heads have two words)
-template <int D>
+// A workgroup's staging of a tile in LDS: HW neighbouring heads of 32 tokens, one
+// wave for each.  Rows are read from global memory in 16-byte chunks, neighbouring
+// lanes in neighbouring chunks of the heads' part of a row, straight into LDS: the
+// memory behind is bound by requests, and whole 128-byte lines make the fewest (a
+// head's part of a row alone is half a line at D = 128).  Every wave copies 1/HW
+// of the rows, of all heads, into a region of its own:
+//   keys    32 rows of HW * D/32 chunks; chunk x of a row at x ^ key_turn(row), so
+//           that the 16 lanes that read one chunk of 16 rows meet different banks
+//   values  8 runs of 4 rows: run 4h + i has tokens 16h + 4g + i, g = 0 .. 3, which
+//           the four lane groups read together; head x of a row at x ^ value_turn(g),
+//           which brings their parts into different banks
+//   scales  the aligned words with a token's scale bytes, one plane of 32 key and
+//           32 value words for each word of a token
+template <int D, int HW>
 struct Stage {
-    static constexpr int kChunks = D / 32;
-    static constexpr int kKeys = 16 * D, kValues = 16 * D, kWords = D == 256 ? 2 : 1;
+    static constexpr int kChunks = D / 32, kRow = HW * kChunks;          // chunks of a head, of a row
+    static constexpr int kKeys = 16 * D, kValues = 16 * D, kWords = D == 256 ? 2 : 1;   // bytes, planes of a wave
     static constexpr int kBytes = kKeys + kValues + kWords * 256;
-    static constexpr int kCopies = D == 64 ? 3 : D == 128 ? 5 : 10;      // instructions to fill it
-    __device__ static constexpr int swizzle(int row) { return (row * kChunks / 16) & (kChunks - 1); }
+    static constexpr int kPlanes = HW * D >= 128 ? HW * D / 128 : 1;
+    static constexpr int kItems = kChunks / 2;                           // copies of keys, and of values, per wave
+    static constexpr int kCopies = 2 * kItems + kWords;
+    __device__ static constexpr int key_turn(int row) {
+        return kRow < 16 ? (row * kRow / 16) & (kRow - 1) : row & (kRow - 1) & 15;
+    }
+    __device__ static constexpr int value_turn(int g) { return HW >= 4 ? g : (g * HW) >> 2; }
 };
 constexpr int kStages = 3;                 // two tiles in flight behind the one in use
 
@@ -176,103 +183,117 @@ template <int kLeft>
 __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
 }
-// LDS reads issued so far have returned: their stage may be copied into.
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// LDS reads issued so far have returned, in all waves of the workgroup.
+template <int HW>
+__device__ __forceinline__ void meet() {
+    if (HW > 1)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
 
 // A lane's part in the copies and in the reads.
-template <int D>
+template <int D, int HW>
 struct Lane {
-    uint32_t key[D == 256 ? 2 : 1], value;                // offsets of its chunks within 16 rows
-    const uint8_t* scale;                                 // its token's first scale word, in row 0
+    static constexpr int kItems = Stage<D, HW>::kItems;
+    uint32_t key[kItems], value[kItems];                  // offsets of its chunks from 16 rows' first head
+    const uint8_t* scale;                                 // its token's scale word, in row 0
     uint32_t read_key, read_value, read_ks, read_vs;      // LDS offsets
     uint32_t kturn, vturn[4];                             // turns that bring a scale byte into place
 };
-template <int D>
-__device__ __forceinline__ Lane<D> lane_of(const TreeArgs& a, int head, int lane) {
-    using S = Stage<D>;
-    constexpr int kC = S::kChunks;
-    const int c = lane & 15, g = lane >> 4, col = head * (D / 2), scol = head * (D / 32);
-    Lane<D> o;
+template <int D, int HW>
+__device__ __forceinline__ Lane<D, HW> lane_of(const TreeArgs& a, int head0, int wave, int lane) {
+    using S = Stage<D, HW>;
+    constexpr int kRegion = kStages * S::kBytes, kShare = D / 32;        // a lane's bytes of a value row
+    const int c = lane & 15, g = lane >> 4, first = head0 * (D / 32);
+    Lane<D, HW> o;
 #pragma unroll
-    for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
-        const int row = (i * 64 + lane) / kC % 16;
-        o.key[i] = row * a.code_row + col + ((lane % kC) ^ S::swizzle(row)) * 16;
+    for (int k = 0; k < S::kItems; ++k) {
+        const int slot = (wave * S::kItems + k) * 64 + lane, row = slot / S::kRow, at = slot % S::kRow;
+        o.key[k] = row % 16 * a.code_row + head0 * (D / 2) + (at ^ S::key_turn(row % 16)) * 16;
+        const int vg = row % 4, token = 4 * vg + row / 4 % 4;            // row: run * 4 + g
+        o.value[k] = token * a.code_row + (head0 + (at / S::kChunks ^ S::value_turn(vg))) * (D / 2) + at % S::kChunks * 16;
     }
+    const int row0 = c * a.scale_row + first;                            // of its token's scale bytes
+    const int plane = wave * S::kWords % S::kPlanes;
+    o.scale = (lane < 32 ? a.ks : a.vs) + (row0 & ~3) + 4 * plane;
     {
-        const int share = lane * 16 / (D / 32);           // the lane whose share this chunk starts with
-        const int run = share / 64, of = share % 64;      // run 4h + i; D = 64: also h
-        o.value = (4 * (of / 16) + run % 4) * a.code_row + col + of % 16 * (D / 32);
+        const int at = (wave * S::kChunks + (D == 64 ? g / 2 : D == 128 ? g : 2 * g)) ^ S::key_turn(c);
+        o.read_key = c / (32 / HW) * kRegion + (c % (32 / HW) * S::kRow + at) * 16 + (D == 64 ? g % 2 * 8 : 0);
     }
-    const int first = c * a.scale_row + scol;
-    o.scale = (lane < 32 ? a.ks : a.vs) + (first & ~3);
-    o.read_key = D == 64 ? (c * kC + ((g / 2) ^ S::swizzle(c))) * 16 + g % 2 * 8
-                         : (c * kC + ((D == 128 ? g : 2 * g) ^ S::swizzle(c))) * 16;
-    o.read_value = S::kKeys + lane * (D / 32);
-    o.read_ks = S::kKeys + S::kValues + (D == 256 ? g / 2 * 256 : 0) + c * 4;
-    o.read_vs = S::kKeys + S::kValues + (D == 256 ? c / 8 * 256 : 0) + 128 + 4 * g * 4;
-    const int kblock = D == 64 ? g / 2 : D == 128 ? g : 2 * g;
-    o.kturn = (8 * ((first + kblock) & 3) + 9) & 31;
+    o.read_value = S::kKeys + (g * S::kRow + (wave ^ S::value_turn(g)) * S::kChunks) * 16 + c * kShare;
+    const int kblock = wave * (D / 32) + (D == 64 ? g / 2 : D == 128 ? g : 2 * g);
+    const int vblock = wave * (D / 32) + c * (D / 16) / 32;
+    auto plane_of = [&](int block) {                      // LDS offset of the plane with a head's scale block
+        const int p = ((first & 3) + block) / 4;
+        return p / S::kWords * kRegion + S::kKeys + S::kValues + p % S::kWords * 256;
+    };
+    // Words start at the row's aligned word; only D = 64 with an odd number of heads
+    // has rows that do not start with one.
+    o.read_ks = (D == 64 && HW == 1 ? S::kKeys + S::kValues : plane_of(kblock)) + c * 4;
+    o.read_vs = (D == 64 && HW == 1 ? S::kKeys + S::kValues : plane_of(vblock)) + 128 + 4 * g * 4;
+    o.kturn = (8 * ((row0 + kblock) & 3) + 9) & 31;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int byte = (4 * g + j) * a.scale_row + scol + c * (D / 16) / 32;
-        // Rows of 4 bytes or more a head keep the byte's place in its word.
-        o.vturn[j] = D >= 128 && j ? o.vturn[0] : (8 * (byte & 3) + 9) & 31;
-    }
+    for (int j = 0; j < 4; ++j)
+        o.vturn[j] = D == 64 && HW == 1 ? (8 * (((4 * g + j) * a.scale_row + first + vblock) & 3) + 9) & 31
+                                        : (8 * ((first + vblock) & 3) + 9) & 31;
     return o;
 }
 
-// Starts the copies of a tile into the stage at lds (global memory to LDS, lane
-// l's 16 or 4 bytes to M0 + offset + l * size); awaited by wait_copies.  Halves
-// without a page read row 0 on (a row of the pool; hidden later).  The copies of a
-// tile are one asm block behind one write of M0 (which needs a wait state); the
-// instruction's offset, -4096 to 4095, counts on the global side as well, so each
-// address is given less it.
-template <int D>
-__device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, const Lane<D>& o, int lane, uint32_t lds) {
-    const int row0 = max(p.row[0], 0), row1 = max(p.row[1], 0);
+// Starts a wave's copies of a tile into its region of the stage at lds (global
+// memory to LDS, lane l's 16 or 4 bytes to M0 + offset + l * size); awaited by
+// wait_copies.  Halves without a page read row 0 on (a row of the pool; hidden
+// later).  A wave's copies are one asm block behind one write of M0 (which needs a
+// wait state); the instruction's offset, -4096 to 4095, counts on the global side
+// as well, so each address is given less it.
+template <int D, int HW>
+__device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, const Lane<D, HW>& o, int wave, int lane,
+                                          uint32_t lds) {
+    const int row0 = max(p.row[0], 0), row1 = max(p.row[1], 0), mine = HW > 1 && wave < HW / 2 ? row0 : row1;
     const uint8_t* scale = o.scale + (uint64_t)(uint32_t)(lane & 16 ? row1 : row0) * (uint32_t)a.scale_row;
-    if constexpr (D == 64) {                              // both halves in one instruction
-        const uint64_t at = (uint64_t)(uint32_t)(lane & 32 ? row1 : row0) * (uint32_t)a.code_row;
+    if constexpr (D == 64) {                              // HW = 1: both halves in one instruction
+        const uint64_t at = (uint64_t)(uint32_t)(HW == 1 && !(lane & 32) ? row0 : mine) * (uint32_t)a.code_row;
         asm volatile(
-            "s_waitcnt lgkmcnt(0)\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+            "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
             "global_load_lds_dwordx4 %0, off\n\t"
             "global_load_lds_dwordx4 %1, off offset:1024\n\t"
             "global_load_lds_dword %2, off offset:2048" ::"v"(a.kc + at + o.key[0]),
-            "v"(a.vc + at + o.value - 1024), "v"(scale - 2048), "s"(lds)
+            "v"(a.vc + at + o.value[0] - 1024), "v"(scale - 2048), "s"(lds)
             : "memory", "m0");
     } else {
-        const int64_t at0 = (int64_t)row0 * a.code_row, at1 = (int64_t)row1 * a.code_row;
+        // HW = 1: the first half of the copies takes the tile's first half.
+        const int64_t at0 = (int64_t)(HW == 1 ? row0 : mine) * a.code_row, at1 = HW == 1 ? (int64_t)row1 * a.code_row : at0;
         if constexpr (D == 128) {
             asm volatile(
-                "s_waitcnt lgkmcnt(0)\n\ts_mov_b32 m0, %7\n\ts_nop 0\n\t"
-                "global_load_lds_dwordx4 %0, %2 offset:-1024\n\t"
-                "global_load_lds_dwordx4 %0, %3\n\t"
-                "global_load_lds_dwordx4 %1, %4 offset:1024\n\t"
-                "global_load_lds_dwordx4 %1, %5 offset:2048\n\t"
-                "global_load_lds_dword %6, off offset:3072" ::"v"(o.key[0]),
-                "v"(o.value), "s"(a.kc + at0 + 1024), "s"(a.kc + at1), "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048),
-                "v"(scale - 3072), "s"(lds + 1024)
+                "s_mov_b32 m0, %9\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, %4 offset:-1024\n\t"
+                "global_load_lds_dwordx4 %1, %5\n\t"
+                "global_load_lds_dwordx4 %2, %6 offset:1024\n\t"
+                "global_load_lds_dwordx4 %3, %7 offset:2048\n\t"
+                "global_load_lds_dword %8, off offset:3072" ::"v"(o.key[0]),
+                "v"(o.key[1]), "v"(o.value[0]), "v"(o.value[1]), "s"(a.kc + at0 + 1024), "s"(a.kc + at1),
+                "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048), "v"(scale - 3072), "s"(lds + 1024)
                 : "memory", "m0");
         } else {
-            const int64_t two = 2 * (int64_t)a.code_row;
             asm volatile(
-                "s_waitcnt lgkmcnt(0)\n\ts_mov_b32 m0, %6\n\ts_nop 0\n\t"
-                "global_load_lds_dwordx4 %0, %2\n\t"
-                "global_load_lds_dwordx4 %1, %3 offset:1024\n\t"
-                "global_load_lds_dwordx4 %0, %4 offset:2048\n\t"
-                "global_load_lds_dwordx4 %1, %5 offset:3072" ::"v"(o.key[0]),
-                "v"(o.key[1]), "s"(a.kc + at0), "s"(a.kc + at0 - 1024), "s"(a.kc + at1 - 2048), "s"(a.kc + at1 - 3072), "s"(lds)
+                "s_mov_b32 m0, %8\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, %4\n\t"
+                "global_load_lds_dwordx4 %1, %5 offset:1024\n\t"
+                "global_load_lds_dwordx4 %2, %6 offset:2048\n\t"
+                "global_load_lds_dwordx4 %3, %7 offset:3072" ::"v"(o.key[0]),
+                "v"(o.key[1]), "v"(o.key[2]), "v"(o.key[3]), "s"(a.kc + at0), "s"(a.kc + at0 - 1024),
+                "s"(a.kc + at1 - 2048), "s"(a.kc + at1 - 3072), "s"(lds)
                 : "memory", "m0");
             asm volatile(
-                "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
-                "global_load_lds_dwordx4 %0, %1 offset:-4096\n\t"
-                "global_load_lds_dwordx4 %0, %2 offset:-3072\n\t"
-                "global_load_lds_dwordx4 %0, %3 offset:-2048\n\t"
-                "global_load_lds_dwordx4 %0, %4 offset:-1024\n\t"
-                "global_load_lds_dword %5, off\n\t"
-                "global_load_lds_dword %7, off offset:256" ::"v"(o.value),
-                "s"(a.vc + at0 + 4096), "s"(a.vc + at0 + two + 3072), "s"(a.vc + at1 + 2048), "s"(a.vc + at1 + two + 1024),
-                "v"(scale), "s"(lds + 8192), "v"(scale + 4 - 256)
+                "s_mov_b32 m0, %10\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, %4 offset:-4096\n\t"
+                "global_load_lds_dwordx4 %1, %5 offset:-3072\n\t"
+                "global_load_lds_dwordx4 %2, %6 offset:-2048\n\t"
+                "global_load_lds_dwordx4 %3, %7 offset:-1024\n\t"
+                "global_load_lds_dword %8, off\n\t"
+                "global_load_lds_dword %9, off offset:256" ::"v"(o.value[0]),
+                "v"(o.value[1]), "v"(o.value[2]), "v"(o.value[3]), "s"(a.vc + at0 + 4096), "s"(a.vc + at0 + 3072),
+                "s"(a.vc + at1 + 2048), "s"(a.vc + at1 + 1024), "v"(scale), "v"(scale + 4 - 256), "s"(lds + 8192)
                 : "memory", "m0");
         }
     }
@@ -284,21 +305,19 @@ __device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
     return __builtin_amdgcn_perm(b, a, kHigh ? 0x07060302u : 0x05040100u);
 }
 
-template <int D, int NR>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
+template <int D, int NR, int HW>
+__global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
     constexpr int kSteps = D / 32, kOut = D / 16;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const int row_groups = (a.rows + 16 * NR - 1) / (16 * NR);
-    const int unit = __builtin_amdgcn_readfirstlane(blockIdx.y * (blockDim.x >> 6) + (threadIdx.x >> 6));
-    if (unit >= a.kv_heads * row_groups) return;
-    const int head = __builtin_amdgcn_readfirstlane(unit % a.kv_heads);
-    const int r0 = __builtin_amdgcn_readfirstlane(unit / a.kv_heads) * 16 * NR;
-
-    using S = Stage<D>;
-    __shared__ __attribute__((aligned(16))) uint8_t staging[kWaves][kStages * S::kBytes];
-    const uint8_t* mine = staging[threadIdx.x >> 6];
-    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)mine);
-    const Lane<D> own = lane_of<D>(a, head, lane);
+    using S = Stage<D, HW>;
+    constexpr int kRegion = kStages * S::kBytes;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = a.kv_heads / HW;
+    const int head0 = __builtin_amdgcn_readfirstlane(blockIdx.y % groups) * HW, head = head0 + wave;
+    const int r0 = __builtin_amdgcn_readfirstlane(blockIdx.y / groups) * 16 * NR;
+    __shared__ __attribute__((aligned(16))) uint8_t staging[HW * kRegion];
+    const uint32_t lds =
+        __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)staging) + wave * kRegion;
+    const Lane<D, HW> own = lane_of<D, HW>(a, head0, wave, lane);
     const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
     if ((int64_t)blockIdx.x >= ranges || total == 0) return;
     const int64_t lo = scalar(blockIdx.x * total / ranges), hi = scalar((blockIdx.x + 1) * total / ranges);
@@ -361,62 +380,43 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
             for (int i = 0; i < kOut; ++i) o[n][i] = v4f{0.f, 0.f, 0.f, 0.f};
         }
 
-        // Places the next 16 tokens at a time.  The lanes hold 64 page ids of the
-        // row (one load per 64 pages), read by lane when their turn comes.
-        int page_i = __builtin_amdgcn_readfirstlane(t0 * (kTile / 16) / (a.page_size / 16));
-        int off = t0 * kTile - page_i * a.page_size;
-        int pages = 0, first_page = page_i - 64;
-        const int width = (int)a.max_pages;
-        const uint32_t pool = (uint32_t)a.num_pages;
-        const bool paired = a.page_size % kTile == 0;         // a tile's halves lie on one page
-        auto row_of = [&]() {
-            if (page_i >= first_page + 64) {
-                first_page = page_i;
-                const int i = page_i + lane;
-                pages = table[min(i, width - 1)];
-                if (i >= width) pages = -1;
-            }
-            const int page = __builtin_amdgcn_readlane(pages, page_i - first_page);
-            return (uint32_t)page < pool ? page * a.page_size + off : -1;
-        };
-        auto advance = [&](int by) {
-            off += by;
-            const int wrap = off == a.page_size;
-            off = wrap ? 0 : off;
-            page_i += wrap;
-        };
+        // The lanes hold the cache rows of the next 64 halves of tiles (-1: no page),
+        // worked out together once in 32 tiles and read by lane when their turn comes.
+        int half_i = 2 * t0, first_half = half_i - 64, rows = 0;
         auto place = [&]() {
-            Place p;
-            p.row[0] = row_of();
-            if (paired) {
-                p.row[1] = p.row[0] < 0 ? -1 : p.row[0] + 16;
-                advance(32);
-            } else {
-                advance(16);
-                p.row[1] = row_of();
-                advance(16);
+            if (half_i >= first_half + 64) {
+                first_half = half_i;
+                const int at = half_i + lane, per = a.page_size / 16, i = at / per;
+                const int page = table[min(i, (int)a.max_pages - 1)];
+                const bool there = i < a.max_pages && (uint32_t)page < (uint32_t)a.num_pages;
+                rows = there ? page * a.page_size + (at - i * per) * 16 : -1;
             }
+            Place p;
+            p.row[0] = __builtin_amdgcn_readlane(rows, half_i - first_half);
+            p.row[1] = __builtin_amdgcn_readlane(rows, half_i - first_half + 1);
+            half_i += 2;
             return p;
         };
         const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
         auto compute = [&](int t, const Place& here, uint32_t stage) {
-            const uint8_t* lk = mine + stage + own.read_key;
+            const uint8_t* mine = staging + stage;
             uint32_t kw[2][D / 32], kscale[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                // Rows 16 on: HW/2 regions further, or in the only one.
+                constexpr int kHalf = HW == 1 ? 16 * S::kRow * 16 : HW / 2 * kRegion;
                 if constexpr (D == 64) {
-                    const u32x2 x = *reinterpret_cast<const u32x2*>(lk + h * 16 * S::kChunks * 16);
+                    const u32x2 x = *reinterpret_cast<const u32x2*>(mine + own.read_key + h * kHalf);
                     kw[h][0] = x[0], kw[h][1] = x[1];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < D / 128; ++i) {
-                        const uint32_t at = i ? (own.read_key ^ 16) - own.read_key : 0;     // chunk 2g + 1 beside 2g
-                        const u32x4 x = *reinterpret_cast<const u32x4*>(lk + (int32_t)at + h * 16 * S::kChunks * 16);
+                    for (int i = 0; i < D / 128; ++i) {       // chunk 2g + 1 lies beside 2g
+                        const u32x4 x = *reinterpret_cast<const u32x4*>(mine + (own.read_key ^ (16 * i)) + h * kHalf);
 #pragma unroll
                         for (int w = 0; w < 4; ++w) kw[h][4 * i + w] = x[w];
                     }
                 }
-                kscale[h] = *reinterpret_cast<const uint32_t*>(mine + stage + own.read_ks + 64 * h);
+                kscale[h] = *reinterpret_cast<const uint32_t*>(mine + own.read_ks + 64 * h);
             }
             const int pos0 = t * kTile;
             const bool edge = pos0 + kTile > len || here.row[0] < 0 || here.row[1] < 0;     // some token is hidden
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
             }
             u32x4 vscale[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vscale[h] = *reinterpret_cast<const u32x4*>(mine + stage + own.read_vs + 64 * h);
+            for (int h = 0; h < 2; ++h) vscale[h] = *reinterpret_cast<const u32x4*>(mine + own.read_vs + 64 * h);
             if (edge) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -491,7 +491,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 scale[j] = scale_of(vscale[j / 4][j % 4], own.vturn[j % 4]);
-                const uint8_t* x = mine + stage + own.read_value + j * 2 * D;
+                const uint8_t* x = mine + own.read_value + j * HW / 8 * kRegion + j % (8 / HW) * 64 * S::kRow;
                 if constexpr (D == 64) {
                     vw[j][0] = *reinterpret_cast<const uint16_t*>(x);
                 } else if constexpr (D == 128) {
@@ -519,22 +519,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
             if constexpr (D == 256) values(Int<4>()), values(Int<5>()), values(Int<6>()), values(Int<7>());
         };
         if (seen > 0) {
-            // Three stages and the places of their tiles take turns, by unrolling.
+            // Three stages and the places of their tiles take turns, by unrolling.  When
+            // the waves meet, a tile's copies have landed in all regions, and the stage
+            // of the tile before is free for the one after next.
             Place at_stage[kStages];
             auto start = [&](int k) {
                 at_stage[k] = place();
-                copy_tile<D>(a, at_stage[k], own, lane, lds + k * S::kBytes);
+                copy_tile<D, HW>(a, at_stage[k], own, wave, lane, lds + k * S::kBytes);
             };
             auto turn = [&](int t, auto tag) {
                 constexpr int k = decltype(tag)::value;
-                if (t + 2 < t1) {
-                    start((k + 2) % kStages);
-                    wait_copies<2 * S::kCopies>();
-                } else if (t + 1 < t1) {
+                if (t + 1 < t1)
                     wait_copies<S::kCopies>();
-                } else {
+                else
                     wait_copies<0>();
-                }
+                meet<HW>();
+                if (t + 2 < t1) start((k + 2) % kStages);
                 compute(t, at_stage[k], k * S::kBytes);
             };
             start(0);
@@ -544,7 +544,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tree_kerne
                 if (t + 1 < t1) turn(t + 1, Int<1>());
                 if (t + 2 < t1) turn(t + 2, Int<2>());
             }
-            wait_lds();                                       // before the next sequence's copies
+            meet<HW>();                                       // before the next sequence's copies
         }
 
         const bool whole = t0 == 0 && t1 == tiles;
@@ -681,26 +681,23 @@ void launch_join(const TreeArgs& a, hipStream_t s) {
 
 // How the call is laid out, from its shapes alone.
 struct Layout {
-    int nr, waves, columns, ranges;        // row tiles per wave, waves per workgroup, workgroups per range
+    int nr, waves, columns, ranges;        // row tiles per wave, waves (heads) per workgroup, workgroups per range
 };
-Layout layout_of(int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim) {
+Layout layout_of(int drafts, int q_heads, int kv_heads, int head_dim) {
     const int rows = drafts * (q_heads / kv_heads);
     Layout l;
     l.nr = rows > 16 && head_dim <= 128 ? 2 : 1;
-    const int units = kv_heads * ((rows + 16 * l.nr - 1) / (16 * l.nr));
-    l.waves = units < kWaves ? units : kWaves;
-    l.columns = (units + l.waves - 1) / l.waves;
-    int64_t ranges = (int64_t)kWorkgroups * kWaves / ((int64_t)l.columns * l.waves);
+    l.waves = kv_heads % 8 == 0 && head_dim <= 128 ? 8 : kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
+    l.columns = kv_heads / l.waves * ((rows + 16 * l.nr - 1) / (16 * l.nr));
     // a multiple of 8, so that a range's workgroups meet on one XCD
-    ranges = ranges / 8 * 8;
-    l.ranges = (int)(ranges < 8 ? 8 : ranges);
-    (void)batch;
+    const int ranges = kGridWaves / (l.columns * l.waves) / 8 * 8;
+    l.ranges = ranges < 8 ? 8 : ranges;
     return l;
 }
 
-template <int D, int NR>
+template <int D, int NR, int HW>
 hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
-    attn_tree_kernel<D, NR><<<dim3((unsigned)l.ranges, (unsigned)l.columns), 64 * l.waves, 0, s>>>(a);
+    attn_tree_kernel<D, NR, HW><<<dim3((unsigned)l.ranges, (unsigned)l.columns), 64 * HW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // Pieces of a sequence on average: how many teams share a row.
@@ -712,16 +709,24 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
         launch_join<D, 1, 256>(a, s);
     return hipGetLastError();
 }
+template <int D, int NR>
+hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
+    if constexpr (D <= 128) {
+        if (l.waves == 8) return launch<D, NR, 8>(a, l, s);
+    }
+    return l.waves == 4 ? launch<D, NR, 4>(a, l, s) : l.waves == 2 ? launch<D, NR, 2>(a, l, s) : launch<D, NR, 1>(a, l, s);
+}
 
 }  // namespace
 
 size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
-    const Layout l = layout_of(batch, drafts, q_heads, kv_heads, head_dim);
+    (void)batch;
+    const Layout l = layout_of(drafts, q_heads, kv_heads, head_dim);
     return (size_t)2 * l.ranges * q_heads * drafts * (head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
-    const Layout l = layout_of(p.batch, p.drafts, p.q_heads, p.kv_heads, p.head_dim);
+    const Layout l = layout_of(p.drafts, p.q_heads, p.kv_heads, p.head_dim);
     TreeArgs a{};
     a.q = p.q, a.ld_q = p.ld_q, a.out = p.out, a.ld_out = p.ld_out;
     a.kc = p.cache.k_codes, a.ks = p.cache.k_scales, a.vc = p.cache.v_codes, a.vs = p.cache.v_scales;
