@@ -40,7 +40,7 @@ namespace fp4 {
 namespace {
 
 constexpr int kTile = 32;                  // tokens per step
-constexpr int kMinTiles = 4;               // tiles per range below which fewer ranges are used
+constexpr int kMinTiles = 2;               // tiles per range below which fewer ranges are used
 constexpr int kGridWaves = 2048;           // two per SIMD
 constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
 constexpr float kNone = -__builtin_inff();   // score of a hidden token
@@ -67,27 +67,27 @@ struct TreeArgs {
     uint32_t flip;                         // sign bits of Q, set for a negative scale
     uint16_t* out;
     int64_t ld_out;
-    float* part;                           // [2 * ranges][kv_heads][rows][D] sums, then [..][2] (m, sum)
-    int ranges;
+    // Partial results [2 << shift][kv_heads][row tiles]: of 16 rows, the sums as the
+    // lanes hold them ([D/16][64] of 4 values), then (m, sum) of each row.
+    float* part;
+    int row_tiles, shift;
 };
 
 __device__ __forceinline__ int drafts_of(const TreeArgs& a, int b) {
     return a.draft_lens ? min(max(a.draft_lens[b], 0), a.drafts) : a.drafts;
 }
 
-// Tokens of sequence b that can be seen at all: its committed and drafted ones,
+// Tokens of a sequence that can be seen at all: its committed and drafted ones,
 // as far as the table's row goes (none in an empty pool).  Positions of a tile
 // stay below 2^31.
-__device__ __forceinline__ int tokens_of(const TreeArgs& a, int b) {
-    const int64_t n = (int64_t)max(a.seq_lens[b], 0) + drafts_of(a, b);
+__device__ __forceinline__ int tokens_of(const TreeArgs& a, int len, int drafts) {
+    const int64_t n = (int64_t)len + drafts;
     return a.num_pages ? (int)min(min(n, a.max_pages * a.page_size), (int64_t)0x7FFFFFC0) : 0;
 }
 
-// Tiles of sequence b; a sequence with drafted tokens has at least one, so that
-// its rows are written.
-__device__ __forceinline__ int tiles_of(const TreeArgs& a, int b) {
-    if (b >= a.batch || drafts_of(a, b) == 0) return 0;
-    return max((tokens_of(a, b) + kTile - 1) / kTile, 1);
+// Its tiles; a sequence with drafted tokens has at least one, so that its rows are written.
+__device__ __forceinline__ uint32_t tiles_of(int seen, int drafts) {
+    return drafts ? max((seen + kTile - 1) / kTile, 1) : 0;
 }
 
 // A value equal in all lanes, as a scalar (so that what follows from it is one too).
@@ -97,27 +97,42 @@ __device__ __forceinline__ int64_t scalar(int64_t v) {
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+// 64 sequences of the batch from first on, one to a lane, with the tiles of those
+// up to a lane's own (fewer than 2^32: a sequence has fewer than 2^26).
+struct Chunk {
+    int first, len, seen, drafts;
+    uint32_t tiles, upto;
+    __device__ __forceinline__ uint32_t all() const { return __builtin_amdgcn_readlane(upto, 63); }
+};
+__device__ __forceinline__ Chunk chunk_at(const TreeArgs& a, int first, int lane) {
+    const int b = min(first + lane, a.batch - 1);
+    Chunk c;
+    c.first = first;
+    c.len = max(a.seq_lens[b], 0);
+    c.drafts = drafts_of(a, b);
+    c.seen = tokens_of(a, c.len, c.drafts);
+    c.tiles = first + lane < a.batch ? tiles_of(c.seen, c.drafts) : 0;
+    c.upto = c.tiles;
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m, 64);
-    return scalar(v);
+    for (int m = 1; m < 64; m *= 2) {
+        const uint32_t o = __shfl_up(c.upto, m, 64);
+        if (lane >= m) c.upto += o;
+    }
+    return c;
 }
 
-// All tiles of the batch, and the ranges they are cut into.
-__device__ __forceinline__ int64_t all_tiles(const TreeArgs& a, int lane) {
-    int64_t n = 0;
-    for (int b = lane; b < a.batch; b += 64) n += tiles_of(a, b);
-    return wave_sum(n);
-}
-__device__ __forceinline__ int64_t used_ranges(const TreeArgs& a, int64_t tiles) {
-    return min((int64_t)a.ranges, max((tiles + kMinTiles - 1) / kMinTiles, (int64_t)1));
+// All tiles of the batch; c: its first chunk.
+__device__ __forceinline__ int64_t all_tiles(const TreeArgs& a, const Chunk& c, int lane) {
+    int64_t n = c.all();
+    for (int b = 64; b < a.batch; b += 64) n += chunk_at(a, b, lane).all();
+    return scalar(n);
 }
 
-// Tiles of the sequences before b (all lanes must call).
-__device__ __forceinline__ int64_t tiles_before(const TreeArgs& a, int b, int lane) {
-    int64_t n = 0;
-    for (int i = lane; i < b; i += 64) n += tiles_of(a, i);
-    return wave_sum(n);
+// The tiles are cut into 2^shift ranges: range x has those from x * tiles >> shift on.
+__device__ __forceinline__ int shift_of(const TreeArgs& a, int64_t tiles) {
+    int shift = a.shift;
+    while (shift > 0 && tiles < (int64_t)kMinTiles << shift) --shift;
+    return shift;
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -318,38 +333,33 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
     const uint32_t lds =
         __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)staging) + wave * kRegion;
     const Lane<D, HW> own = lane_of<D, HW>(a, head0, wave, lane);
-    const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
-    if ((int64_t)blockIdx.x >= ranges || total == 0) return;
-    const int64_t lo = scalar(blockIdx.x * total / ranges), hi = scalar((blockIdx.x + 1) * total / ranges);
+    Chunk chunk = chunk_at(a, 0, lane);
+    const int64_t total = all_tiles(a, chunk, lane);
+    const int shift = shift_of(a, total);
+    const int64_t lo = blockIdx.x * total >> shift, hi = (blockIdx.x + 1) * total >> shift;
+    if (blockIdx.x >> shift || lo == hi) return;
 
     // The sequence that holds tile lo, and the tiles before it.
-    int b = 0;
     int64_t before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
-        int64_t n = tiles_of(a, b0 + lane);
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-            const int64_t o = __shfl_up(n, m, 64);
-            if (lane >= m) n += o;
-        }
-        const int64_t chunk = scalar(__shfl(n, 63, 64));
-        if (before + chunk > lo) {
-            const int k = __popcll(__ballot(before + n <= lo));       // sequences of this chunk that end by lo
-            if (k) before += scalar(__shfl(n, k - 1, 64));
-            b = b0 + k;
-            break;
-        }
-        before += chunk;
+    while (before + chunk.all() <= lo) {
+        before += chunk.all();
+        chunk = chunk_at(a, chunk.first + 64, lane);
     }
-    b = __builtin_amdgcn_readfirstlane(b);
+    int b = chunk.first;
+    {
+        const int k = __popcll(__ballot((int64_t)(before + chunk.upto) <= lo));       // those that end by lo
+        if (k) before += (uint32_t)__builtin_amdgcn_readlane(chunk.upto, k - 1);
+        b += k;
+    }
 
     for (int64_t at = lo; at < hi; ++b) {
-        const int tiles = __builtin_amdgcn_readfirstlane(tiles_of(a, b));
+        if (b - chunk.first == 64) chunk = chunk_at(a, b, lane);
+        const int tiles = __builtin_amdgcn_readlane(chunk.tiles, b - chunk.first);
         if (tiles == 0) continue;
         const int t0 = (int)(at - before), t1 = (int)min(hi - before, (int64_t)tiles);
-        const int len = __builtin_amdgcn_readfirstlane(max(a.seq_lens[b], 0));
-        const int seen = __builtin_amdgcn_readfirstlane(tokens_of(a, b));
-        const int nd = __builtin_amdgcn_readfirstlane(drafts_of(a, b));
+        const int len = __builtin_amdgcn_readlane(chunk.len, b - chunk.first);
+        const int seen = __builtin_amdgcn_readlane(chunk.seen, b - chunk.first);
+        const int nd = __builtin_amdgcn_readlane(chunk.drafts, b - chunk.first);
         const int32_t* table = a.table + (int64_t)b * a.max_pages;
 
         u32x4 q[NR][kSteps];
@@ -552,8 +562,8 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
         for (int n = 0; n < NR; ++n) {
             const float l = sum[n][0];
             const int row = r0 + 16 * n + c, t = row / a.group;
-            if (t >= nd) continue;
             if (whole) {
+                if (t >= nd) continue;
                 const float inv = l > 0.f ? 1.0f / l : 0.f;
                 uint16_t* y = a.out + ((int64_t)b * a.drafts + t) * a.ld_out +
                               ((int64_t)head * a.group + row % a.group) * D + g * (D / 4);
@@ -566,20 +576,14 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
                     for (int j = 0; j < kOut / 2; j += 2)
                         *reinterpret_cast<uint2*>(y + i * kOut + 2 * j) = make_uint2(w[j], w[j + 1]);
                 }
-            } else {
+            } else if (r0 + 16 * n < a.rows) {
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (at == lo ? 0 : 1);
-                const int64_t at_row = (slot * a.kv_heads + head) * a.rows + row;
-                float* y = a.part + at_row * D + g * (D / 4);
+                const int64_t rt = (slot * a.kv_heads + head) * a.row_tiles + r0 / 16 + n;
+                v4f* y = reinterpret_cast<v4f*>(a.part) + rt * (4 * D) + lane;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < kOut; j += 4)
-                        *reinterpret_cast<float4*>(y + i * kOut + j) =
-                            make_float4(o[n][j][i], o[n][j + 1][i], o[n][j + 2][i], o[n][j + 3][i]);
-                if (g == 0) {
-                    float* ml = a.part + 2 * (int64_t)a.ranges * a.kv_heads * a.rows * D + at_row * 2;
-                    ml[0] = m[n], ml[1] = l;
-                }
+                for (int i = 0; i < kOut; ++i) y[64 * i] = o[n][i];
+                float2* ml = reinterpret_cast<float2*>(a.part + ((int64_t)2 << a.shift) * a.kv_heads * a.row_tiles * 16 * D);
+                if (g == 0) ml[rt * 16 + c] = make_float2(m[n], l);
             }
         }
         at += t1 - t0;
@@ -587,101 +591,108 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
     }
 }
 
-// Joins the partial results of the sequences that were cut.  A team of D/4 lanes
-// takes a row (16 bytes a lane); kTeams of them share one, pieces dealt to them in
-// turn, and their sums are joined through LDS in team order.  Workgroups of
-// sequence y stride over its rows, so what the pieces are is found once for many.
-template <int D, int kTeams, int kBlock>
-__global__ __launch_bounds__(kBlock) void attn_tree_join_kernel(const TreeArgs a) {
-    constexpr int kLanes = D / 4, kRows = kBlock / kLanes / kTeams, kBatch = 8;
-    __shared__ float4 sums[kTeams > 1 ? kBlock : 1];
-    __shared__ float2 stats[kTeams > 1 ? kBlock / kLanes : 1];
-    const int lane = threadIdx.x & 63, b = blockIdx.y;
-    const int64_t total = all_tiles(a, lane), ranges = used_ranges(a, total);
-    const int tiles = __builtin_amdgcn_readfirstlane(tiles_of(a, b)), nd = drafts_of(a, b);
-    if (tiles == 0) return;
-    const int64_t before = tiles_before(a, b, lane);
-    const int first = (int)scalar(((before + 1) * ranges - 1) / total);
-    const int last = (int)scalar(((before + tiles) * ranges - 1) / total);
+// Joins the partial results of the sequences that were cut: workgroup (x, y) 16
+// rows of a head (x) of sequence y.  A team of D/16 waves reads a piece as it was
+// written, 16 bytes a lane; kTeams of them take the pieces in turn, and their sums
+// are joined through LDS in team order.  The rows go out through LDS in 16-byte parts.
+template <int D, int kTeams>
+__global__ __launch_bounds__(4 * D * kTeams) void attn_tree_join_kernel(const TreeArgs a) {
+    constexpr int kTeam = 4 * D, kBatch = 8, kOut = D / 16;
+    __shared__ v4f sums[kTeams > 1 ? kTeam * kTeams : 1];
+    __shared__ float2 stats[kTeams][16];
+    __shared__ __attribute__((aligned(16))) uint16_t rows[16][D + 8];
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int b = blockIdx.y, head = blockIdx.x / a.row_tiles, r0 = blockIdx.x % a.row_tiles * 16;
+    Chunk chunk = chunk_at(a, 0, lane);
+    const int64_t total = all_tiles(a, chunk, lane);
+    const int shift = shift_of(a, total);
+    int64_t before = 0;
+    while (b - chunk.first >= 64) {
+        before += chunk.all();
+        chunk = chunk_at(a, chunk.first + 64, lane);
+    }
+    const uint32_t tiles = __builtin_amdgcn_readlane(chunk.tiles, b - chunk.first);
+    const int nd = __builtin_amdgcn_readlane(chunk.drafts, b - chunk.first);
+    before += (uint32_t)__builtin_amdgcn_readlane(chunk.upto, b - chunk.first) - tiles;
+    if (tiles == 0 || r0 >= nd * a.group) return;
+    // The ranges that hold its first and last tile: tile t lies in the last range
+    // whose start, x * total >> shift, is at most t.
+    const int first = (int)scalar((((before + 1) << shift) - 1) / total);
+    const int last = (int)scalar((((before + tiles) << shift) - 1) / total);
     if (first == last) return;                                // one piece: written already
     // The first piece is its range's second one unless the range starts with it.
-    const int first_slot = 2 * first + (scalar(first * total / ranges) == before ? 0 : 1);
-    const int all_rows = a.kv_heads * a.rows;
-    const float* ml = a.part + 2 * (int64_t)a.ranges * all_rows * D;
-    const int team = threadIdx.x / kLanes, part = team % kTeams, l4 = threadIdx.x % kLanes * 4;
-    for (int r0 = blockIdx.x * kRows; r0 < all_rows; r0 += gridDim.x * kRows) {
-        const int r = r0 + team / kTeams;
-        const bool live = r < all_rows && r % a.rows / a.group < nd;
-        float m = kFloor, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int x0 = first + part; live && x0 <= last; x0 += kBatch * kTeams) {
-            float2 s[kBatch];
-            float4 o[kBatch];
+    const int first_slot = 2 * first + ((first * total >> shift) == before ? 0 : 1);
+    const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = part >> 6;
+    const int64_t step = (int64_t)a.kv_heads * a.row_tiles;
+    const v4f* o = reinterpret_cast<const v4f*>(a.part) + (int64_t)blockIdx.x * kTeam + part;
+    const float2* ml = reinterpret_cast<const float2*>(a.part + ((int64_t)2 << a.shift) * step * 16 * D) +
+                       (int64_t)blockIdx.x * 16 + c;
+
+    float m = kFloor, l = 0.f;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    for (int x0 = first + team; x0 <= last; x0 += kBatch * kTeams) {
+        float2 s[kBatch];
+        v4f v[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int x = x0 + k * kTeams;
-                s[k] = make_float2(kFloor, 0.f);
-                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (x <= last) {
-                    const int64_t at = (int64_t)(x == first ? first_slot : 2 * x) * all_rows + r;
-                    s[k] = *reinterpret_cast<const float2*>(ml + at * 2);
-                    o[k] = *reinterpret_cast<const float4*>(a.part + at * D + l4);
-                }
-            }
-            float top = m;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
-            const float keep = exp2_hw(m - top);
-            m = top;
-            l *= keep;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] *= keep;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float e = exp2_hw(s[k].x - top);
-                l += s[k].y * e;
-                acc[0] += o[k].x * e, acc[1] += o[k].y * e, acc[2] += o[k].z * e, acc[3] += o[k].w * e;
+        for (int k = 0; k < kBatch; ++k) {
+            const int x = x0 + k * kTeams;
+            s[k] = make_float2(kFloor, 0.f);
+            v[k] = v4f{0.f, 0.f, 0.f, 0.f};
+            if (x <= last) {
+                const int64_t at = (x == first ? first_slot : 2 * (int64_t)x) * step;
+                s[k] = ml[at * 16];
+                v[k] = o[at * kTeam];
             }
         }
-        if constexpr (kTeams > 1) {
-            sums[threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (l4 == 0) stats[team] = make_float2(m, l);
-            __syncthreads();
-            if (part == 0) {
-                float top = kFloor;
+        float top = m;
 #pragma unroll
-                for (int k = 0; k < kTeams; ++k) top = fmaxf(top, stats[team + k].x);
-                l = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, s[k].x);
+        const float keep = exp2_hw(m - top);
+        m = top;
+        l *= keep;
+        acc *= keep;
 #pragma unroll
-                for (int k = 0; k < kTeams; ++k) {
-                    const float e = exp2_hw(stats[team + k].x - top);
-                    const float4 o = sums[threadIdx.x + k * kLanes];
-                    l += stats[team + k].y * e;
-                    acc[0] += o.x * e, acc[1] += o.y * e, acc[2] += o.z * e, acc[3] += o.w * e;
-                }
-            }
-            __syncthreads();                                  // sums free for the next rows
-        }
-        if (live && part == 0) {
-            const float inv = l > 0.f ? 1.0f / l : 0.f;
-            const int row = r % a.rows, head = r / a.rows;
-            uint16_t* y = a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out +
-                          ((int64_t)head * a.group + row % a.group) * D + l4;
-            *reinterpret_cast<uint2*>(y) = make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+        for (int k = 0; k < kBatch; ++k) {
+            const float e = exp2_hw(s[k].x - top);
+            l += s[k].y * e;
+            acc += v[k] * e;
         }
     }
-}
-
-template <int D, int kTeams, int kBlock>
-void launch_join(const TreeArgs& a, hipStream_t s) {
-    constexpr int kRows = kBlock / (D / 4) / kTeams;
-    const int64_t need = ((int64_t)a.kv_heads * a.rows + kRows - 1) / kRows, most = 2048 * 256 / kBlock / a.batch;
-    const unsigned x = (unsigned)(need < most ? need : most < 1 ? 1 : most);
-    attn_tree_join_kernel<D, kTeams, kBlock><<<dim3(x, (unsigned)a.batch), kBlock, 0, s>>>(a);
+    if constexpr (kTeams > 1) {
+        sums[threadIdx.x] = acc;
+        if (part < 16) stats[team][part] = make_float2(m, l);
+        __syncthreads();
+        if (team == 0) {
+            float top = kFloor;
+#pragma unroll
+            for (int k = 0; k < kTeams; ++k) top = fmaxf(top, stats[k][c].x);
+            l = 0.f;
+            acc = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kTeams; ++k) {
+                const float e = exp2_hw(stats[k][c].x - top);
+                l += stats[k][c].y * e;
+                acc += sums[part + k * kTeam] * e;
+            }
+        }
+    }
+    if (team == 0) {
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rows[c][g * (D / 4) + k * kOut + i] = (uint16_t)pack2(acc[k] * inv, 0.f);
+    }
+    __syncthreads();
+    const int chunks = D / 8, r = threadIdx.x / chunks, row = r0 + r;
+    if (r < 16 && row < nd * a.group) {
+        uint16_t* y = a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out +
+                      ((int64_t)head * a.group + row % a.group) * D + threadIdx.x % chunks * 8;
+        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(&rows[r][threadIdx.x % chunks * 8]);
+    }
 }
 
 // How the call is laid out, from its shapes alone.
 struct Layout {
-    int nr, waves, columns, ranges;        // row tiles per wave, waves (heads) per workgroup, workgroups per range
+    int nr, waves, columns, shift;         // row tiles per wave, waves (heads) per workgroup, workgroups per range
 };
 Layout layout_of(int drafts, int q_heads, int kv_heads, int head_dim) {
     const int rows = drafts * (q_heads / kv_heads);
@@ -689,24 +700,23 @@ Layout layout_of(int drafts, int q_heads, int kv_heads, int head_dim) {
     l.nr = rows > 16 && head_dim <= 128 ? 2 : 1;
     l.waves = kv_heads % 8 == 0 && head_dim <= 128 ? 8 : kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
     l.columns = kv_heads / l.waves * ((rows + 16 * l.nr - 1) / (16 * l.nr));
-    // a multiple of 8, so that a range's workgroups meet on one XCD
-    const int ranges = kGridWaves / (l.columns * l.waves) / 8 * 8;
-    l.ranges = ranges < 8 ? 8 : ranges;
+    // 2^shift ranges (at least 8, so that a range's workgroups meet on one XCD)
+    l.shift = 3;
+    while ((int64_t)l.columns * l.waves << (l.shift + 1) <= kGridWaves) ++l.shift;
     return l;
 }
 
 template <int D, int NR, int HW>
 hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
-    attn_tree_kernel<D, NR, HW><<<dim3((unsigned)l.ranges, (unsigned)l.columns), 64 * HW, 0, s>>>(a);
+    attn_tree_kernel<D, NR, HW><<<dim3(1u << l.shift, (unsigned)l.columns), 64 * HW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // Pieces of a sequence on average: how many teams share a row.
-    if (l.ranges >= 32 * a.batch)
-        launch_join<D, 16, 1024>(a, s);
-    else if (l.ranges >= 8 * a.batch)
-        launch_join<D, 4, 256>(a, s);
+    // Pieces of a sequence on average: whether several teams share a row tile.
+    const dim3 grid((unsigned)(a.kv_heads * a.row_tiles), (unsigned)a.batch);
+    if (1 << l.shift >= 16 * a.batch)
+        attn_tree_join_kernel<D, 256 / D><<<grid, 1024, 0, s>>>(a);
     else
-        launch_join<D, 1, 256>(a, s);
+        attn_tree_join_kernel<D, 1><<<grid, 4 * D, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int D, int NR>
@@ -722,7 +732,8 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
 size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
     (void)batch;
     const Layout l = layout_of(drafts, q_heads, kv_heads, head_dim);
-    return (size_t)2 * l.ranges * q_heads * drafts * (head_dim + 2) * sizeof(float);
+    const size_t row_tiles = (size_t)(drafts * (q_heads / kv_heads) + 15) / 16;
+    return ((size_t)2 << l.shift) * kv_heads * row_tiles * 16 * (head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
@@ -739,7 +750,7 @@ hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
     // Never 0: a hidden score is -inf and has to stay that when scaled.
     a.scale2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
     a.flip = p.scale < 0 ? 0x80008000u : 0u;
-    a.part = static_cast<float*>(p.ws), a.ranges = l.ranges;
+    a.part = static_cast<float*>(p.ws), a.row_tiles = (a.rows + 15) / 16, a.shift = l.shift;
     switch (p.head_dim) {
         case 64: return l.nr == 2 ? launch<64, 2>(a, l, s) : launch<64, 1>(a, l, s);
         case 128: return l.nr == 2 ? launch<128, 2>(a, l, s) : launch<128, 1>(a, l, s);
