@@ -14,7 +14,8 @@
 //   alike);
 //   V^T: transposing LDS reads (ds_read_b64_tr_b16): 4 tokens of one value.
 // The running reference m moves only when a score exceeds it by more than 2^8.
-// Weights are rounded to bf16 for the second product; their sum stays fp32.
+// Weights are rounded to bf16 for the second product (they enter it with V's
+// 16-bit format); the rounded weights are what is summed, in fp32.
 #include "fp4_internal.h"
 #include "mma_core.h"
 
@@ -24,7 +25,8 @@ namespace {
 constexpr int kRows = 128;                 // query rows of a workgroup
 constexpr int kThreads = 256;
 constexpr float kSlack = 8.0f;
-constexpr float kNone = -__builtin_inff();
+constexpr float kNone = -__builtin_inff();   // score of a hidden token
+constexpr float kFloor = -3e38f;           // reference before the first tile
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -49,15 +51,64 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+typedef __attribute__((address_space(3))) uint8_t* lds_bytes;
+
+// A tile of keys and one of values in LDS, rows of D values without padding.  They
+// come straight from global memory (a wave copies a quarter of each, 16 bytes a
+// lane, 1 KiB an instruction), so rows are spread over the 64 banks by where a
+// 16-byte chunk is put: chunk x of key row r at x ^ key_turn(r), which keeps the 16
+// lanes that read one chunk of 16 rows apart, and of value row r at x ^ 2 (r % 4),
+// which does so for the 4 rows of 32 bytes that a transposing read takes.
 template <int D>
 struct Shape {
     static constexpr int kTokens = D == 256 ? 32 : 64;       // keys of a tile
-    // Row pitches in LDS (bf16 values), off the multiples of the 64 banks so that
-    // the rows that one instruction reads fall into different banks.
-    static constexpr int kPitchK = D + 8;
-    static constexpr int kPitchV = D + 16;
-    static constexpr int kChunks = kTokens * D / 8 / kThreads;   // 16-byte chunks per lane and tile
+    static constexpr int kRow = 2 * D, kTile = kTokens * kRow;           // bytes
+    static constexpr int kCopies = kTile / 4096;             // of keys, and of values, per wave
+    static constexpr int kPerCopy = 1024 / kRow;             // rows
+    __device__ static constexpr int key_turn(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
+    __device__ static constexpr int value_turn(int row) { return 2 * (row & 3); }
 };
+
+// A wave's copies of one tile, into LDS at keys and values; k and v: where the
+// tile's first rows lie, less 1024 (kCopies - 1), which the lane offsets carry (the
+// instruction's offset counts on both sides).  Awaited by wait_copies.
+template <int D>
+__device__ __forceinline__ void copy_tile(const uint8_t* k, const uint8_t* v, const uint32_t* ko, const uint32_t* vo,
+                                          uint32_t keys, uint32_t values) {
+    if constexpr (Shape<D>::kCopies == 2) {
+        asm volatile(
+            "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %0, %4\n\t"
+            "global_load_lds_dwordx4 %1, %4 offset:1024\n\t"
+            "s_mov_b32 m0, %7\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %2, %5\n\t"
+            "global_load_lds_dwordx4 %3, %5 offset:1024" ::"v"(ko[0]),
+            "v"(ko[1]), "v"(vo[0]), "v"(vo[1]), "s"(k), "s"(v), "s"(keys), "s"(values)
+            : "memory", "m0");
+    } else {
+        asm volatile(
+            "s_mov_b32 m0, %10\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %0, %8\n\t"
+            "global_load_lds_dwordx4 %1, %8 offset:1024\n\t"
+            "global_load_lds_dwordx4 %2, %8 offset:2048\n\t"
+            "global_load_lds_dwordx4 %3, %8 offset:3072\n\t"
+            "s_mov_b32 m0, %11\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %4, %9\n\t"
+            "global_load_lds_dwordx4 %5, %9 offset:1024\n\t"
+            "global_load_lds_dwordx4 %6, %9 offset:2048\n\t"
+            "global_load_lds_dwordx4 %7, %9 offset:3072" ::"v"(ko[0]),
+            "v"(ko[1]), "v"(ko[2]), "v"(ko[3]), "v"(vo[0]), "v"(vo[1]), "v"(vo[2]), "v"(vo[3]), "s"(k), "s"(v), "s"(keys),
+            "s"(values)
+            : "memory", "m0");
+    }
+}
+// This wave's copies have landed and its LDS reads have returned, then all waves'.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ float add_pair(float sum, uint32_t pair) {    // both bf16 of pair, in fp32
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), sum,
+                                           false);
+}
 
 // Sequences that start at or before tile x of the row tiles: tile numbers of
 // sequence s run from cu[s] / kRows + s on, which leaves every sequence enough of
@@ -69,10 +120,9 @@ __device__ __forceinline__ int64_t row_of(const PromptArgs& a, int s) {
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel(const PromptArgs a) {
     using S = Shape<D>;
-    constexpr int kTokens = S::kTokens, kSteps = D / 16, kOut = D / 32, kSub = kTokens / 32;
-    __shared__ __attribute__((aligned(16))) uint16_t lk[2][kTokens * S::kPitchK];
-    __shared__ __attribute__((aligned(16))) uint16_t lv[2][kTokens * S::kPitchV];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, h = lane >> 5;
+    constexpr int kTokens = S::kTokens, kSteps = D / 16, kOut = D / 32, kSub = kTokens / 32, kBatch = kSteps < 8 ? kSteps : 8;
+    __shared__ __attribute__((aligned(16))) uint8_t tiles_lds[2 * 2 * S::kTile];        // keys, values; twice
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
 
     // Query heads of one key/value head meet on one XCD (workgroups are dealt to
     // the 8 XCDs in turn); late row tiles, which see the most keys, come first.
@@ -98,8 +148,33 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
     if (q0 < 0 || q0 >= len) return;
 
     const int kv = head / a.group;
-    const uint16_t* kg = a.k + start * a.ld_k + (int64_t)kv * D;
-    const uint16_t* vg = a.v + start * a.ld_v + (int64_t)kv * D;
+    const uint8_t* kg = reinterpret_cast<const uint8_t*>(a.k + start * a.ld_k + (int64_t)kv * D);
+    const uint8_t* vg = reinterpret_cast<const uint8_t*>(a.v + start * a.ld_v + (int64_t)kv * D);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)tiles_lds);
+
+    // Where this lane's chunks of a tile lie; rows behind the sequence are read as
+    // its last one (hidden by the mask, and finite).
+    uint32_t ko[S::kCopies], vo[S::kCopies];
+    auto offsets = [&](int rows) {
+#pragma unroll
+        for (int i = 0; i < S::kCopies; ++i) {
+            const int r = (wave * S::kCopies + i) * S::kPerCopy + lane / (D / 8), at = lane % (D / 8);
+            const uint32_t pad = 1024 * (S::kCopies - 1 - i), from = min(r, rows - 1);
+            ko[i] = from * (uint32_t)(2 * a.ld_k) + (at ^ S::key_turn(r)) * 16 + pad;
+            vo[i] = from * (uint32_t)(2 * a.ld_v) + (at ^ S::value_turn(r)) * 16 + pad;
+        }
+    };
+    offsets(kTokens);
+    const int last_row = (int)min(q0 + kRows, len) - 1, tiles = last_row / kTokens + 1;
+    auto copy = [&](int t) {
+        const int64_t t0 = (int64_t)t * kTokens;
+        if (len - t0 < kTokens) offsets((int)(len - t0));    // the sequence's last tile
+        const uint32_t at = lds + (t & 1) * 2 * S::kTile + wave * S::kCopies * 1024;
+        copy_tile<D>(kg + t0 * 2 * a.ld_k - 1024 * (S::kCopies - 1), vg + t0 * 2 * a.ld_v - 1024 * (S::kCopies - 1), ko, vo, at,
+                     at + S::kTile);
+    };
+    copy(0);
+
     const int64_t row = q0 + 32 * wave + c;                  // this lane's query row
     const bool live = row < len;
     u32x4 q[kSteps];
@@ -114,105 +189,102 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
     v16f o[kOut];
 #pragma unroll
     for (int i = 0; i < kOut; ++i) o[i] = v16f{};
-    float m = kNone, sum = 0.f;
+    float m = kFloor, sum[4] = {0.f, 0.f, 0.f, 0.f};         // sum: of the rounded weights, in four parts
 
-    u32x4 sk[S::kChunks], sv[S::kChunks];
-    auto fetch = [&](int64_t t0) {
+    // LDS offsets of this lane's reads: a step's keys (steps 8 on lie 256 bytes
+    // further), and the values of even and odd 32s.
+    uint32_t rk[kBatch], rv[2];
 #pragma unroll
-        for (int i = 0; i < S::kChunks; ++i) {
-            const int chunk = i * kThreads + threadIdx.x, r = chunk / (D / 8), col = chunk % (D / 8) * 8;
-            const bool in = t0 + r < len;                    // behind the sequence: zeros, whatever lies there
-            sk[i] = in ? *reinterpret_cast<const u32x4*>(kg + (t0 + r) * a.ld_k + col) : u32x4{0, 0, 0, 0};
-            sv[i] = in ? *reinterpret_cast<const u32x4*>(vg + (t0 + r) * a.ld_v + col) : u32x4{0, 0, 0, 0};
-        }
-    };
-    auto store = [&](int buf) {
+    for (int i = 0; i < kBatch; ++i) rk[i] = c * S::kRow + ((2 * i + h) ^ S::key_turn(c)) * 16;
+    {
+        const int r = 4 * h + (lane & 15) / 4, x = (2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ S::value_turn(r);
 #pragma unroll
-        for (int i = 0; i < S::kChunks; ++i) {
-            const int chunk = i * kThreads + threadIdx.x, r = chunk / (D / 8), col = chunk % (D / 8) * 8;
-            *reinterpret_cast<u32x4*>(&lk[buf][r * S::kPitchK + col]) = sk[i];
-            *reinterpret_cast<u32x4*>(&lv[buf][r * S::kPitchV + col]) = sv[i];
-        }
-    };
+        for (int i = 0; i < 2; ++i) rv[i] = S::kTile + r * S::kRow + (x ^ (4 * i)) * 16 + (lane & 1) * 8;
+    }
 
-    const int64_t last_row = min(q0 + kRows, len) - 1;
-    const int64_t wave_first = q0 + 32 * wave;
-    const int tiles = (int)(last_row / kTokens) + 1;
-    fetch(0);
-    store(0);
-    __syncthreads();
-    for (int t = 0; t < tiles; ++t) {
-        const int buf = t & 1;
-        const int64_t t0 = (int64_t)t * kTokens;
-        if (t + 1 < tiles) fetch(t0 + kTokens);
-        if (t0 <= wave_first + 31) {                         // else nothing of this tile is visible to the wave
-            v16f s[kSub];
+    const int wave_first = (int)q0 + 32 * wave;
+    auto compute = [&](int t, const uint8_t* tile) {
+        const int t0 = t * kTokens;
+        v16f s[kSub];
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                s[u] = v16f{};
-                const uint16_t* p = &lk[buf][(32 * u + c) * S::kPitchK + 8 * h];
+        for (int u = 0; u < kSub; ++u) {
+            s[u] = v16f{};
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p + 16 * i)),
-                        __builtin_bit_cast(bf16x8, q[i]), s[u], 0, 0, 0);
+            for (int b = 0; b < kSteps / kBatch; ++b) {
+                u32x4 kf[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    kf[i] = *reinterpret_cast<const u32x4*>(tile + rk[i] + 32 * u * S::kRow + 256 * b);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[i]),
+                                                                   __builtin_bit_cast(bf16x8, q[b * kBatch + i]), s[u], 0, 0, 0);
             }
-            if (t0 + kTokens - 1 > wave_first) {             // the diagonal
-                const int d = (int)(row - t0);
-#pragma unroll
-                for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (32 * u + 8 * (i / 4) + 4 * h + i % 4 > d) s[u][i] = kNone;
-            }
-            float top = s[0][0];
+        }
+        if (t0 + kTokens - 1 > wave_first) {                 // the diagonal
+            const int d = (int)row - t0;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-            top *= a.scale2;
-            if (__any(top > m + kSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float up = fmaxf(m, top);
-                const float alpha = up == m ? 1.0f : exp2_hw(m - up);
-                m = up;
-                sum *= alpha;
+                for (int i = 0; i < 16; ++i)
+                    s[u][i] = 32 * u + 8 * (i / 4) + 4 * h + i % 4 > d ? kNone : s[u][i];
+        }
+        float top = s[0][0];
 #pragma unroll
-                for (int i = 0; i < kOut; ++i) o[i] *= alpha;
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top *= a.scale2;
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float up = fmaxf(m, top);
+            const float alpha = exp2_hw(m - up);
+            m = up;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] *= alpha;
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) o[i] *= alpha;
+        }
+        // Every row sees token 0, so m is finite from the first tile on.
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            uint32_t p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = pack2(exp2_hw(fmaf(s[u][2 * i], a.scale2, -m)), exp2_hw(fmaf(s[u][2 * i + 1], a.scale2, -m)));
+                sum[i & 3] = add_pair(sum[i & 3], p[i]);
             }
-            // Every row sees token 0, so m is finite from the first tile on.
 #pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                uint32_t p[8];
+            for (int w = 0; w < 2; ++w) {                    // 16 tokens
+                const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[4 * w], p[4 * w + 1], p[4 * w + 2], p[4 * w + 3]});
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a0 = exp2_hw(fmaf(s[u][2 * i], a.scale2, -m));
-                    const float a1 = exp2_hw(fmaf(s[u][2 * i + 1], a.scale2, -m));
-                    sum += a0 + a1;
-                    p[i] = pack2(a0, a1);
-                }
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {                // 16 tokens
-                    const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[4 * w], p[4 * w + 1], p[4 * w + 2], p[4 * w + 3]});
-                    const uint16_t* base = &lv[buf][(32 * u + 16 * w + 4 * h + (lane & 15) / 4) * S::kPitchV +
-                                                    16 * ((lane >> 4) & 1) + 4 * (lane & 3)];
-#pragma unroll
-                    for (int i = 0; i < kOut; ++i) {
-                        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + 32 * i));
-                        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + 32 * i + 8 * S::kPitchV));
-                        const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va, pb, o[i], 0, 0, 0);
-                    }
+                for (int i = 0; i < kOut; ++i) {
+                    const uint8_t* x = tile + rv[i & 1] + (32 * u + 16 * w) * S::kRow + 128 * (i >> 1);
+                    const v4s x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(x));
+                    const v4s x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(x + 8 * S::kRow));
+                    const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va, pb, o[i], 0, 0, 0);
                 }
             }
         }
-        if (t + 1 < tiles) store(buf ^ 1);
-        __syncthreads();
+    };
+    // When the waves meet, tile t is in LDS, and the other buffer is free.
+    auto turn = [&](int t, const uint8_t* tile) {
+        meet();
+        if (t + 1 < tiles) copy(t + 1);
+        if (t * kTokens <= wave_first + 31) compute(t, tile);    // else nothing of it is visible to the wave
+    };
+    int t = 0;
+    for (; t + 2 <= tiles; t += 2) {
+        turn(t, tiles_lds);
+        turn(t + 1, tiles_lds + 2 * S::kTile);
     }
+    if (t < tiles) turn(t, tiles_lds);
 
-    sum += __shfl_xor(sum, 32, 64);
+    float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    total += __shfl_xor(total, 32, 64);
     if (!live) return;
-    const float inv = 1.0f / sum;
+    const float inv = 1.0f / total;
     uint16_t* y = a.out + (start + row) * a.ld_out + (int64_t)head * D + 4 * h;
 #pragma unroll
     for (int i = 0; i < kOut; ++i)
