@@ -57,8 +57,9 @@ typedef __attribute__((address_space(3))) uint8_t* lds_bytes;
 // come straight from global memory (a wave copies a quarter of each, 16 bytes a
 // lane, 1 KiB an instruction), so rows are spread over the 64 banks by where a
 // 16-byte chunk is put: chunk x of key row r at x ^ key_turn(r), which keeps the 16
-// lanes that read one chunk of 16 rows apart, and of value row r at x ^ 2 (r % 4),
-// which does so for the 4 rows of 32 bytes that a transposing read takes.
+// lanes that read one chunk of 16 rows apart, and of value row r at x ^
+// value_turn(r), which does so for the 4 rows of 64 bytes that half the lanes of a
+// transposing read take (256 bytes a cycle).
 template <int D>
 struct Shape {
     static constexpr int kTokens = D == 256 ? 32 : 64;       // keys of a tile
@@ -66,7 +67,7 @@ struct Shape {
     static constexpr int kCopies = kTile / 4096;             // of keys, and of values, per wave
     static constexpr int kPerCopy = 1024 / kRow;             // rows
     __device__ static constexpr int key_turn(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
-    __device__ static constexpr int value_turn(int row) { return 2 * (row & 3); }
+    __device__ static constexpr int value_turn(int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); }
 };
 
 // A wave's copies of one tile, into LDS at keys and values; k and v: where the
@@ -192,14 +193,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
     float m = kFloor, sum[4] = {0.f, 0.f, 0.f, 0.f};         // sum: of the rounded weights, in four parts
 
     // LDS offsets of this lane's reads: a step's keys (steps 8 on lie 256 bytes
-    // further), and the values of even and odd 32s.
-    uint32_t rk[kBatch], rv[2];
+    // further), and the values of each 32 (the fifth on 256 bytes further).
+    constexpr int kTurns = kOut < 4 ? kOut : 4;
+    uint32_t rk[kBatch], rv[kTurns];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) rk[i] = c * S::kRow + ((2 * i + h) ^ S::key_turn(c)) * 16;
     {
         const int r = 4 * h + (lane & 15) / 4, x = (2 * ((lane >> 4) & 1) + (lane & 3) / 2) ^ S::value_turn(r);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) rv[i] = S::kTile + r * S::kRow + (x ^ (4 * i)) * 16 + (lane & 1) * 8;
+        for (int i = 0; i < kTurns; ++i) rv[i] = S::kTile + r * S::kRow + (x ^ (4 * i)) * 16 + (lane & 1) * 8;
     }
 
     const int wave_first = (int)q0 + 32 * wave;
@@ -259,7 +261,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
                 const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[4 * w], p[4 * w + 1], p[4 * w + 2], p[4 * w + 3]});
 #pragma unroll
                 for (int i = 0; i < kOut; ++i) {
-                    const uint8_t* x = tile + rv[i & 1] + (32 * u + 16 * w) * S::kRow + 128 * (i >> 1);
+                    const uint8_t* x = tile + rv[i % kTurns] + (32 * u + 16 * w) * S::kRow + 256 * (i / kTurns);
                     const v4s x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(x));
                     const v4s x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(x + 8 * S::kRow));
                     const bf16x8 va = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
