@@ -734,7 +734,7 @@ int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* 
                 (long long)tokens);
     FP4_REQUIRE(tokens < (int64_t)1 << 31 && seqs < kMaxList, FP4_ERR_SHAPE, "tokens=%lld or seqs=%lld too large",
                 (long long)tokens, (long long)seqs);
-    FP4_REQUIRE(fp4::attn_prompt_tiles(seqs, tokens) < ((int64_t)1 << 24) / q_heads, FP4_ERR_SHAPE,
+    FP4_REQUIRE(fp4::attn_prompt_tiles(seqs, tokens, head_dim) < ((int64_t)1 << 24) / q_heads, FP4_ERR_SHAPE,
                 "tokens=%lld, seqs=%lld and q_heads=%d give too many row tiles (2^24)", (long long)tokens, (long long)seqs,
                 q_heads);
     FP4_REQUIRE(std::isfinite(scale), FP4_ERR_INVALID, "scale is not finite");

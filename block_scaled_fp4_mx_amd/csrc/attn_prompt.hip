@@ -22,8 +22,10 @@
 namespace fp4 {
 namespace {
 
-constexpr int kRows = 128;                 // query rows of a workgroup
-constexpr int kThreads = 256;
+// Waves of a workgroup, 32 query rows each.  8 waves (256 rows) at D = 256 keep two
+// waves per SIMD in 256 registers, where 4 take 420; below, 4 and 8 measured alike
+// (16384 rows: 2.04 and 1.97 ms; four documents of 8k rows in all: 341 and 357 us).
+constexpr int waves_of(int head_dim) { return head_dim == 256 ? 8 : 4; }
 constexpr float kSlack = 8.0f;
 constexpr float kNone = -__builtin_inff();   // score of a hidden token
 constexpr float kFloor = -3e38f;           // reference before the first tile
@@ -54,17 +56,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 typedef __attribute__((address_space(3))) uint8_t* lds_bytes;
 
 // A tile of keys and one of values in LDS, rows of D values without padding.  They
-// come straight from global memory (a wave copies a quarter of each, 16 bytes a
-// lane, 1 KiB an instruction), so rows are spread over the 64 banks by where a
+// come straight from global memory (each of the W waves copies its share, 16 bytes
+// a lane, 1 KiB an instruction), so rows are spread over the 64 banks by where a
 // 16-byte chunk is put: chunk x of key row r at x ^ key_turn(r), which keeps the 16
 // lanes that read one chunk of 16 rows apart, and of value row r at x ^
 // value_turn(r), which does so for the 4 rows of 64 bytes that half the lanes of a
 // transposing read take (256 bytes a cycle).
 template <int D>
 struct Shape {
+    static constexpr int W = waves_of(D);
+    static constexpr int kRows = 32 * W;                     // query rows of a workgroup
     static constexpr int kTokens = D == 256 ? 32 : 64;       // keys of a tile
     static constexpr int kRow = 2 * D, kTile = kTokens * kRow;           // bytes
-    static constexpr int kCopies = kTile / 4096;             // of keys, and of values, per wave
+    static constexpr int kCopies = kTile / 1024 / W;            // of keys, and of values, per wave
     static constexpr int kPerCopy = 1024 / kRow;             // rows
     __device__ static constexpr int key_turn(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
     __device__ static constexpr int value_turn(int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); }
@@ -73,10 +77,18 @@ struct Shape {
 // A wave's copies of one tile, into LDS at keys and values; k and v: where the
 // tile's first rows lie, less 1024 (kCopies - 1), which the lane offsets carry (the
 // instruction's offset counts on both sides).  Awaited by wait_copies.
-template <int D>
+template <int kCopies>
 __device__ __forceinline__ void copy_tile(const uint8_t* k, const uint8_t* v, const uint32_t* ko, const uint32_t* vo,
                                           uint32_t keys, uint32_t values) {
-    if constexpr (Shape<D>::kCopies == 2) {
+    if constexpr (kCopies == 1) {
+        asm volatile(
+            "s_mov_b32 m0, %4\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %0, %2\n\t"
+            "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+            "global_load_lds_dwordx4 %1, %3" ::"v"(ko[0]),
+            "v"(vo[0]), "s"(k), "s"(v), "s"(keys), "s"(values)
+            : "memory", "m0");
+    } else if constexpr (kCopies == 2) {
         asm volatile(
             "s_mov_b32 m0, %6\n\ts_nop 0\n\t"
             "global_load_lds_dwordx4 %0, %4\n\t"
@@ -111,17 +123,16 @@ __device__ __forceinline__ float add_pair(float sum, uint32_t pair) {    // both
                                            false);
 }
 
-// Sequences that start at or before tile x of the row tiles: tile numbers of
-// sequence s run from cu[s] / kRows + s on, which leaves every sequence enough of
-// them and needs no table of lengths.
-__device__ __forceinline__ int64_t row_of(const PromptArgs& a, int s) {
-    return min(max((int64_t)a.cu[s], (int64_t)0), a.tokens);
+// First row of sequence s.  Its row tiles are numbered from row_of(s) / kRows + s
+// on, which leaves every sequence enough of them and needs no table of lengths.
+__device__ __forceinline__ int row_of(const PromptArgs& a, int s) {
+    return min(max(a.cu[s], 0), (int)a.tokens);
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel(const PromptArgs a) {
+__global__ __launch_bounds__(64 * waves_of(D), 2) void attn_prompt_kernel(const PromptArgs a) {
     using S = Shape<D>;
-    constexpr int kTokens = S::kTokens, kSteps = D / 16, kOut = D / 32, kSub = kTokens / 32, kBatch = kSteps < 8 ? kSteps : 8;
+    constexpr int kRows = S::kRows, kTokens = S::kTokens, kSteps = D / 16, kOut = D / 32, kSub = kTokens / 32, kBatch = kSteps < 8 ? kSteps : 8;
     __shared__ __attribute__((aligned(16))) uint8_t tiles_lds[2 * 2 * S::kTile];        // keys, values; twice
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
 
@@ -136,16 +147,22 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
         head = blockIdx.x % a.q_heads;
         x = a.tiles - 1 - blockIdx.x / a.q_heads;
     }
-    int lo = 0, hi = a.seqs - 1;
-    while (lo < hi) {                                        // last sequence whose tiles start at or before x
-        const int mid = (lo + hi + 1) / 2;
+    // The last sequence whose tiles start at or before x: 64 candidates at once, a
+    // bound to a lane, after halving for larger batches.
+    int lo = 0, hi = a.seqs;
+    while (hi - lo > 64) {
+        const int mid = (lo + hi) / 2;
         if (row_of(a, mid) / kRows + mid <= x)
             lo = mid;
         else
-            hi = mid - 1;
+            hi = mid;
     }
-    const int64_t start = row_of(a, lo), end = row_of(a, lo + 1);
-    const int64_t q0 = (x - (start / kRows + lo)) * kRows, len = end - start;
+    const int at = min(lo + lane, a.seqs);
+    const int first = (int)row_of(a, at), behind = (int)row_of(a, min(at + 1, a.seqs));
+    const int seq = __popcll(__ballot(lo + lane < hi && first / kRows + at <= x)) - 1;
+    if (seq < 0) return;
+    const int64_t start = __builtin_amdgcn_readlane(first, seq), end = __builtin_amdgcn_readlane(behind, seq);
+    const int64_t q0 = (x - (start / kRows + lo + seq)) * kRows, len = end - start;
     if (q0 < 0 || q0 >= len) return;
 
     const int kv = head / a.group;
@@ -171,7 +188,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
         const int64_t t0 = (int64_t)t * kTokens;
         if (len - t0 < kTokens) offsets((int)(len - t0));    // the sequence's last tile
         const uint32_t at = lds + (t & 1) * 2 * S::kTile + wave * S::kCopies * 1024;
-        copy_tile<D>(kg + t0 * 2 * a.ld_k - 1024 * (S::kCopies - 1), vg + t0 * 2 * a.ld_v - 1024 * (S::kCopies - 1), ko, vo, at,
+        copy_tile<S::kCopies>(kg + t0 * 2 * a.ld_k - 1024 * (S::kCopies - 1), vg + t0 * 2 * a.ld_v - 1024 * (S::kCopies - 1), ko, vo, at,
                      at + S::kTile);
     };
     copy(0);
@@ -285,38 +302,48 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_prompt_kernel
 
     float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     total += __shfl_xor(total, 32, 64);
-    if (!live) return;
     const float inv = 1.0f / total;
-    uint16_t* y = a.out + (start + row) * a.ld_out + (int64_t)head * D + 4 * h;
+    // Lanes (c, 0) and (c, 1) hold alternate fours of values: they exchange a four of
+    // every pair of eights, and each stores one eight.
+    uint16_t* y = a.out + (start + row) * a.ld_out + (int64_t)head * D + 8 * h;
 #pragma unroll
     for (int i = 0; i < kOut; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint2*>(y + 32 * i + 8 * j) =
-                make_uint2(pack2(o[i][4 * j] * inv, o[i][4 * j + 1] * inv), pack2(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+        for (int j = 0; j < 4; j += 2) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const auto x = __builtin_amdgcn_permlane32_swap(
+                    pack2(o[i][4 * j + 2 * k] * inv, o[i][4 * j + 2 * k + 1] * inv),
+                    pack2(o[i][4 * j + 4 + 2 * k] * inv, o[i][4 * j + 4 + 2 * k + 1] * inv), false, false);
+                w[0][k] = x[0], w[1][k] = x[1];
+            }
+            if (live) *reinterpret_cast<uint4*>(y + 32 * i + 8 * j) = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+        }
 }
 
 }  // namespace
 
-// Workgroups per query head: the tile numbers of attn_prompt_kernel.
-int64_t attn_prompt_tiles(int64_t seqs, int64_t tokens) { return tokens / kRows + seqs; }
+// Row tiles per query head: the tile numbers of attn_prompt_kernel.
+int64_t attn_prompt_tiles(int64_t seqs, int64_t tokens, int head_dim) { return tokens / (32 * waves_of(head_dim)) + seqs; }
 
 hipError_t launch_attn_prompt(const AttnPrompt& p, hipStream_t s) {
     PromptArgs a{};
     a.q = p.q, a.k = p.k, a.v = p.v, a.out = p.out;
     a.ld_q = p.ld_q, a.ld_k = p.ld_k, a.ld_v = p.ld_v, a.ld_out = p.ld_out;
     a.cu = p.cu_seqlens, a.seqs = (int)p.seqs, a.q_heads = p.q_heads, a.group = p.q_heads / p.kv_heads;
-    a.tokens = p.tokens, a.tiles = (int)attn_prompt_tiles(p.seqs, p.tokens);
+    a.tokens = p.tokens, a.tiles = (int)attn_prompt_tiles(p.seqs, p.tokens, p.head_dim);
     // Never 0: a hidden score is -inf and has to stay that when scaled.
     a.scale2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
     a.flip = p.scale < 0 ? 0x80008000u : 0u;
     const unsigned grid = (unsigned)((int64_t)a.tiles * p.q_heads);
+    const unsigned threads = 64 * waves_of(p.head_dim);
     if (p.head_dim == 64)
-        attn_prompt_kernel<64><<<grid, kThreads, 0, s>>>(a);
+        attn_prompt_kernel<64><<<grid, threads, 0, s>>>(a);
     else if (p.head_dim == 128)
-        attn_prompt_kernel<128><<<grid, kThreads, 0, s>>>(a);
+        attn_prompt_kernel<128><<<grid, threads, 0, s>>>(a);
     else
-        attn_prompt_kernel<256><<<grid, kThreads, 0, s>>>(a);
+        attn_prompt_kernel<256><<<grid, threads, 0, s>>>(a);
     return hipGetLastError();
 }
 

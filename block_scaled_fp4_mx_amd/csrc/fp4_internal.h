@@ -192,7 +192,7 @@ struct AttnPrompt {
     uint16_t* out;
     int64_t ld_out;
 };
-int64_t attn_prompt_tiles(int64_t seqs, int64_t tokens);
+int64_t attn_prompt_tiles(int64_t seqs, int64_t tokens, int head_dim);
 hipError_t launch_attn_prompt(const AttnPrompt& p, hipStream_t s);
 
 }  // namespace fp4
