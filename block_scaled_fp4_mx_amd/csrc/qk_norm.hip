@@ -157,22 +157,36 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const QkNormArgs
     }
 }
 
+template <int kLanes, int kHeads>
+void launch(const QkNormArgs& a, int64_t tokens, bool interleaved, hipStream_t s) {
+    constexpr int kSpan = kThreads / kLanes * kHeads;
+    const dim3 grid((unsigned)tokens, (unsigned)((a.heads + kSpan - 1) / kSpan));
+    if (interleaved)
+        qk_norm_rope_kernel<kLanes, kHeads, true><<<grid, kThreads, 0, s>>>(a);
+    else
+        qk_norm_rope_kernel<kLanes, kHeads, false><<<grid, kThreads, 0, s>>>(a);
+}
+
 template <int kLanes>
 void launch(const QkNormArgs& a, int64_t tokens, bool interleaved, hipStream_t s) {
     constexpr int kGroups = kThreads / kLanes;
-    // Few tokens: one head per lane group, so the heads spread over workgroups.
-    const int per = tokens * a.heads >= (int64_t)kGroups * 4 * 1024 ? 4 : 1;
-    const dim3 grid((unsigned)tokens, (unsigned)((a.heads + kGroups * per - 1) / (kGroups * per)));
-    if (interleaved) {
-        if (per == 4)
-            qk_norm_rope_kernel<kLanes, 4, true><<<grid, kThreads, 0, s>>>(a);
-        else
-            qk_norm_rope_kernel<kLanes, 1, true><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (per == 4)
-            qk_norm_rope_kernel<kLanes, 4, false><<<grid, kThreads, 0, s>>>(a);
-        else
-            qk_norm_rope_kernel<kLanes, 1, false><<<grid, kThreads, 0, s>>>(a);
+    // Few tokens: one head to a lane group, so that the heads spread over the CUs.
+    // Else the number of 2 .. 5 that leaves the fewest groups without a head (the
+    // larger of two that leave as many).
+    int per = 1;
+    if (tokens * a.heads >= (int64_t)kGroups * 4 * 1024) {
+        int least = 1 << 30;
+        for (int k = 2; k <= 5; ++k) {
+            const int slots = (a.heads + kGroups * k - 1) / (kGroups * k) * k;
+            if (slots <= least) least = slots, per = k;
+        }
+    }
+    switch (per) {
+        case 1: return launch<kLanes, 1>(a, tokens, interleaved, s);
+        case 2: return launch<kLanes, 2>(a, tokens, interleaved, s);
+        case 3: return launch<kLanes, 3>(a, tokens, interleaved, s);
+        case 4: return launch<kLanes, 4>(a, tokens, interleaved, s);
+        default: return launch<kLanes, 5>(a, tokens, interleaved, s);
     }
 }
 
