@@ -1,6 +1,6 @@
 """Host-side refusals of the attention path's entry points: the documented
 status before any HIP call, and the binding's checks (no GPU needed)."""
-import ctypes
+import struct
 
 import pytest
 import torch
@@ -39,12 +39,12 @@ def test_norm_rope_rejections():
 
 def _cache(**kw):
     v = dict(k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, num_pages=10, d=64, page_size=16) | kw
-    return ctypes.byref(F._KvCacheC(*(v[n] for n, _ in F._KvCacheC._fields_)))
+    return struct.pack("=4Q3q", *(v[n] or 0 for n in v))
 
 
 def _pages(**kw):
     v = dict(page_table=FAKE, page_counts=FAKE, seq_lens=FAKE, page_refs=FAKE, batch=3, max_pages=4, num_pages=10) | kw
-    return ctypes.byref(F._KvPagesC(*(v[n] for n, _ in F._KvPagesC._fields_)))
+    return struct.pack("=4Q3q", *(v[n] or 0 for n in v))
 
 
 BAD_CACHES = [(dict(d=48), SHAPE), (dict(page_size=24), SHAPE), (dict(page_size=0), INVALID), (dict(num_pages=-1), INVALID),
