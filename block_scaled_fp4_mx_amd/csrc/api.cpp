@@ -541,6 +541,8 @@ int fp4_qk_norm_rope(const void* q, const void* k, int64_t tokens, int q_heads, 
         if (int e = check_ld(ld_k, wk, "ld_k")) return e;
         if (int e = check_ld(ld_ko, wk, "ld_ko")) return e;
     }
+    if (q_heads == 0) q_weight = nullptr;
+    if (kv_heads == 0) k_weight = nullptr;
     FP4_REQUIRE(aligned16(q_weight), FP4_ERR_ALIGN, "q_weight is not 16-byte aligned");
     FP4_REQUIRE(aligned16(k_weight), FP4_ERR_ALIGN, "k_weight is not 16-byte aligned");
     if (rot_dim) {
@@ -732,10 +734,10 @@ int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* 
     if (int e = check_heads(q_heads, kv_heads, head_dim)) return e;
     FP4_REQUIRE(seqs >= 0 && tokens >= 0, FP4_ERR_INVALID, "negative size seqs=%lld tokens=%lld", (long long)seqs,
                 (long long)tokens);
-    FP4_REQUIRE(tokens < (int64_t)1 << 31 && seqs < kMaxList, FP4_ERR_SHAPE, "tokens=%lld or seqs=%lld too large",
+    FP4_REQUIRE(tokens < (int64_t)1 << 30 && seqs < kMaxList, FP4_ERR_SHAPE, "tokens=%lld or seqs=%lld too large",
                 (long long)tokens, (long long)seqs);
-    FP4_REQUIRE(fp4::attn_prompt_tiles(seqs, tokens, head_dim) < ((int64_t)1 << 24) / q_heads, FP4_ERR_SHAPE,
-                "tokens=%lld, seqs=%lld and q_heads=%d give too many row tiles (2^24)", (long long)tokens, (long long)seqs,
+    FP4_REQUIRE(fp4::attn_prompt_tiles(seqs, tokens, head_dim) < ((int64_t)1 << 23) / q_heads, FP4_ERR_SHAPE,
+                "tokens=%lld, seqs=%lld and q_heads=%d give too many row tiles (2^23)", (long long)tokens, (long long)seqs,
                 q_heads);
     FP4_REQUIRE(std::isfinite(scale), FP4_ERR_INVALID, "scale is not finite");
     if (seqs == 0 || tokens == 0) return ok();
@@ -749,6 +751,8 @@ int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* 
     if (int e = check_ld(ld_k, wk, "ld_k")) return e;
     if (int e = check_ld(ld_v, wk, "ld_v")) return e;
     if (int e = check_ld(ld_out, wq, "ld_out")) return e;
+    FP4_REQUIRE(ld_k < (int64_t)1 << 24 && ld_v < (int64_t)1 << 24, FP4_ERR_SHAPE, "ld_k=%lld or ld_v=%lld too large (2^24)",
+                (long long)ld_k, (long long)ld_v);
     FP4_REQUIRE(!rows_overlap(out, ld_out * 2, wq * 2, q, ld_q * 2, wq * 2, tokens), FP4_ERR_INVALID, "out overlaps q");
     FP4_REQUIRE(!rows_overlap(out, ld_out * 2, wq * 2, k, ld_k * 2, wk * 2, tokens), FP4_ERR_INVALID, "out overlaps k");
     FP4_REQUIRE(!rows_overlap(out, ld_out * 2, wq * 2, v, ld_v * 2, wk * 2, tokens), FP4_ERR_INVALID, "out overlaps v");

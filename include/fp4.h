@@ -413,7 +413,9 @@ size_t fp4_moe_workspace_bytes(fp4_format fmt, int64_t tokens, int64_t hidden, i
  * q [tokens, ld_q], k [tokens, ld_k], q_out [tokens, ld_qo], k_out [tokens,
  * ld_ko]: bf16.  Either output may be its own input (same pointer and leading
  * dimension); any other overlap of an output with an input or the other output
- * is FP4_ERR_INVALID.  q_heads or kv_heads may be 0 (pointers then ignored).
+ * is FP4_ERR_INVALID.  q_heads or kv_heads may be 0 (its pointers are then
+ * ignored).  The squares are summed in fp32: a head whose sum passes 3e38 (values
+ * of 1e18 on) or whose values are no numbers comes out as the formula does there.
  * Errors: head_dim not a multiple of 16 in [16, 256], rot_dim not a multiple of
  * 16 in [0, head_dim], 2^24 tokens or more -> FP4_ERR_SHAPE; eps negative or not finite -> FP4_ERR_INVALID.
  */
@@ -474,7 +476,8 @@ typedef struct fp4_kv_pages {
  *   fp4_kv_append_mx.  May be NULL with max_new 0.
  *   *n_short: int32, 0, or how many pages the pool or the table rows lack; then
  *   nothing is reserved for any sequence and every slot is -1.
- * workspace: fp4_kv_reserve_workspace_bytes(batch, num_pages) bytes.
+ * workspace: fp4_kv_reserve_workspace_bytes(batch, num_pages) bytes; calls (and
+ * replays) that share one are ordered by the caller.
  */
 int fp4_kv_reserve(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* new_tokens, int32_t* slots,
                    int64_t max_new, int32_t* n_short, void* workspace, size_t workspace_bytes, void* stream);
@@ -485,7 +488,10 @@ size_t fp4_kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages);
  * target holds the source's committed tokens, sharing their pages; no row is
  * copied until one of the holders writes (fp4_kv_reserve).  A pair is skipped
  * when an id is outside [0, batch), the target still holds pages, an earlier
- * pair names the same target, or the source is a target of this call.
+ * pair names the same target, or the source is a target of this call.  Drafted
+ * tokens that the source has not committed are not shared; their rows on the
+ * page that is now shared stay where they are if it commits them afterwards, so
+ * fork between a commit and the next reservation.
  */
 int fp4_kv_fork(const fp4_kv_pages* pages, const int32_t* pairs, int64_t n, int64_t page_size, void* stream);
 
@@ -533,7 +539,9 @@ int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const in
  * j < draft_lens[b]:
  *   out = sum_j softmax_j(scale * q . k_j) v_j, softmax statistics and sums in
  *   fp32, keys and values dequantized exactly, weights rounded to bf16.
- * A row that sees nothing gives zeros.
+ * A row that sees nothing gives zeros, and cache rows that nobody sees may hold
+ * anything.  A drafted token's block whose scale leaves bf16's range (bytes 253 on)
+ * reaches only the rows that see it.
  * q: bf16 [batch * drafts, ld_q]; out: bf16 [batch * drafts, ld_out]; rows
  * i >= draft_lens[b] are left as they were.  draft_lens: int32 [batch], NULL =
  * drafts for all.  tree_mask: uint64 [batch, drafts], NULL = token i sees
@@ -541,7 +549,8 @@ int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const in
  * [batch].  Positions behind the table's end or on a page id outside
  * [0, num_pages) are not seen.
  * workspace: fp4_attn_tree_workspace_bytes(...) bytes, for the partial results
- * of contexts that are split over workgroups.  The order of the sums depends on
+ * of contexts that are split over workgroups; calls (and replays) that share one
+ * are ordered by the caller.  The order of the sums depends on
  * the shapes and lengths alone, so equal calls give equal bits.
  * Errors: head_dim not 64, 128 or 256, or cache->d != kv_heads * head_dim, or
  * q_heads not a multiple of kv_heads -> FP4_ERR_SHAPE; drafts outside [1, 64] ->
@@ -561,8 +570,11 @@ size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int
  * [cu_seqlens[s], cu_seqlens[s + 1]); empty sequences are fine, values are taken
  * as within [0, tokens], and rows outside every sequence are left as they were.
  * q [tokens, ld_q], k [tokens, ld_k], v [tokens, ld_v], out [tokens, ld_out]: bf16.
- * out may not overlap q, k or v.
- * Errors: head_dim not 64, 128 or 256, or q_heads not a multiple of kv_heads ->
+ * out may not overlap q, k or v.  A key or value that is infinite or no number
+ * reaches only the rows that see it.
+ * Errors: head_dim not 64, 128 or 256, q_heads not a multiple of kv_heads, ld_k
+ * or ld_v of 2^24 or more, 2^30 tokens or more, or 2^23 row tiles (of 128 rows, 256
+ * at head_dim 256; one more for every sequence) over all query heads ->
  * FP4_ERR_SHAPE; scale not finite -> FP4_ERR_INVALID.
  */
 int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int64_t seqs,

@@ -234,6 +234,21 @@ def test_attn_prompt_rejections():
     assert _prompt(tokens=0, q=None) == OK and _prompt(seqs=0, q=None) == OK
 
 
+def test_attn_prompt_refuses_what_its_offsets_cannot_hold():
+    """Rows of a tile are 32-bit offsets apart, and a launch has fewer than 2^32 threads."""
+    assert _prompt(ld_k=1 << 24) == SHAPE and _prompt(ld_v=1 << 24) == SHAPE and b"2^24" in F.lib.fp4_last_error()
+    assert _prompt(tokens=1 << 30, hq=1, hk=1) == SHAPE
+    assert _prompt(tokens=1 << 29, hq=4, hk=2, d=256, ld_q=1024, ld_k=512, ld_v=512, ld_out=1024) == SHAPE
+    assert b"row tiles" in F.lib.fp4_last_error()
+
+
+def test_weights_of_absent_heads_are_ignored():
+    """A dangling weight pointer of heads that a call has none of is no error: the
+    call is refused for its own fault only (a table that is missing)."""
+    assert _norm(hk=0, k=None, ko=None, kw=FAKE + 2, table=None) == INVALID
+    assert _norm(hq=0, q=None, qo=None, qw=FAKE + 2, table=None) == INVALID
+
+
 def test_binding_checks_the_prompt_attention():
     x = torch.zeros((8, 4, 64), dtype=torch.bfloat16)
     args = dict(q=x, k=x[:, :2], v=x[:, :2], cu_seqlens=_int(3), out=x.clone())
