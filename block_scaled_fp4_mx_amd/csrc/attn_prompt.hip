@@ -118,10 +118,11 @@ __device__ __forceinline__ void copy_tile(const uint8_t* k, const uint8_t* v, co
 // This wave's copies have landed and its LDS reads have returned, then all waves'.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-__device__ __forceinline__ float add_pair(float sum, uint32_t pair) {    // both bf16 of pair, in fp32
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), sum,
-                                           false);
+// sum + the products of two pairs of bf16, in fp32.
+__device__ __forceinline__ float add_products(float sum, uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), sum, false);
 }
+__device__ __forceinline__ float add_pair(float sum, uint32_t pair) { return add_products(sum, pair, 0x3F803F80u); }
 
 // First row of sequence s.  Its row tiles are numbered from row_of(s) / kRows + s
 // on, which leaves every sequence enough of them and needs no table of lengths.
@@ -193,7 +194,7 @@ __global__ __launch_bounds__(64 * waves_of(D), 2) void attn_prompt_kernel(const 
     };
     copy(0);
 
-    const int64_t row = q0 + 32 * wave + c;                  // this lane's query row
+    const int row = (int)q0 + 32 * wave + c;                 // this lane's query row
     const bool live = row < len;
     u32x4 q[kSteps];
     {
@@ -222,6 +223,7 @@ __global__ __launch_bounds__(64 * waves_of(D), 2) void attn_prompt_kernel(const 
     }
 
     const int wave_first = (int)q0 + 32 * wave;
+    bool apart = false;
     auto compute = [&](int t, const uint8_t* tile) {
         const int t0 = t * kTokens;
         v16f s[kSub];
@@ -240,8 +242,21 @@ __global__ __launch_bounds__(64 * waves_of(D), 2) void attn_prompt_kernel(const 
                                                                    __builtin_bit_cast(bf16x8, q[b * kBatch + i]), s[u], 0, 0, 0);
             }
         }
-        if (t0 + kTokens - 1 > wave_first) {                 // the diagonal
-            const int d = (int)row - t0;
+        if (t0 + kTokens - 1 > wave_first) {                 // the diagonal, in the wave's last tile
+            // A weight of 0 does not hide a value that is infinite or no number.  The wave's
+            // last tile holds its diagonal: if one of the tokens that some of its rows do
+            // not see has such a value (a product with 0 tells), it is taken apart below.
+            float odd = 0.f;
+            for (int u = (wave_first - t0) / 32; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 32 * S::kRow / 1024; ++i) {
+                    const u32x4 x = *reinterpret_cast<const u32x4*>(tile + S::kTile + 32 * u * S::kRow + 1024 * i + 16 * lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) odd = add_products(odd, x[j], 0);
+                }
+            apart = __any(odd != 0.f);
+            if (apart) return;
+            const int d = row - t0;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -299,6 +314,40 @@ __global__ __launch_bounds__(64 * waves_of(D), 2) void attn_prompt_kernel(const 
         turn(t + 1, tiles_lds + 2 * S::kTile);
     }
     if (t < tiles) turn(t, tiles_lds);
+
+    if (apart) {                                             // one token at a time
+#pragma unroll 1
+        for (int token = wave_first / kTokens * kTokens; token <= min(wave_first + 31, (int)len - 1); ++token) {
+            const uint8_t* x = kg + (int64_t)token * 2 * a.ld_k + 16 * h;
+            float score = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(x + 32 * s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) score = add_products(score, w[j], q[s][j]);
+            }
+            score += __shfl_xor(score, 32, 64);
+            const bool see = token <= row;
+            const float top = see ? score * a.scale2 : m, up = fmaxf(m, top), alpha = exp2_hw(m - up);
+            const uint32_t weight = pack2(see ? exp2_hw(fmaf(score, a.scale2, -up)) : 0.f, 0.f);
+            const float p = bf16_lo(weight);
+            m = up;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] *= alpha;
+            sum[0] += h ? 0.f : p;
+            const uint8_t* y = vg + (int64_t)token * 2 * a.ld_v + 8 * h;
+#pragma unroll
+            for (int i = 0; i < 4 * kOut; ++i) {
+                const uint2 w = *reinterpret_cast<const uint2*>(y + 16 * i);
+                const float v[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float old = o[i / 4][4 * (i % 4) + j] * alpha;
+                    o[i / 4][4 * (i % 4) + j] = see ? fmaf(p, v[j], old) : old;
+                }
+            }
+        }
+    }
 
     float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     total += __shfl_xor(total, 32, 64);

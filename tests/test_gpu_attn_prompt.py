@@ -79,6 +79,46 @@ def test_rising_scores_move_the_reference():
     b.run(0.1)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_hidden_keys_and_values_that_are_no_numbers(d):
+    """Only rows that see an infinite value or one that is no number have it, each in
+    its own place; rows that see such a key are no numbers."""
+    hq, hk, seqs = 4, 2, [(0, 330), (330, 400)]
+    b = Batch(8, [330, 70], hq, hk, d)
+    b.bits[[150, 290, 345, 399], hq + hk:] &= 0x807F         # tiny values where the bad ones will stand
+    bad = W.from_bits(b.bits).to(DEV)
+    expected = np.zeros((400, hq, d))                        # added to the result
+    for token, head, first, last, value in ((150, 0, 3, 4, np.nan), (150, 1, 0, d, np.inf), (290, 0, 17, 40, -np.inf),
+                                            (345, 1, 1, 2, np.nan), (399, 0, 0, d, np.nan)):
+        bad[token, hq + hk + head, first:last] = value
+        end = 330 if token < 330 else 400
+        expected[token:end, 2 * head:2 * head + 2, first:last] += value
+    for token, head in ((200, 0), (360, 1)):
+        bad[token, hq + head] = np.nan
+        expected[token:(330 if token < 330 else 400), 2 * head:2 * head + 2] = np.nan
+    out = torch.full((400, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    F.fp4_attn_prompt(bad[:, :hq], bad[:, hq:hq + hk], bad[:, hq + hk:], torch.from_numpy(b.cu).to(DEV), out)
+    q, k, v = np.split(b.bits, [hq, hq + hk], axis=1)
+    ref, size = A.attn_prompt(q, k, v, b.cu, d ** -0.5)
+    got = out.cpu().float().numpy()
+    odd = ~np.isfinite(expected)
+    np.testing.assert_array_equal(got[odd], expected[odd])
+    ref[odd] = np.nan
+    check(out, ref, size, d, 330, d ** -0.5, norm(q), norm(k), np.abs(FM.bf16_bits_to_f64(v)).max())
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    """Query, key, value and result rows 32 MB apart."""
+    b = Batch(9, [3, 130, 20], 4, 2, 64)
+    ld = (1 << 24) - 8
+    base = torch.empty(153 * ld, dtype=torch.bfloat16, device=DEV)
+    x = base.as_strided((153, 8, 64), (ld, 64, 1))
+    x.copy_(W.from_bits(b.bits).to(DEV))
+    out = base.as_strided((153, 4, 64), (ld, 64, 1), 1024)
+    out.fill_(7.0)
+    b.run(x=x, out=out)
+
+
 def test_separate_tensors_wide_rows_and_no_rows():
     b = Batch(5, [90, 40], 4, 2, 64)
     x = W.from_bits(b.bits).to(DEV)
