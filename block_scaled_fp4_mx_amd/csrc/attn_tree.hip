@@ -150,11 +150,18 @@ __device__ __forceinline__ uint32_t widen(uint32_t w, float scale) {
 __device__ __forceinline__ u32x4 widen8(uint32_t w, float scale) {
     return u32x4{widen<0>(w, scale), widen<1>(w, scale), widen<2>(w, scale), widen<3>(w, scale)};
 }
+// sum + the products of two pairs of bf16, in fp32.
+__device__ __forceinline__ float add_products(float sum, uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), sum, false);
+}
 // A block's scale from the aligned word that holds its byte: rotated so that the
 // byte stands in the exponent's bits; widen looks at no others.
 __device__ __forceinline__ float scale_of(uint32_t word, uint32_t turn) {
     return __uint_as_float(__builtin_amdgcn_alignbit(word, word, turn));
 }
+// Whether a block of this scale may hold values that are infinite in bf16 or no
+// numbers: 4 * 2^126 is.
+__device__ __forceinline__ bool is_huge(float scale) { return (__float_as_uint(scale) << 1) >> 24 >= 253; }
 constexpr uint32_t kOnes = 0x7F7F7F7Fu;    // scales of 1
 
 template <int N>
@@ -407,6 +414,7 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
             half_i += 2;
             return p;
         };
+        bool any_apart = false;
         const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
         auto compute = [&](int t, const Place& here, uint32_t stage) {
             const uint8_t* mine = staging + stage;
@@ -449,17 +457,22 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
 #pragma unroll
             for (int h = 0; h < 2; ++h) vscale[h] = *reinterpret_cast<const u32x4*>(mine + own.read_vs + 64 * h);
             if (edge) {
+                bool apart = false;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int pos = pos0 + 16 * (j / 4) + 4 * g + j % 4, d = pos - len;
                     const bool there = (pos < seen) & (here.row[j / 4] >= 0);
-                    vscale[j / 4][j % 4] = there ? vscale[j / 4][j % 4] : kOnes;      // whatever lies there, finite
+                    // Whatever lies there, finite; blocks that may not be are added apart (2^-127 of them here).
+                    const bool huge = there & (d >= 0) & is_huge(scale_of(vscale[j / 4][j % 4], own.vturn[j % 4]));
+                    apart |= huge;
+                    vscale[j / 4][j % 4] = huge ? 0u : there ? vscale[j / 4][j % 4] : kOnes;
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         const bool see = there & ((d < 0) | ((uint32_t)(vis[n] >> (d & 63)) & 1u));
                         s[n][j / 4][j % 4] = see ? s[n][j / 4][j % 4] : kNone;
                     }
                 }
+                any_apart |= __any(apart);
             }
             float top[NR];
             bool rises = false;
@@ -555,6 +568,53 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
                 if (t + 2 < t1) turn(t + 2, Int<2>());
             }
             meet<HW>();                                       // before the next sequence's copies
+        }
+        // A weight of 0 does not hide an infinite value, so the drafted tokens' blocks
+        // with such values are left out above and added here, to the rows that see them.
+        if (any_apart) {
+            constexpr int kBlocks = D == 256 ? 2 : 1;              // that a lane's D/4 values lie in
+            const int at_code = head * (D / 2) + g * (D / 8), at_scale = head * (D / 32) + (D == 64 ? g / 2 : kBlocks * g);
+#pragma unroll 1
+            for (int pos = max(t0 * kTile, len); pos < min(t1 * kTile, seen); ++pos) {
+                const int page = table[pos / a.page_size], d = pos - len;
+                if ((uint32_t)page >= (uint32_t)a.num_pages) continue;
+                const int64_t cache_row = (int64_t)page * a.page_size + pos % a.page_size;
+                const uint8_t* ks = a.ks + cache_row * a.scale_row + at_scale;
+                const uint8_t* vs = a.vs + cache_row * a.scale_row + at_scale;
+                const uint32_t* kc = reinterpret_cast<const uint32_t*>(a.kc + cache_row * a.code_row + at_code);
+                const uint32_t* vc = reinterpret_cast<const uint32_t*>(a.vc + cache_row * a.code_row + at_code);
+                float x[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) x[n] = 0.f;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const u32x4 k = widen8(kc[i], __uint_as_float((uint32_t)ks[i / 4] << 23));
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[n] = add_products(x[n], k[j], q[n][i][j]);
+                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    x[n] += __shfl_xor(x[n], 16, 64);
+                    x[n] += __shfl_xor(x[n], 32, 64);
+                    x[n] = bf16_lo(pack2(exp2_hw(fmaf(x[n], a.scale2, -m[n])), 0.f));
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const float scale = __uint_as_float((uint32_t)vs[i / 4] << 23);
+                    const u32x4 v = widen8(vc[i], scale);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int at_o = (8 * i + j) % kOut, e = (8 * i + j) / kOut;
+                            if (is_huge(scale) && (vis[n] >> (d & 63)) & 1)
+                                o[n][at_o][e] = fmaf(x[n], j & 1 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]), o[n][at_o][e]);
+                        }
+                }
+            }
         }
 
         const bool whole = t0 == 0 && t1 == tiles;

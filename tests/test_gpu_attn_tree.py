@@ -132,6 +132,85 @@ def test_what_is_not_seen_may_hold_anything():
     s.run()
 
 
+@pytest.mark.parametrize("d,q_heads,kv_heads,drafts", [(64, 4, 2, 6), (128, 16, 2, 6), (128, 8, 8, 9), (256, 4, 4, 5)])
+def test_drafted_values_past_the_range_reach_only_rows_that_see_them(d, q_heads, kv_heads, drafts):
+    """Blocks of drafted values with the largest scales: infinite in bf16 (code 7 at
+    2^126), near the end of its range (code 1) and no number (scale byte 255), in a
+    sequence of one piece and in one of several; rows that do not see them, and other
+    values of those that do, are as without."""
+    lens = [40, 2500]
+    s = Step(11, lens, drafts, q_heads, kv_heads, d, 64, masks=_tree(11, 2, drafts))
+    group, odd = q_heads // kv_heads, []
+    for b, n in enumerate(lens):
+        for token, block, code, scale in ((1, 0, 0x77, 253), (2, 1, 0x11, 253), (drafts - 1, kv_heads * d // 32 - 1, 0x22, 255)):
+            row = A.cache_rows(s.table[b], 64, len(s.kc) // 64, n + drafts)[n + token]
+            s.vc[row, 16 * block:16 * block + 16], s.vs[row, block] = code, 0
+            odd.append((b, token, block, row, scale))
+    a = s.device()
+    for *_, block, row, scale in odd:
+        a["cache"].v_scales[row, block] = scale
+    F.fp4_attn_tree_mx(**a)
+    ref, size = A.attn_tree_mx(s.q, s.kc, s.ks, s.vc, s.vs, 64, s.table, lens, kv_heads, d ** -0.5, None, s.masks)
+    got = a["out"].cpu().float().numpy()
+    k_norm = float(np.sqrt((Q.mx_dequant_f64(s.kc, s.ks).reshape(-1, d) ** 2).sum(-1)).max())
+    for b, token, block, row, scale in odd:
+        head, at = block * 32 // d, block * 32 % d
+        heads, values = slice(head * group, (head + 1) * group), slice(at, at + 32)
+        sees = np.array([int(s.masks[b, i]) >> token & 1 for i in range(drafts)], bool)
+        assert sees.any() and not sees.all()
+        if token == 2:                                       # finite: its own reference and magnitudes
+            s.vs[row, block] = scale
+            r, z = A.attn_tree_mx(s.q, s.kc, s.ks, s.vc, s.vs, 64, s.table, lens, kv_heads, d ** -0.5, None, s.masks)
+            s.vs[row, block] = 0
+            only = np.full_like(r, np.nan)
+            only[b, sees, heads, values] = r[b, sees, heads, values]
+            check(a["out"], only, z, d, 2500 + drafts, d ** -0.5, norm(s.q), k_norm, 2.0 ** 125)
+        else:
+            x = got[b, sees, heads, values]
+            assert (x == np.inf).all() if scale == 253 else not np.isfinite(x).any()
+        ref[b, sees, heads, values] = np.nan
+    check(a["out"], ref, size, d, 2500 + drafts, d ** -0.5, norm(s.q), k_norm, np.abs(Q.mx_dequant_f64(s.vc, s.vs)).max())
+
+
+def test_cache_offsets_past_32_bits_and_the_end_of_the_workspace():
+    """Pages beyond the first 4 GiB of codes, between others; bytes behind the workspace stay."""
+    heads, d, ps, pages = 16, 128, 64, 1 << 16               # codes: 4 GiB each
+    rng = np.random.default_rng(12)
+    s = Step(12, [700, 90], 3, 32, heads, d, ps)
+    small = s.device()
+    used = len(s.kc) // ps
+    far = np.sort(rng.choice(np.arange(pages - 64, pages), used, replace=False))[rng.permutation(used)]
+    far[::3] = rng.permutation(np.arange(1, 1 + len(far[::3])))
+    big = [torch.empty((pages * ps, x.shape[1]), dtype=torch.uint8, device=DEV) for x in small["cache"][:4]]
+    assert pages * ps * heads * d // 2 == 1 << 32
+    to, at = _i32(far), torch.arange(used, dtype=torch.int32, device=DEV)
+    cache = F.KvCache(*big, ps)
+    F.fp4_kv_copy_pages(small["cache"], cache, at, to)
+    back = F.KvCache(*(torch.zeros_like(x) for x in small["cache"][:4]), ps)
+    F.fp4_kv_copy_pages(cache, back, to, at)
+    assert all(torch.equal(x, y) for x, y in zip(back[:4], small["cache"][:4]))
+    table = np.where(s.table >= 0, far[np.maximum(s.table, 0)], -1).astype(np.int32)
+    size = F.fp4_attn_tree_workspace_bytes(*s.q.shape, heads)
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    F.fp4_attn_tree_mx(**small | dict(cache=cache, page_table=torch.from_numpy(table).to(DEV), workspace=ws[:size]))
+    s.check(small["out"])
+    assert (ws[size:] == 0xA5).all()
+
+
+def test_two_streams_with_a_workspace_each():
+    """Calls that run at once; each is as it is alone."""
+    steps = [Step(20 + i, [5000 + 700 * i, 10], 2, 8, 2, 128, 32) for i in range(2)]
+    args = [s.device() for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, stream in zip(args, streams):
+            F.fp4_attn_tree_mx(**a, stream=stream)
+    torch.cuda.synchronize()
+    for s, a in zip(steps, args):
+        s.check(a["out"])
+
+
 def test_ids_outside_the_pool_and_short_tables_are_not_seen():
     s = Step(6, [200, 100, 90, -5], 2, 4, 2, 64, 16)
     s.table[0, 3], s.table[0, 7], s.table[1, 0] = -1, 1 << 30, -9
