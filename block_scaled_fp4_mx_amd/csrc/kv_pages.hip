@@ -275,6 +275,18 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
     n = min(n, room);
     if (n == 0) return;
     if (accepted) {
+        // The page of the first uncommitted row may be shared by forks since the rows
+        // were reserved: it is written unless another holder's tokens reach that far.
+        const int64_t last = len / ps;
+        const int32_t first_page = len % ps ? t.page_table[b * t.max_pages + last] : -1;
+        bool alone = true;
+        if (first_page >= 0 && first_page < t.num_pages && t.page_refs[first_page] > 1) {
+            bool seen = false;
+            for (int64_t o = threadIdx.x; o < t.batch; o += kThreads)
+                seen |= o != b && last < held_pages(t, o) && t.page_table[o * t.max_pages + last] == first_page &&
+                        t.seq_lens[o] > len;
+            alone = !__syncthreads_or(seen);
+        }
         if (threadIdx.x < 64) {
             int64_t row[2] = {-1, -1};
             const int64_t i = threadIdx.x, a = i < n ? accepted[b * max_accepted + i] : -1;
@@ -283,7 +295,8 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
                 for (int k = 0; k < 2; ++k) {
                     const int64_t pos = len + (k ? i : a);
                     const int64_t page = t.page_table[b * t.max_pages + pos / ps];
-                    if (page >= 0 && page < t.num_pages && (k == 0 || t.page_refs[page] == 1)) row[k] = page * ps + pos % ps;
+                    if (page >= 0 && page < t.num_pages && (k == 0 || (page == first_page ? alone : t.page_refs[page] == 1)))
+                        row[k] = page * ps + pos % ps;
                 }
             }
             from[i] = row[1] < 0 ? -1 : row[0];

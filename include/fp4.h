@@ -489,9 +489,8 @@ size_t fp4_kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages);
  * copied until one of the holders writes (fp4_kv_reserve).  A pair is skipped
  * when an id is outside [0, batch), the target still holds pages, an earlier
  * pair names the same target, or the source is a target of this call.  Drafted
- * tokens that the source has not committed are not shared; their rows on the
- * page that is now shared stay where they are if it commits them afterwards, so
- * fork between a commit and the next reservation.
+ * tokens that the source has not committed are not shared; it may commit them
+ * afterwards.
  */
 int fp4_kv_fork(const fp4_kv_pages* pages, const int32_t* pairs, int64_t n, int64_t page_size, void* stream);
 
@@ -514,9 +513,9 @@ int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const
  * int32 [batch], taken as within [0, max_accepted].  accepted NULL: the first
  * accepted_lens[b] reserved tokens are committed where they are (max_accepted
  * ignored; the end of a prompt's append).  Rows move between pages that the
- * sequence holds, onto pages that nobody else holds (fp4_kv_reserve saw to
- * that), and the length never passes its pages; an accepted index that points
- * elsewhere moves nothing.
+ * sequence holds, onto rows that no other sequence sees (fp4_kv_reserve saw to
+ * that, and a fork since then shares committed rows only), and the length never
+ * passes its pages; an accepted index that points elsewhere moves nothing.
  */
 int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
                    int64_t max_accepted, const int32_t* accepted_lens, void* stream);

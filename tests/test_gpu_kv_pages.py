@@ -156,6 +156,32 @@ def test_accepted_rows_may_cross():
     s.compact(acc, [100, 100, -1])                      # lengths never pass the pages
 
 
+@pytest.mark.parametrize("committed", [10, 16, 40])
+def test_a_fork_between_a_reservation_and_its_commit(committed):
+    """The source still moves its accepted rows, on the page that is shared now; the
+    targets keep theirs and write into copies."""
+    s = Both(8, 4, 6, 24, 16, 64)
+    s.write(s.reserve([committed, 3, 0, 0], committed), 1)
+    s.compact(None, [committed, 3, 0, 0])
+    s.write(s.reserve([20, 1, 0, 0], 20), 2)
+    s.fork([(0, 2), (0, 3)])
+    s.compact([[19, 0, 7, 2, 18] + [0] * 15, [0] * 20, [0] * 20, [0] * 20], [5, 1, 0, 0])
+    s.write(s.reserve([2, 1, 8, 9], 9), 3)
+    s.compact([[1, 0], [0, 0], [7, 1], [8, 8]], [2, 1, 2, 2])
+
+
+def test_a_commit_without_a_reservation_moves_nothing_that_others_see():
+    s = Both(9, 2, 4, 8, 16, 64)
+    s.write(s.reserve([10, 0], 10), 1)
+    s.compact(None, [10, 0])
+    s.fork([(0, 1)])
+    s.free([0], [5])
+    before = [a.clone() for a in s.cache[:4]]
+    F.fp4_kv_compact(s.cache, s.pages, _i32([[3], [0]]), _i32([1, 0]))
+    assert all(torch.equal(a, b) for a, b in zip(s.cache[:4], before))
+    assert s.pages.seq_lens.tolist() == [6, 10]
+
+
 def test_ids_outside_are_not_followed():
     """Table entries outside the pool and counts outside the row: no access, no fault."""
     s = Both(8, 4, 4, 10, 16, 64)
