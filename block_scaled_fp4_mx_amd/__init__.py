@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import NamedTuple
 
 import torch
@@ -40,12 +39,6 @@ class MoeDebug(_c.Structure):
     _fields_ = [("x_codes", _vp), ("x_scales", _vp), ("counts", _vp), ("offsets", _vp), ("perm", _vp), ("gate_up", _vp),
                 ("h_bf16", _vp), ("h_codes", _vp), ("h_scales", _vp), ("y", _vp),
                 ("gate_up_in", _vp), ("h_codes_in", _vp), ("h_scales_in", _vp), ("stage_events", _vp * 6)]
-
-
-# struct fp4_kv_cache (k_codes, k_scales, v_codes, v_scales, num_pages, d, page_size) and
-# struct fp4_kv_pages (page_table, page_counts, seq_lens, page_refs, batch, max_pages,
-# num_pages): four pointers and three int64, passed as bytes.
-_pack_kv = struct.Struct("=4Q3q").pack
 
 
 _SIGS = {
@@ -104,6 +97,10 @@ def _load():
 
 
 lib = _load()
+try:
+    from . import _binding                  # csrc/binding.cpp; calls the same library
+except ImportError as e:
+    raise ImportError(f"_binding.so, which is built with {os.path.basename(LIB_PATH)}, does not load: {e}") from e
 
 
 class Fp4Error(RuntimeError):
@@ -119,7 +116,7 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_U8, _I32, _I64, _F32, _BF16 = (torch.uint8,), (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
+_U8, _I32, _F32, _BF16 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _OUT = (torch.bfloat16, torch.float32)
 
 
@@ -155,49 +152,6 @@ class _Args:
         for name, t in self.items:
             if t.device.type != "cuda":
                 raise ValueError(f"{self.fn}: {name} must be on the GPU, got a {t.device.type} tensor")
-
-
-def _check_all(fn, tensors):
-    """Checks (name, tensor, dtypes, dense) of a call as _Args does, in one pass.
-    Returns the GPU that all of them are on, or -1 (which _go reports, so that a
-    caller's own checks come before any device check)."""
-    dev = tensors[0][1].get_device() if isinstance(tensors[0][1], torch.Tensor) else -1
-    for name, t, dtypes, dense in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{fn}: {name} must be a torch tensor, got {type(t).__name__}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-        if not t.is_contiguous():
-            if t.stride(-1) != 1 and t.size(-1) > 1 and t.numel():
-                raise ValueError(f"{fn}: {name} must be contiguous along its last axis")
-            if dense and t.numel():
-                raise ValueError(f"{fn}: {name} must be contiguous")
-        if t.get_device() != dev:
-            dev = -1
-    return dev
-
-
-def _go(fn, dev, tensors, stream, *args):
-    """Calls the C entry point with args and the stream (by default the current
-    one of the tensors' GPU), with that GPU as the current device."""
-    if dev < 0:
-        for name, t, _, _ in tensors:
-            if t.device.type != "cuda":
-                raise ValueError(f"{fn}: {name} must be on the GPU, got a {t.device.type} tensor")
-        raise ValueError(f"{fn}: the tensors are on several GPUs: "
-                         + ", ".join(f"{name} on {t.device}" for name, t, _, _ in tensors))
-    if stream is None:
-        stream = _raw_stream(dev)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    f = getattr(lib, fn)
-    if torch.cuda.current_device() == dev:
-        status = f(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = f(*args, stream)
-    if status:
-        raise Fp4Error(fn, status)
 
 
 # The current stream's handle of a GPU by index, without a Stream object where torch has that.
@@ -350,12 +304,7 @@ def fp4_kv_append_mx(x, slots, cache_codes, cache_scales, tokens=None, d=None, l
     tokens = x.shape[0] if tokens is None else tokens
     d = x.shape[1] if d is None else d
     ld_x = x.stride(0) if ld_x is None else ld_x
-    fn = "fp4_kv_append_mx"
-    tensors = (("x", x, _BF16, False), ("slots", slots, _I32, True), ("cache_codes", cache_codes, _U8, True),
-               ("cache_scales", cache_scales, _U8, True))
-    dev = _check_all(fn, tensors)
-    _go(fn, dev, tensors, stream, x.data_ptr(), tokens, d, ld_x, slots.data_ptr(), cache_codes.data_ptr(),
-        cache_scales.data_ptr(), cache_codes.shape[0])
+    _check("fp4_kv_append_mx", _binding.fp4_kv_append_mx(x, slots, cache_codes, cache_scales, tokens, d, ld_x, stream))
 
 
 def fp4_fake_quant(fmt, x, out, tensor_scale=None, tensor_scale_is_input=False, workspace=None, rows=None, k=None,
@@ -494,54 +443,13 @@ def fp4_moe_grouped_gemm(fmt, x, topk_ids, topk_weights, num_experts, inter, w13
         _ptr(w2_tensor_scales), _ptr(act_tensor_scales), _ptr(out), _ptr(workspace), wsb, dbg, _stream(stream)))
 
 
-def _heads(fn, name, t):
-    """The leading dimension of a [tokens, heads, head_dim] tensor, whose heads
-    must lie one after another; tokens may be any number of elements apart."""
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{fn}: {name} must be [tokens, heads, head_dim], got shape {tuple(shape)}")
-    tokens, heads, d = shape
-    ld, head, _ = t.stride()
-    if head != d and heads > 1 and tokens and d:
-        raise ValueError(f"{fn}: the heads of {name} must be contiguous")
-    return ld if tokens > 1 else heads * d
-
-
 def fp4_qk_norm_rope(q, k, q_out, k_out, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, stream=None):
     """q [tokens, q_heads, head_dim], k [tokens, kv_heads, head_dim]: their rms
     norms and rotation into q_out and k_out (which may be q and k).  cos_sin:
     fp32 [max_positions, rot_dim]; None: norms only."""
-    fn = "fp4_qk_norm_rope"
-    tensors = [("q", q, _BF16, False), ("k", k, _BF16, False), ("q_out", q_out, _BF16, False), ("k_out", k_out, _BF16, False)]
-    weight = q_weight if q_weight is not None else k_weight
-    if q_weight is not None:
-        tensors.append(("q_weight", q_weight, _OUT, True))
-    if k_weight is not None:
-        tensors.append(("k_weight", k_weight, _OUT if q_weight is None else (q_weight.dtype,), True))
-    if cos_sin is not None:
-        tensors += (("cos_sin", cos_sin, _F32, True), ("positions", positions, _I32, True))
-    dev = _check_all(fn, tensors)
-    ld_q, ld_k, ld_qo, ld_ko = _heads(fn, "q", q), _heads(fn, "k", k), _heads(fn, "q_out", q_out), _heads(fn, "k_out", k_out)
-    tokens, q_heads, head_dim = shape = q.shape
-    k_tokens, kv_heads, k_dim = k_shape = k.shape
-    if k_tokens != tokens or k_dim != head_dim:
-        raise ValueError(f"{fn}: k has shape {tuple(k_shape)}, q {tuple(shape)}")
-    if q_out.shape != shape or k_out.shape != k_shape:
-        raise ValueError(f"{fn}: q_out and k_out must have the shapes of q and k")
-    for nm, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and w.shape != (head_dim,):
-            raise ValueError(f"{fn}: {nm} has shape {tuple(w.shape)}, expected {(head_dim,)}")
-    places = rot_dim = 0
-    table = where = None
-    if cos_sin is not None:
-        if cos_sin.dim() != 2 or positions.shape != (tokens,):
-            raise ValueError(f"{fn}: cos_sin must be [max_positions, rot_dim] and positions [tokens]")
-        places, rot_dim = cos_sin.shape
-        table, where = cos_sin.data_ptr(), positions.data_ptr()
-    _go(fn, dev, tensors, stream, q.data_ptr(), k.data_ptr(), tokens, q_heads, kv_heads, head_dim, ld_q, ld_k,
-        _ptr(q_weight), _ptr(k_weight), DT_BF16 if weight is None or weight.dtype is torch.bfloat16 else DT_F32, eps, table,
-        places, rot_dim, 1 if interleaved else 0, where, q_out.data_ptr(), ld_qo, k_out.data_ptr(), ld_ko)
+    _check("fp4_qk_norm_rope", _binding.fp4_qk_norm_rope(q, k, q_out, k_out, positions, cos_sin, q_weight, k_weight, eps,
+                                                         interleaved, stream))
 
 
 class KvCache(NamedTuple):
@@ -565,56 +473,6 @@ class KvPages(NamedTuple):
     page_refs: torch.Tensor
 
 
-def _cache_tensors(cache, name=""):
-    kc, ks, vc, vs, _ = cache
-    tensors = [(name + "k_codes", kc, _U8, True), (name + "k_scales", ks, _U8, True)]
-    if vc is not None:
-        tensors.append((name + "v_codes", vc, _U8, True))
-    if vs is not None:
-        tensors.append((name + "v_scales", vs, _U8, True))
-    return tensors
-
-
-def _pages_tensors(pages):
-    table, counts, lens, refs = pages
-    return [("page_table", table, _I32, True), ("page_counts", counts, _I32, True), ("seq_lens", lens, _I32, True),
-            ("page_refs", refs, _I32, True)]
-
-
-def _cache_struct(fn, cache):
-    """Checks the shapes of a KvCache's (checked) tensors; its C struct and d."""
-    kc, ks, vc, vs, page_size = cache
-    if (vc is None) != (vs is None):
-        raise ValueError(f"{fn}: v_codes and v_scales must both be given or both be None")
-    if kc.dim() != 2 or page_size <= 0 or len(kc) % page_size:
-        raise ValueError(f"{fn}: k_codes must be [num_pages * {page_size}, d/2], got {tuple(kc.shape)}")
-    rows, half = shape = kc.shape
-    scales = ks.shape
-    if scales != (rows, half // 16):
-        raise ValueError(f"{fn}: k_scales has shape {tuple(scales)}, expected {(rows, half // 16)}")
-    if vc is None:
-        return _pack_kv(kc.data_ptr(), ks.data_ptr(), 0, 0, rows // page_size, 2 * half, page_size), 2 * half
-    if vc.shape != shape or vs.shape != scales:
-        raise ValueError(f"{fn}: the cache's values must have the shapes of its keys")
-    return _pack_kv(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), rows // page_size, 2 * half, page_size), 2 * half
-
-
-def _pages_struct(fn, pages):
-    """Checks the shapes of a KvPages' (checked) tensors; its C struct and batch."""
-    table, counts, lens, refs = pages
-    shape = table.shape
-    if len(shape) != 2 or counts.shape != shape[:1] or lens.shape != shape[:1] or refs.dim() != 1:
-        raise ValueError(f"{fn}: page_table must be [batch, max_pages], page_counts and seq_lens [batch], "
-                         "page_refs [num_pages]")
-    batch, width = shape
-    return _pack_kv(table.data_ptr(), counts.data_ptr(), lens.data_ptr(), refs.data_ptr(), batch, width, len(refs)), batch
-
-
-def _per_seq(fn, name, t, n):
-    if t is not None and t.shape != (n,):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {(n,)}")
-
-
 def fp4_kv_reserve_workspace_bytes(batch: int, num_pages: int) -> int:
     return lib.fp4_kv_reserve_workspace_bytes(batch, num_pages)
 
@@ -622,156 +480,44 @@ def fp4_kv_reserve_workspace_bytes(batch: int, num_pages: int) -> int:
 def fp4_kv_reserve(cache: KvCache, pages: KvPages, new_tokens, slots, n_short, workspace, stream=None):
     """Room for new_tokens[b] tokens behind every sequence; their cache rows in
     slots [batch, max_new] (None: not wanted), -1 past new_tokens[b]."""
-    fn = "fp4_kv_reserve"
-    tensors = _cache_tensors(cache) + _pages_tensors(pages)
-    tensors += (("new_tokens", new_tokens, _I32, True), ("n_short", n_short, _I32, True), ("workspace", workspace, _U8, True))
-    if slots is not None:
-        tensors.append(("slots", slots, _I32, True))
-    dev = _check_all(fn, tensors)
-    c, _ = _cache_struct(fn, cache)
-    p, batch = _pages_struct(fn, pages)
-    _per_seq(fn, "new_tokens", new_tokens, batch)
-    _per_seq(fn, "n_short", n_short, 1)
-    max_new = 0
-    if slots is not None:
-        if slots.dim() != 2 or slots.shape[0] != batch:
-            raise ValueError(f"{fn}: slots has shape {tuple(slots.shape)}, expected [{batch}, max_new]")
-        max_new = slots.shape[1]
-    _go(fn, dev, tensors, stream, c, p, new_tokens.data_ptr(), _ptr(slots), max_new, n_short.data_ptr(), workspace.data_ptr(),
-        workspace.numel())
+    _check("fp4_kv_reserve", _binding.fp4_kv_reserve(cache, pages, new_tokens, slots, n_short, workspace, stream))
 
 
 def fp4_kv_fork(pages: KvPages, pairs, page_size: int, stream=None):
     """pairs int32 [n, 2]: (source, target) sequences."""
-    fn = "fp4_kv_fork"
-    tensors = _pages_tensors(pages)
-    tensors.append(("pairs", pairs, _I32, True))
-    dev = _check_all(fn, tensors)
-    p, _ = _pages_struct(fn, pages)
-    if pairs.dim() != 2 or pairs.shape[1] != 2:
-        raise ValueError(f"{fn}: pairs has shape {tuple(pairs.shape)}, expected [n, 2]")
-    _go(fn, dev, tensors, stream, p, pairs.data_ptr(), pairs.shape[0], page_size)
+    _check("fp4_kv_fork", _binding.fp4_kv_fork(pages, pairs, page_size, stream))
 
 
 def fp4_kv_free(pages: KvPages, seqs, page_size: int, keep_lens=None, stream=None):
     """Cuts the sequences seqs int32 [n] back to keep_lens int32 [n] tokens (None: none)."""
-    fn = "fp4_kv_free"
-    tensors = _pages_tensors(pages)
-    tensors.append(("seqs", seqs, _I32, True))
-    if keep_lens is not None:
-        tensors.append(("keep_lens", keep_lens, _I32, True))
-    dev = _check_all(fn, tensors)
-    p, _ = _pages_struct(fn, pages)
-    if seqs.dim() != 1:
-        raise ValueError(f"{fn}: seqs has shape {tuple(seqs.shape)}, expected [n]")
-    _per_seq(fn, "keep_lens", keep_lens, len(seqs))
-    _go(fn, dev, tensors, stream, p, seqs.data_ptr(), len(seqs), _ptr(keep_lens), page_size)
+    _check("fp4_kv_free", _binding.fp4_kv_free(pages, seqs, page_size, keep_lens, stream))
 
 
 def fp4_kv_compact(cache: KvCache, pages: KvPages, accepted, accepted_lens, stream=None):
     """Commits the drafted tokens accepted[b, :accepted_lens[b]] (None: the first
     accepted_lens[b] reserved ones) behind every sequence."""
-    fn = "fp4_kv_compact"
-    tensors = _cache_tensors(cache) + _pages_tensors(pages)
-    tensors.append(("accepted_lens", accepted_lens, _I32, True))
-    if accepted is not None:
-        tensors.append(("accepted", accepted, _I32, True))
-    dev = _check_all(fn, tensors)
-    c, _ = _cache_struct(fn, cache)
-    p, batch = _pages_struct(fn, pages)
-    _per_seq(fn, "accepted_lens", accepted_lens, batch)
-    most = 0
-    if accepted is not None:
-        if accepted.dim() != 2 or accepted.shape[0] != batch:
-            raise ValueError(f"{fn}: accepted has shape {tuple(accepted.shape)}, expected [{batch}, max_accepted]")
-        most = accepted.shape[1]
-        if most == 0:
-            return                                                    # nothing can be accepted
-    _go(fn, dev, tensors, stream, c, p, _ptr(accepted), most, accepted_lens.data_ptr())
+    _check("fp4_kv_compact", _binding.fp4_kv_compact(cache, pages, accepted, accepted_lens, stream))
 
 
 def fp4_kv_copy_pages(src: KvCache, dst: KvCache, src_pages, dst_pages, stream=None):
     """Page src_pages[i] of src to page dst_pages[i] of dst (int32 [n] each)."""
-    fn = "fp4_kv_copy_pages"
-    tensors = _cache_tensors(src, "src.") + _cache_tensors(dst, "dst.")
-    tensors += (("src_pages", src_pages, _I32, True), ("dst_pages", dst_pages, _I32, True))
-    dev = _check_all(fn, tensors)
-    (s, _), (d, _) = _cache_struct(fn, src), _cache_struct(fn, dst)
-    if src_pages.dim() != 1:
-        raise ValueError(f"{fn}: src_pages has shape {tuple(src_pages.shape)}, expected [n]")
-    _per_seq(fn, "dst_pages", dst_pages, len(src_pages))
-    _go(fn, dev, tensors, stream, s, d, src_pages.data_ptr(), dst_pages.data_ptr(), len(src_pages))
+    _check("fp4_kv_copy_pages", _binding.fp4_kv_copy_pages(src, dst, src_pages, dst_pages, stream))
 
 
 def fp4_attn_tree_workspace_bytes(batch: int, drafts: int, q_heads: int, head_dim: int, kv_heads: int) -> int:
     return lib.fp4_attn_tree_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads)
 
 
-def _drafted(fn, name, t):
-    """The pitch of the tokens of a [batch, drafts, q_heads, head_dim] tensor, which must be one."""
-    shape = t.shape
-    if len(shape) != 4:
-        raise ValueError(f"{fn}: {name} must be [batch, drafts, q_heads, head_dim], got shape {tuple(shape)}")
-    batch, drafts, heads, d = shape
-    seq, token, head, _ = t.stride()
-    empty = not (batch and drafts and heads and d)
-    if heads > 1 and head != d and not empty:
-        raise ValueError(f"{fn}: the heads of {name} must be contiguous")
-    ld = token if drafts > 1 else seq if batch > 1 else heads * d
-    if batch > 1 and seq != drafts * ld and not empty:
-        raise ValueError(f"{fn}: the tokens of {name} must be one pitch apart")
-    return ld
-
-
 def fp4_attn_tree_mx(q, cache: KvCache, page_table, seq_lens, out, workspace, draft_lens=None, tree_mask=None, scale=None,
                      stream=None):
     """q, out [batch, drafts, q_heads, head_dim]; tree_mask int64 [batch, drafts]
     (bit j: sees drafted token j; None: tokens up to itself); scale None: head_dim ** -0.5."""
-    fn = "fp4_attn_tree_mx"
-    tensors = [("q", q, _BF16, False), ("out", out, _BF16, False)]
-    tensors += _cache_tensors(cache)
-    tensors += (("page_table", page_table, _I32, True), ("seq_lens", seq_lens, _I32, True), ("workspace", workspace, _U8, True))
-    if draft_lens is not None:
-        tensors.append(("draft_lens", draft_lens, _I32, True))
-    if tree_mask is not None:
-        tensors.append(("tree_mask", tree_mask, _I64, True))
-    dev = _check_all(fn, tensors)
-    ld_q, ld_out = _drafted(fn, "q", q), _drafted(fn, "out", out)
-    batch, drafts, q_heads, head_dim = shape = q.shape
-    if out.shape != shape:
-        raise ValueError(f"{fn}: out has shape {tuple(out.shape)}, expected {tuple(shape)}")
-    c, d = _cache_struct(fn, cache)
-    if cache.v_codes is None:
-        raise ValueError(f"{fn}: the cache has no values")
-    if not head_dim or not d or d % head_dim:
-        raise ValueError(f"{fn}: the cache's rows hold {d} values, not a multiple of head_dim {head_dim}")
-    if page_table.dim() != 2 or page_table.shape[0] != batch:
-        raise ValueError(f"{fn}: page_table has shape {tuple(page_table.shape)}, expected [{batch}, max_pages]")
-    _per_seq(fn, "seq_lens", seq_lens, batch)
-    _per_seq(fn, "draft_lens", draft_lens, batch)
-    if tree_mask is not None and tree_mask.shape != (batch, drafts):
-        raise ValueError(f"{fn}: tree_mask has shape {tuple(tree_mask.shape)}, expected {(batch, drafts)}")
-    _go(fn, dev, tensors, stream, q.data_ptr(), ld_q, c, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
-        _ptr(draft_lens), _ptr(tree_mask), batch, drafts, q_heads, d // head_dim, head_dim,
-        head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ld_out, workspace.data_ptr(), workspace.numel())
+    _check("fp4_attn_tree_mx", _binding.fp4_attn_tree_mx(q, cache, page_table, seq_lens, out, workspace, draft_lens, tree_mask,
+                                                         scale, stream))
 
 
 def fp4_attn_prompt(q, k, v, cu_seqlens, out, scale=None, stream=None):
     """q, out [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim]:
     causal attention inside each sequence [cu_seqlens[s], cu_seqlens[s + 1])
     (int32 [seqs + 1]); scale None: head_dim ** -0.5."""
-    fn = "fp4_attn_prompt"
-    tensors = (("q", q, _BF16, False), ("k", k, _BF16, False), ("v", v, _BF16, False), ("out", out, _BF16, False),
-               ("cu_seqlens", cu_seqlens, _I32, True))
-    dev = _check_all(fn, tensors)
-    ld_q, ld_k, ld_v, ld_out = _heads(fn, "q", q), _heads(fn, "k", k), _heads(fn, "v", v), _heads(fn, "out", out)
-    tokens, q_heads, head_dim = shape = q.shape
-    k_tokens, kv_heads, k_dim = k_shape = k.shape
-    if k_tokens != tokens or k_dim != head_dim or v.shape != k_shape:
-        raise ValueError(f"{fn}: k and v have shapes {tuple(k_shape)} and {tuple(v.shape)}, q {tuple(shape)}")
-    if out.shape != shape:
-        raise ValueError(f"{fn}: out has shape {tuple(out.shape)}, expected {tuple(shape)}")
-    if cu_seqlens.dim() != 1 or len(cu_seqlens) < 1:
-        raise ValueError(f"{fn}: cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected [seqs + 1]")
-    _go(fn, dev, tensors, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), len(cu_seqlens) - 1, tokens,
-        q_heads, kv_heads, head_dim, ld_q, ld_k, ld_v, head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ld_out)
+    _check("fp4_attn_prompt", _binding.fp4_attn_prompt(q, k, v, cu_seqlens, out, scale, stream))
