@@ -4,33 +4,46 @@
 //   c = scale * log2(e), over the visible tokens j, in one pass: m is a running
 //   reference near the row's maximum, and o and the sum are scaled when it moves.
 //
-// Bound by HBM: a token's keys and values are 2 * (d/2 + d/32) bytes for all
-// its heads and are read once for all query rows of a sequence.  A wave takes
-// one key/value head and up to 16 * NR of the query rows that share it (drafts
-// times q_heads / kv_heads), and walks its tokens 32 at a time without LDS or
-// barriers: every operand is loaded in the layout the matrix core takes.
+// A wave takes one key/value head and up to 16 * NR of the query rows that share it
+// (drafts times q_heads / kv_heads), and walks its tokens 32 at a time.  The waves of
+// a workgroup take HW neighbouring heads of the same tokens, which they stage
+// together through LDS (Stage, copy_tile).
 //
 //   S^T = K Q^T on v_mfma_f32_16x16x32_bf16: lane (c = lane % 16, g = lane / 16)
-//   loads the quarter g of token c's row, one load for all K steps (the order of
-//   a row's values among the steps is free as long as Q is loaded alike), and
-//   widens it with its block scales (exact in bf16).
+//   reads the quarter g of token c's row (the order of a row's values among the
+//   steps is free as long as Q is loaded alike), and widens it with its block scales
+//   (exact in bf16).
 //   The result leaves lane (c, g) with query row c and tokens 4g .. 4g+3, which
 //   is what the B operand of O^T = V^T P^T takes if the token order within a
 //   step is (g, tile, i): the weights never leave their lane.
-//   V^T needs 8 tokens of one value per lane: a lane loads the same d/16 values
+//   V^T needs 8 tokens of one value per lane: a lane reads the same d/16 values
 //   of its 8 tokens (16 lanes cover the row), widens each with its token's
 //   scale, and pairs tokens with byte permutes.
 //   O^T leaves lane (c, g) with d/4 consecutive values of row c.
 //
 // The reference m moves only when some score exceeds it by more than 2^8 (one
 // ballot); until then no lane exchange is needed.  Weights are rounded to bf16
-// for the second product (they enter it with V's 16-bit format); their sum is
-// kept in fp32 from the unrounded weights.
+// for the second product (they enter it with V's 16-bit format); the rounded
+// weights are what is summed, in fp32, by one more matrix instruction with ones.
 //
 // Work split: the batch's tiles of 32 tokens are laid end to end and cut into
 // equal ranges, one per workgroup column, whatever the lengths; a sequence that
 // a cut goes through leaves partial (m, sum, o) in the workspace, at most two
 // per range, and a second kernel joins them in order.
+//
+// What bounds it: a token's keys and values are 2 * (d/2 + d/32) bytes and are read
+// once for all query rows of a sequence, which HBM would do at 5 TB/s; the
+// instructions that widen FP4, turn V and take the exponentials cost more.  At 32
+// rows a head a step of 32 tokens takes a wave about 560 instructions, of which 36
+// are matrix products, and a SIMD issues one in about 4.9 cycles with its two waves.
+// 64 / 8 heads of 128 values, kernel and join:
+//   64 sequences of 0 .. 8191 tokens, 8 drafts (287 MB)      115 + 13 us, 2.5 TB/s
+//   4 of 90001 .. 131072 tokens, 16 drafts (524 MB)          198 + 11 us, 2.5 TB/s
+//   one of 100000 tokens, 1 draft (109 MB)                    24 +  8 us, 4.5 TB/s
+//   one of 1500 tokens, 1 draft                              8.4 + 4.8 us, latency
+// Tried and slower: each wave loading its head in the matrix core's layout (first
+// case 128 us: half-line requests), 64 rows to a wave (154 us), three waves to a SIMD
+// (151 us, spills), 64 tokens a step (117 us), 1 row tile of 16 to a wave (162 us).
 #include <type_traits>
 
 #include "fp4_internal.h"
@@ -40,8 +53,13 @@ namespace fp4 {
 namespace {
 
 constexpr int kTile = 32;                  // tokens per step
-constexpr int kMinTiles = 2;               // tiles per range below which fewer ranges are used
-constexpr int kGridWaves = 2048;           // two per SIMD
+// Tiles per range below which fewer ranges are used.  One token over 1500, kernel and
+// join: 8.4 + 4.8 us; with 4, 12.2 + 4.0; with 1, 7.8 + 5.2, but over 8000 tokens
+// 11.8 + 5.6 against 11.2 + 4.8.
+constexpr int kMinTiles = 2;
+// Waves of a full grid, two per SIMD.  The long contexts above take 198 + 11 us; with
+// 1024 waves 236 + 14, with 4096 228 + 20 (twice the partial results).
+constexpr int kGridWaves = 2048;
 constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
 constexpr float kNone = -__builtin_inff();   // score of a hidden token
 constexpr float kFloor = -3e38f;           // reference of a row that has seen nothing
@@ -176,7 +194,9 @@ struct Place {
 // wave for each.  Rows are read from global memory in 16-byte chunks, neighbouring
 // lanes in neighbouring chunks of the heads' part of a row, straight into LDS: the
 // memory behind is bound by requests, and whole 128-byte lines make the fewest (a
-// head's part of a row alone is half a line at D = 128).  Every wave copies 1/HW
+// head's part of a row alone is half a line at D = 128).  4 heads to a workgroup
+// where their number allows, else 2 or 1: of the cases above the first takes 115 us
+// with 4 and 116 with 1, the second 196 and 203 (8 heads: 119 and 198).  Every wave copies 1/HW
 // of the rows, of all heads, into a region of its own:
 //   keys    32 rows of HW * D/32 chunks; chunk x of a row at x ^ key_turn(row), so
 //           that the 16 lanes that read one chunk of 16 rows meet different banks
@@ -328,7 +348,7 @@ __device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
 }
 
 template <int D, int NR, int HW>
-__global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
+__global__ __launch_bounds__(64 * HW, D == 256 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
     constexpr int kSteps = D / 32, kOut = D / 16;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     using S = Stage<D, HW>;
@@ -651,16 +671,16 @@ __global__ __launch_bounds__(64 * HW, D == 256 || HW == 8 ? 1 : 2) void attn_tre
     }
 }
 
-// Joins the partial results of the sequences that were cut: workgroup (x, y) 16
-// rows of a head (x) of sequence y.  A team of D/16 waves reads a piece as it was
-// written, 16 bytes a lane; kTeams of them take the pieces in turn, and their sums
-// are joined through LDS in team order.  The rows go out through LDS in 16-byte parts.
-template <int D, int kTeams>
-__global__ __launch_bounds__(4 * D * kTeams) void attn_tree_join_kernel(const TreeArgs a) {
-    constexpr int kTeam = 4 * D, kBatch = 8, kOut = D / 16;
+// Joins the partial results of the sequences that were cut: workgroup (x, y) takes
+// 16 rows of a head (x) of sequence y, and of their values the kPer slices from
+// kPer * z on (slice i: the values i, i + D/16, ...).  A wave reads a slice of a
+// piece as it was written, 16 bytes a lane; kTeams of kPer waves take the pieces in
+// turn, and their sums are joined through LDS in team order.
+template <int D, int kPer, int kTeams>
+__global__ __launch_bounds__(64 * kPer * kTeams) void attn_tree_join_kernel(const TreeArgs a) {
+    constexpr int kTeam = 64 * kPer, kBatch = 8, kOut = D / 16;
     __shared__ v4f sums[kTeams > 1 ? kTeam * kTeams : 1];
     __shared__ float2 stats[kTeams][16];
-    __shared__ __attribute__((aligned(16))) uint16_t rows[16][D + 8];
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int b = blockIdx.y, head = blockIdx.x / a.row_tiles, r0 = blockIdx.x % a.row_tiles * 16;
     Chunk chunk = chunk_at(a, 0, lane);
@@ -682,9 +702,9 @@ __global__ __launch_bounds__(4 * D * kTeams) void attn_tree_join_kernel(const Tr
     if (first == last) return;                                // one piece: written already
     // The first piece is its range's second one unless the range starts with it.
     const int first_slot = 2 * first + ((first * total >> shift) == before ? 0 : 1);
-    const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = part >> 6;
+    const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = kPer * blockIdx.z + (part >> 6);
     const int64_t step = (int64_t)a.kv_heads * a.row_tiles;
-    const v4f* o = reinterpret_cast<const v4f*>(a.part) + (int64_t)blockIdx.x * kTeam + part;
+    const v4f* o = reinterpret_cast<const v4f*>(a.part) + (int64_t)blockIdx.x * (4 * D) + 64 * i + lane;
     const float2* ml = reinterpret_cast<const float2*>(a.part + ((int64_t)2 << a.shift) * step * 16 * D) +
                        (int64_t)blockIdx.x * 16 + c;
 
@@ -701,7 +721,7 @@ __global__ __launch_bounds__(4 * D * kTeams) void attn_tree_join_kernel(const Tr
             if (x <= last) {
                 const int64_t at = (x == first ? first_slot : 2 * (int64_t)x) * step;
                 s[k] = ml[at * 16];
-                v[k] = o[at * kTeam];
+                v[k] = o[at * (4 * D)];
             }
         }
         float top = m;
@@ -736,17 +756,22 @@ __global__ __launch_bounds__(4 * D * kTeams) void attn_tree_join_kernel(const Tr
             }
         }
     }
-    if (team == 0) {
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    auto out_at = [&](int row) {
+        return a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out + ((int64_t)head * a.group + row % a.group) * D;
+    };
+    if constexpr (kPer == kOut) {                             // whole rows go out through LDS in 16-byte parts
+        __shared__ __attribute__((aligned(16))) uint16_t rows[16][D + 8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) rows[c][g * (D / 4) + k * kOut + i] = (uint16_t)pack2(acc[k] * inv, 0.f);
-    }
-    __syncthreads();
-    const int chunks = D / 8, r = threadIdx.x / chunks, row = r0 + r;
-    if (r < 16 && row < nd * a.group) {
-        uint16_t* y = a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out +
-                      ((int64_t)head * a.group + row % a.group) * D + threadIdx.x % chunks * 8;
-        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(&rows[r][threadIdx.x % chunks * 8]);
+        __syncthreads();
+        const int chunks = D / 8, r = threadIdx.x / chunks, at = threadIdx.x % chunks * 8;
+        if (r < 16 && r0 + r < nd * a.group)
+            *reinterpret_cast<uint4*>(out_at(r0 + r) + at) = *reinterpret_cast<const uint4*>(&rows[r][at]);
+    } else if (team == 0 && r0 + c < nd * a.group) {
+        uint16_t* y = out_at(r0 + c) + g * (D / 4) + i;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k * kOut] = (uint16_t)pack2(acc[k] * inv, 0.f);
     }
 }
 
@@ -754,11 +779,13 @@ __global__ __launch_bounds__(4 * D * kTeams) void attn_tree_join_kernel(const Tr
 struct Layout {
     int nr, waves, columns, shift;         // row tiles per wave, waves (heads) per workgroup, workgroups per range
 };
+// Two row tiles to a wave share the widened keys and values (above: 115 us, against
+// 162 with one); at 256 values their sums do not fit the registers.
 Layout layout_of(int drafts, int q_heads, int kv_heads, int head_dim) {
     const int rows = drafts * (q_heads / kv_heads);
     Layout l;
     l.nr = rows > 16 && head_dim <= 128 ? 2 : 1;
-    l.waves = kv_heads % 8 == 0 && head_dim <= 128 ? 8 : kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
+    l.waves = kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
     l.columns = kv_heads / l.waves * ((rows + 16 * l.nr - 1) / (16 * l.nr));
     // 2^shift ranges (at least 8, so that a range's workgroups meet on one XCD)
     l.shift = 3;
@@ -771,19 +798,18 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
     attn_tree_kernel<D, NR, HW><<<dim3(1u << l.shift, (unsigned)l.columns), 64 * HW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // Pieces of a sequence on average: whether several teams share a row tile.
-    const dim3 grid((unsigned)(a.kv_heads * a.row_tiles), (unsigned)a.batch);
-    if (1 << l.shift >= 16 * a.batch)
-        attn_tree_join_kernel<D, 256 / D><<<grid, 1024, 0, s>>>(a);
+    const unsigned row_tiles = (unsigned)(a.kv_heads * a.row_tiles);
+    // Many pieces of few rows (on average of the sequences, and so that all workgroups
+    // are resident): 16 waves to a slice.  One sequence of 100000 tokens: 8 us, against
+    // 37 with a wave to a slice; 4 of 131072 with 16 drafts: 16 us against 11.
+    if (1 << l.shift >= 16 * a.batch && (int64_t)row_tiles * a.batch * (D / 16) <= 512)
+        attn_tree_join_kernel<D, 1, 16><<<dim3(row_tiles, (unsigned)a.batch, D / 16), 1024, 0, s>>>(a);
     else
-        attn_tree_join_kernel<D, 1><<<grid, 4 * D, 0, s>>>(a);
+        attn_tree_join_kernel<D, D / 16, 1><<<dim3(row_tiles, (unsigned)a.batch), 4 * D, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int D, int NR>
 hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
-    if constexpr (D <= 128) {
-        if (l.waves == 8) return launch<D, NR, 8>(a, l, s);
-    }
     return l.waves == 4 ? launch<D, NR, 4>(a, l, s) : l.waves == 2 ? launch<D, NR, 2>(a, l, s) : launch<D, NR, 1>(a, l, s);
 }
 
