@@ -3,10 +3,9 @@
 //   o_i = sum_{j<=i} 2^(c s_ij - m_i) v_j / sum_{j<=i} 2^(c s_ij - m_i),
 //   s_ij = q_i . k_j,  c = scale * log2(e), in one pass over the keys.
 //
-// Bound by the matrix core (4 D flop per visible pair and query head).  A
-// workgroup of 4 waves takes 128 consecutive rows of one sequence and one query
-// head; a wave takes 32 of them against tiles of kTokens keys in LDS, all on
-// v_mfma_f32_32x32x16_bf16:
+// A workgroup of 4 waves (8 at D = 256) takes 32 consecutive rows a wave of one
+// sequence and one query head, against tiles of kTokens keys and values in LDS, all
+// on v_mfma_f32_32x32x16_bf16:
 //   S^T = K Q^T: lane (c = lane % 32, h = lane / 32) ends with query row c and
 //   tokens 8i + 4h .. 8i + 4h+3 of each 32, so a row's maximum and sum are lane
 //   local but for one exchange, and the weights are the B operand of
@@ -16,6 +15,17 @@
 // The running reference m moves only when a score exceeds it by more than 2^8.
 // Weights are rounded to bf16 for the second product (they enter it with V's
 // 16-bit format); the rounded weights are what is summed, in fp32.
+//
+// Bound by the matrix core (4 D flop per visible pair and query head):
+//   16384 rows, 32 / 4 heads of 128 values: 2.00 ms, 1.10 PFLOP/s (a large library
+//   product reaches 1.37 on the same card); matrix cores busy 58% of the cycles, at
+//   a clock that falls to 1.75 GHz under this load, the rest the exponentials and
+//   sums, which two waves on a SIMD overlap in part;
+//   4 prompts of 7676 rows in all, 64 / 8 heads: 345 us, 0.71 PFLOP/s: a workgroup's
+//   queries and results (56 us of traffic in all) pass while it computes nothing;
+//   24 prompts of 3 .. 421 rows, 16 / 16 heads of 64: 13 us, one round of workgroups.
+// Tried and slower or alike: tiles loaded through registers into padded LDS rows (2.41
+// ms), interleaving the two halves' products, s_setprio around them.
 #include "fp4_internal.h"
 #include "mma_core.h"
 

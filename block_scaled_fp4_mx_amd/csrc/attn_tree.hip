@@ -34,8 +34,10 @@
 // What bounds it: a token's keys and values are 2 * (d/2 + d/32) bytes and are read
 // once for all query rows of a sequence, which HBM would do at 5 TB/s; the
 // instructions that widen FP4, turn V and take the exponentials cost more.  At 32
-// rows a head a step of 32 tokens takes a wave about 560 instructions, of which 36
-// are matrix products, and a SIMD issues one in about 4.9 cycles with its two waves.
+// rows a head a step of 32 tokens takes a wave about 320 instructions, 34 of them
+// matrix products.  Of the 169 us that the second case below takes with its copies
+// left out, leaving out a kind more saves: products 70, conversions 35, exponentials
+// 33, turning V 15, the meeting of the waves 10.
 // 64 / 8 heads of 128 values, kernel and join:
 //   64 sequences of 0 .. 8191 tokens, 8 drafts (287 MB)      115 + 13 us, 2.5 TB/s
 //   4 of 90001 .. 131072 tokens, 16 drafts (524 MB)          198 + 11 us, 2.5 TB/s
