@@ -195,12 +195,15 @@ __global__ __launch_bounds__(64 * waves_of(D), 2) void attn_prompt_kernel(const 
     };
     offsets(kTokens);
     const int last_row = (int)min(q0 + kRows, len) - 1, tiles = last_row / kTokens + 1;
+    const uint8_t* next_k = kg - 1024 * (S::kCopies - 1);    // the next tile to copy
+    const uint8_t* next_v = vg - 1024 * (S::kCopies - 1);
+    const int64_t step_k = 2 * kTokens * a.ld_k, step_v = 2 * kTokens * a.ld_v;
     auto copy = [&](int t) {
-        const int64_t t0 = (int64_t)t * kTokens;
-        if (len - t0 < kTokens) offsets((int)(len - t0));    // the sequence's last tile
+        const int left = (int)len - t * kTokens;
+        if (left < kTokens) offsets(left);                   // the sequence's last tile
         const uint32_t at = lds + (t & 1) * 2 * S::kTile + wave * S::kCopies * 1024;
-        copy_tile<S::kCopies>(kg + t0 * 2 * a.ld_k - 1024 * (S::kCopies - 1), vg + t0 * 2 * a.ld_v - 1024 * (S::kCopies - 1), ko, vo, at,
-                     at + S::kTile);
+        copy_tile<S::kCopies>(next_k, next_v, ko, vo, at, at + S::kTile);
+        next_k += step_k, next_v += step_v;
     };
     copy(0);
 
