@@ -167,6 +167,29 @@ def _tree(q=FAKE, ld_q=512, cache=None, table=FAKE, width=4, lens=FAKE, nd=None,
                                   ld_out, ws, n, None)
 
 
+def test_binding_survives_what_is_no_cache_no_tensor_and_no_strided_tensor():
+    x = torch.zeros((4, 6, 64), dtype=torch.bfloat16)
+    pages = F.KvPages(_int(3, 4), _int(3), _int(3), _int(10))
+    with pytest.raises(TypeError, match="KvPages, got list"):
+        F.fp4_kv_fork(list(pages), _int(1, 2), 16)
+    with pytest.raises(TypeError, match="KvCache, got"):
+        F.fp4_kv_compact(pages, pages, _int(3, 4), _int(3))
+    with pytest.raises(TypeError, match="q must be a torch tensor, got NoneType"):
+        F.fp4_attn_prompt(None, x, x, _int(2), x)
+    with pytest.raises(TypeError):
+        F.fp4_kv_fork(pages, _int(1, 2), "16")
+    with pytest.raises(TypeError):
+        F.fp4_qk_norm_rope(x, x, x, x, eps="small")
+    with pytest.raises(OverflowError):
+        F.fp4_kv_fork(pages, _int(1, 2), 1 << 70)
+    with pytest.raises(ValueError, match="GPU, got a meta tensor"):
+        F.fp4_qk_norm_rope(x.to("meta"), x, x, x)
+    with pytest.raises((RuntimeError, ValueError)):
+        F.fp4_kv_fork(pages._replace(page_refs=_int(10).to_sparse()), _int(1, 2), 16)
+    with pytest.raises(TypeError, match="arguments"):
+        F._binding.fp4_kv_fork(pages)
+
+
 def test_attn_tree_rejections():
     for kw, status in BAD_CACHES:
         assert _tree(cache=_cache(**kw)) == status, kw

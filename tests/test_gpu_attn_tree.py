@@ -102,6 +102,18 @@ def test_ragged_batch_split_and_whole():
     Step(1, lens, 4, 8, 8, 64, 32, masks=_tree(1, len(lens), 4)).run()
 
 
+@pytest.mark.parametrize("d,q_heads,kv_heads,drafts", [(64, 24, 12, 9), (128, 16, 8, 9), (128, 12, 6, 4), (128, 15, 5, 2),
+                                                       (256, 8, 4, 4), (256, 10, 10, 3)])
+def test_ragged_batches_of_other_heads(d, q_heads, kv_heads, drafts):
+    lens = [1700, 0, 5, 64, 2049, 1, 300, 0, 0, 40, 31, 777]
+    Step(d + drafts, lens, drafts, q_heads, kv_heads, d, 32, masks=_tree(2, len(lens), drafts)).run()
+
+
+@pytest.mark.parametrize("d,q_heads,kv_heads,drafts", [(64, 8, 4, 2), (128, 8, 8, 4), (128, 32, 4, 5), (256, 8, 4, 1)])
+def test_one_long_context_in_many_pieces(d, q_heads, kv_heads, drafts):
+    Step(d, [17003], drafts, q_heads, kv_heads, d, 128).run()
+
+
 def test_more_sequences_than_lanes():
     rng = np.random.default_rng(2)
     lens = rng.integers(0, 130, 150).tolist()

@@ -66,6 +66,43 @@ def test_norm_rope_shapes(tokens, hq, hk, d, rot, interleaved):
     _check(q, k, qo, ko, wt.double().cpu().numpy(), cos_sin, positions, interleaved)
 
 
+@pytest.mark.parametrize("hq,hk,d,rot,interleaved", [(28, 4, 128, 128, False), (40, 8, 128, 64, True), (56, 8, 128, 96, False),
+                                                     (64, 8, 128, 128, True), (20, 4, 96, 64, True), (130, 7, 64, 64, False),
+                                                     (30, 3, 256, 256, False), (100, 25, 32, 32, True), (260, 5, 16, 16, False)])
+def test_many_tokens(hq, hk, d, rot, interleaved):
+    """Enough tokens that a group of lanes takes 2 to 5 heads; some of them checked."""
+    tokens = 4096 * 256 // (1 << max(1, (d // 8 - 1).bit_length())) // (hq + hk) + 3
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x = torch.randn((tokens, hq + hk, d), generator=g, device=DEV).bfloat16()
+    wt = (1 + 0.3 * torch.randn((2, d), generator=g, device=DEV)).float()
+    cos_sin = _table(300, rot)
+    positions = torch.randint(0, 300, (tokens,), generator=g, device=DEV).int()
+    qo = torch.full((tokens, hq, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ko = torch.full((tokens, hk, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    F.fp4_qk_norm_rope(x[:, :hq], x[:, hq:], qo, ko, positions, cos_sin, wt[0].contiguous(), wt[1].contiguous(),
+                       interleaved=interleaved)
+    some = torch.tensor([0, 1, 2, tokens // 2, tokens - 2, tokens - 1], device=DEV)
+    _check(x[some, :hq], x[some, hq:], qo[some], ko[some], wt.double().cpu().numpy(), cos_sin, positions[some], interleaved)
+    # every token's result depends on that token alone
+    q1, k1 = torch.empty_like(qo[:50]), torch.empty_like(ko[:50])
+    for t in range(0, tokens, 50):
+        n = min(50, tokens - t)
+        F.fp4_qk_norm_rope(x[t:t + n, :hq], x[t:t + n, hq:], q1[:n], k1[:n], positions[t:t + n], cos_sin, wt[0].contiguous(),
+                           wt[1].contiguous(), interleaved=interleaved)
+        assert torch.equal(q1[:n], qo[t:t + n]) and torch.equal(k1[:n], ko[t:t + n])
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    """Tokens 2 GiB apart."""
+    qkv, _ = _inputs(12, 4, 3, 1, 64)
+    ld = (1 << 30) + 8
+    base = torch.empty(3 * ld + 1024, dtype=torch.bfloat16, device=DEV)
+    x, out = base.as_strided((4, 4, 64), (ld, 64, 1)), base.as_strided((4, 4, 64), (ld, 64, 1), 512)
+    x.copy_(qkv[:, :4])
+    F.fp4_qk_norm_rope(x[:, :3], x[:, 3:], out[:, :3], out[:, 3:])
+    _check(qkv[:, :3], qkv[:, 3:4], out[:, :3], out[:, 3:], np.ones((2, 64)), None, None, False)
+
+
 def test_norms_alone_without_weights_and_zero_rows():
     qkv, _ = _inputs(3, 11, 4, 2, 128)
     qkv[4] = 0
