@@ -17,11 +17,11 @@
 // 16-bit format); the rounded weights are what is summed, in fp32.
 //
 // Bound by the matrix core (4 D flop per visible pair and query head):
-//   16384 rows, 32 / 4 heads of 128 values: 2.00 ms, 1.10 PFLOP/s (a large library
+//   16384 rows, 32 / 4 heads of 128 values: 1.94 ms, 1.13 PFLOP/s (a large library
 //   product reaches 1.37 on the same card); matrix cores busy 58% of the cycles, at
 //   a clock that falls to 1.75 GHz under this load, the rest the exponentials and
 //   sums, which two waves on a SIMD overlap in part;
-//   4 prompts of 7676 rows in all, 64 / 8 heads: 345 us, 0.71 PFLOP/s: a workgroup's
+//   4 prompts of 7676 rows in all, 64 / 8 heads: 291 us, 0.84 PFLOP/s: a workgroup's
 //   queries and results (56 us of traffic in all) pass while it computes nothing;
 //   24 prompts of 3 .. 421 rows, 16 / 16 heads of 64: 13 us, one round of workgroups.
 // Tried and slower or alike: tiles loaded through registers into padded LDS rows (2.41
