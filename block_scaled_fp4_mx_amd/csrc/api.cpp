@@ -674,7 +674,7 @@ int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const in
 
 size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
     if (batch <= 0 || drafts < 1 || drafts > 64 || check_heads(q_heads, kv_heads, head_dim) != FP4_OK) return 0;
-    return fp4::attn_tree_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads);
+    return fp4::attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
 }
 
 int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
@@ -703,7 +703,7 @@ int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, con
     FP4_REQUIRE((reinterpret_cast<uintptr_t>(tree_mask) & 7u) == 0, FP4_ERR_ALIGN, "tree_mask is not 8-byte aligned");
     FP4_REQUIRE(!rows_overlap(out, ld_out * 2, width * 2, q, ld_q * 2, width * 2, batch * drafts), FP4_ERR_INVALID,
                 "out overlaps q");
-    const size_t need = fp4::attn_tree_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads);
+    const size_t need = fp4::attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
     FP4_REQUIRE(workspace != nullptr && workspace_bytes >= need, FP4_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu",
                 need, workspace ? workspace_bytes : (size_t)0);
     FP4_REQUIRE(aligned16(workspace), FP4_ERR_ALIGN, "workspace is not 16-byte aligned");

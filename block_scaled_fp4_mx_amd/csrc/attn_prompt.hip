@@ -114,12 +114,12 @@ __device__ __forceinline__ void copy_tile(const uint8_t* k, const uint8_t* v, co
             "global_load_lds_dwordx4 %0, %8\n\t"
             "global_load_lds_dwordx4 %1, %8 offset:1024\n\t"
             "global_load_lds_dwordx4 %2, %8 offset:2048\n\t"
-            "global_load_lds_dwordx4 %3, %8 offset:3072\n\t"
+            "global_load_lds_dwordx4 %3, %8 offset:3*1024\n\t"
             "s_mov_b32 m0, %11\n\ts_nop 0\n\t"
             "global_load_lds_dwordx4 %4, %9\n\t"
             "global_load_lds_dwordx4 %5, %9 offset:1024\n\t"
             "global_load_lds_dwordx4 %6, %9 offset:2048\n\t"
-            "global_load_lds_dwordx4 %7, %9 offset:3072" ::"v"(ko[0]),
+            "global_load_lds_dwordx4 %7, %9 offset:3*1024" ::"v"(ko[0]),
             "v"(ko[1]), "v"(ko[2]), "v"(ko[3]), "v"(vo[0]), "v"(vo[1]), "v"(vo[2]), "v"(vo[3]), "s"(k), "s"(v), "s"(keys),
             "s"(values)
             : "memory", "m0");

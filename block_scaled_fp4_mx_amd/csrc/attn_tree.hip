@@ -314,9 +314,9 @@ __device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, con
                 "global_load_lds_dwordx4 %1, %5\n\t"
                 "global_load_lds_dwordx4 %2, %6 offset:1024\n\t"
                 "global_load_lds_dwordx4 %3, %7 offset:2048\n\t"
-                "global_load_lds_dword %8, off offset:3072" ::"v"(o.key[0]),
+                "global_load_lds_dword %8, off offset:3*1024" ::"v"(o.key[0]),
                 "v"(o.key[1]), "v"(o.value[0]), "v"(o.value[1]), "s"(a.kc + at0 + 1024), "s"(a.kc + at1),
-                "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048), "v"(scale - 3072), "s"(lds + 1024)
+                "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048), "v"(scale - 3 * 1024), "s"(lds + 1024)
                 : "memory", "m0");
         } else {
             asm volatile(
@@ -324,19 +324,19 @@ __device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, con
                 "global_load_lds_dwordx4 %0, %4\n\t"
                 "global_load_lds_dwordx4 %1, %5 offset:1024\n\t"
                 "global_load_lds_dwordx4 %2, %6 offset:2048\n\t"
-                "global_load_lds_dwordx4 %3, %7 offset:3072" ::"v"(o.key[0]),
+                "global_load_lds_dwordx4 %3, %7 offset:3*1024" ::"v"(o.key[0]),
                 "v"(o.key[1]), "v"(o.key[2]), "v"(o.key[3]), "s"(a.kc + at0), "s"(a.kc + at0 - 1024),
-                "s"(a.kc + at1 - 2048), "s"(a.kc + at1 - 3072), "s"(lds)
+                "s"(a.kc + at1 - 2048), "s"(a.kc + at1 - 3 * 1024), "s"(lds)
                 : "memory", "m0");
             asm volatile(
                 "s_mov_b32 m0, %10\n\ts_nop 0\n\t"
                 "global_load_lds_dwordx4 %0, %4 offset:-4096\n\t"
-                "global_load_lds_dwordx4 %1, %5 offset:-3072\n\t"
+                "global_load_lds_dwordx4 %1, %5 offset:-3*1024\n\t"
                 "global_load_lds_dwordx4 %2, %6 offset:-2048\n\t"
                 "global_load_lds_dwordx4 %3, %7 offset:-1024\n\t"
                 "global_load_lds_dword %8, off\n\t"
                 "global_load_lds_dword %9, off offset:256" ::"v"(o.value[0]),
-                "v"(o.value[1]), "v"(o.value[2]), "v"(o.value[3]), "s"(a.vc + at0 + 4096), "s"(a.vc + at0 + 3072),
+                "v"(o.value[1]), "v"(o.value[2]), "v"(o.value[3]), "s"(a.vc + at0 + 4096), "s"(a.vc + at0 + 3 * 1024),
                 "s"(a.vc + at1 + 2048), "s"(a.vc + at1 + 1024), "v"(scale), "v"(scale + 4 - 256), "s"(lds + 8192)
                 : "memory", "m0");
         }
@@ -817,8 +817,7 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
-    (void)batch;
+size_t attn_tree_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads) {
     const Layout l = layout_of(drafts, q_heads, kv_heads, head_dim);
     const size_t row_tiles = (size_t)(drafts * (q_heads / kv_heads) + 15) / 16;
     return ((size_t)2 << l.shift) * kv_heads * row_tiles * 16 * (head_dim + 2) * sizeof(float);

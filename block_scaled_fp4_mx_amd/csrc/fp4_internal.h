@@ -179,7 +179,7 @@ struct AttnTree {
     int64_t ld_out;
     void* ws;
 };
-size_t attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
+size_t attn_tree_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads);
 hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s);
 
 struct AttnPrompt {
