@@ -10,9 +10,10 @@
 //
 // All but copy_pages are bound by latency: a launch and two to four round trips to
 // memory.  64 sequences of 200 .. 4096 tokens in pages of 64 rows of 1024 values, 8
-// new tokens each: free 3.2 us, plan 7.0, apply 3.0, compact 7.6.  16 sequences forked
-// into 8 each: fork 4.3; plan 7.1 and apply 4.5 where each child copies its last page
-// (6.3 with one workgroup to a sequence instead of 8).
+// new tokens each: free 3.0 us, plan 6.3 (7.0 with the references asked for after the
+// sequences' needs), apply 2.6, compact 5.5 (7.7 with one array read after another).
+// 16 sequences forked into 8 each: fork 4.2; apply 4.5 where each child copies its last
+// page (6.3 with one workgroup to a sequence instead of 8).
 #include "fp4_internal.h"
 
 namespace fp4 {
@@ -57,20 +58,24 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {       // inc
     return v;
 }
 
-// Exclusive prefix of v over the workgroup; the sum over all threads in `total`.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
+// Exclusive prefix of v over the workgroup; the sums of v and w over all threads in
+// `total` and `total_w`.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t w, int64_t* sums, int64_t& total, int64_t& total_w) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t in = wave_scan(v, lane);
+    const int64_t in_w = __any(w != 0) ? wave_scan(w, lane) : 0;
     __syncthreads();                                                       // sums free again
-    if (lane == 63) sums[wave] = in;
+    if (lane == 63) sums[wave] = in, sums[kPlanWaves + wave] = in_w;
     __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
+    int64_t before = 0, all = 0, all_w = 0;
+#pragma unroll 4
     for (int i = 0; i < kPlanWaves; ++i) {
         before += i < wave ? sums[i] : 0;
         all += sums[i];
+        all_w += sums[kPlanWaves + i];
     }
     total = all;
+    total_w = all_w;
     return before + in - v;
 }
 
@@ -84,7 +89,15 @@ __device__ __forceinline__ int32_t held_pages(const fp4_kv_pages& t, int64_t b) 
 // last page needed.
 __global__ __launch_bounds__(kPlanThreads) void reserve_plan_kernel(fp4_kv_pages t, const int32_t* new_tokens,
                                                                     int64_t page_size, int32_t* n_short, ReserveWs ws) {
-    __shared__ int64_t sums[kPlanWaves];
+    __shared__ int64_t sums[2 * kPlanWaves];
+    // References of this lane's pages of a round; the first round's are on their way
+    // while the sequences' needs are worked out.
+    int32_t refs[kScanPages];
+    auto load_refs = [&](int64_t q) {
+#pragma unroll
+        for (int i = 0; i < kScanPages; ++i) refs[i] = q + i < t.num_pages ? t.page_refs[q + i] : 1;
+    };
+    load_refs((int64_t)threadIdx.x * kScanPages);
     int64_t want_all = 0, over_all = 0;
     for (int64_t b0 = 0; b0 < t.batch; b0 += kPlanThreads) {
         const int64_t b = b0 + threadIdx.x;
@@ -105,8 +118,7 @@ __global__ __launch_bounds__(kPlanThreads) void reserve_plan_kernel(fp4_kv_pages
             }
         }
         int64_t chunk, chunk_over;
-        const int64_t first = want_all + block_scan(want, sums, chunk);
-        block_scan(over, sums, chunk_over);
+        const int64_t first = want_all + block_scan(want, over, sums, chunk, chunk_over);
         want_all += chunk;
         over_all += chunk_over;
         p.first = (int32_t)min(first, (int64_t)0x7FFFFFFF);               // past the pool only in a refused call
@@ -115,12 +127,12 @@ __global__ __launch_bounds__(kPlanThreads) void reserve_plan_kernel(fp4_kv_pages
     int64_t found = 0;
     for (int64_t q0 = 0; q0 < t.num_pages && found < want_all; q0 += kPlanThreads * kScanPages) {
         const int64_t q = q0 + (int64_t)threadIdx.x * kScanPages;
+        if (q0) load_refs(q);
         uint32_t free_bits = 0;
 #pragma unroll
-        for (int i = 0; i < kScanPages; ++i)
-            if (q + i < t.num_pages && t.page_refs[q + i] == 0) free_bits |= 1u << i;
-        int64_t chunk;
-        int64_t rank = found + block_scan(__popc(free_bits), sums, chunk);
+        for (int i = 0; i < kScanPages; ++i) free_bits |= refs[i] == 0 ? 1u << i : 0u;
+        int64_t chunk, none;
+        int64_t rank = found + block_scan(__popc(free_bits), 0, sums, chunk, none);
         for (; free_bits && rank < want_all; ++rank, free_bits &= free_bits - 1)
             ws.taken[rank] = (int32_t)(q + __ffs(free_bits) - 1);
         found += chunk;
@@ -244,28 +256,52 @@ __global__ __launch_bounds__(kThreads) void free_kernel(fp4_kv_pages t, const in
     }
 }
 
-// Rows of one array (row_bytes apart and wide) to other rows of it, all reads of
-// a column before its writes.  from/to: rows in LDS, -1 = none.
+// The rows of one or two arrays (key and value codes, or scales) in units of T, and
+// their way through registers: units u0 .. u0 + w of n rows.  from/to: rows in LDS,
+// -1 = none.
 template <typename T>
-__device__ __forceinline__ void move_rows(uint8_t* base, int64_t row_bytes, const int64_t* from, const int64_t* to, int n) {
-    const int units = (int)(row_bytes / sizeof(T));
-    const int columns = min(kThreads * kMoveUnits / n, units);           // n <= 64: at least 32
-    for (int u0 = 0; u0 < units; u0 += columns) {
-        const int w = min(columns, units - u0), items = w * n;
-        T v[kMoveUnits];
+struct Rows {
+    uint8_t *a, *b;                          // b: NULL for one array
+    int64_t bytes;                           // of a row
+    int per, all;                            // units of an array's row, of both
+    __device__ Rows(uint8_t* x, uint8_t* y, int64_t row_bytes)
+        : a(x), b(y), bytes(row_bytes), per((int)(row_bytes / sizeof(T))), all(y ? 2 * per : per) {}
+    __device__ __forceinline__ T* at(int64_t row, int u) const {
+        return reinterpret_cast<T*>((u < per ? a : b) + row * bytes) + (u < per ? u : u - per);
+    }
+    __device__ __forceinline__ int width(int n) const { return min(kThreads * kMoveUnits / n, all); }   // n <= 64: at least 32
+    __device__ __forceinline__ void gather(T* v, int u0, int w, int n, const int64_t* from) const {
 #pragma unroll
         for (int k = 0; k < kMoveUnits; ++k) {
-            const int item = k * kThreads + threadIdx.x;
-            if (item < items && from[item / w] >= 0)
-                v[k] = reinterpret_cast<const T*>(base + from[item / w] * row_bytes)[u0 + item % w];
+            const int item = k * kThreads + threadIdx.x, i = item / w;
+            if (k * kThreads < w * n && item < w * n && from[i] >= 0) v[k] = *at(from[i], u0 + item - i * w);
         }
+    }
+    __device__ __forceinline__ void scatter(const T* v, int u0, int w, int n, const int64_t* from, const int64_t* to) const {
+#pragma unroll
+        for (int k = 0; k < kMoveUnits; ++k) {
+            const int item = k * kThreads + threadIdx.x, i = item / w;
+            if (k * kThreads < w * n && item < w * n && from[i] >= 0) *at(to[i], u0 + item - i * w) = v[k];
+        }
+    }
+};
+
+// All reads of a unit of the rows before its writes; as a rule (8 rows of 4096 values,
+// 64 of 512) everything is read before one meeting of the waves.
+template <typename T>
+__device__ __forceinline__ void move_rows(const fp4_kv_cache& c, const int64_t* from, const int64_t* to, int n) {
+    const Rows<u32x4> codes(c.k_codes, c.v_codes, c.d / 2);
+    const Rows<T> scales(c.k_scales, c.v_scales, c.d / 32);
+    const int cw = codes.width(n), sw = scales.width(n);
+    u32x4 v[kMoveUnits];
+    T s[kMoveUnits];
+    for (int u = 0, x = 0; u < codes.all || x < scales.all; u += cw, x += sw) {
+        const int nu = max(min(cw, codes.all - u), 0), nx = max(min(sw, scales.all - x), 0);
+        if (nu) codes.gather(v, u, nu, n, from);
+        if (nx) scales.gather(s, x, nx, n, from);
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kMoveUnits; ++k) {
-            const int item = k * kThreads + threadIdx.x;
-            if (item < items && from[item / w] >= 0)
-                reinterpret_cast<T*>(base + to[item / w] * row_bytes)[u0 + item % w] = v[k];
-        }
+        if (nu) codes.scatter(v, u, nu, n, from, to);
+        if (nx) scales.scatter(s, x, nx, n, from, to);
     }
 }
 
@@ -309,18 +345,10 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
             to[i] = row[1];
         }
         __syncthreads();
-        const int64_t cb = c.d / 2, sb = c.d / 32;
-        move_rows<uint4>(c.k_codes, cb, from, to, (int)n);
-        if (c.v_codes) move_rows<uint4>(c.v_codes, cb, from, to, (int)n);
-        for (int k = 0; k < (c.v_scales ? 2 : 1); ++k) {
-            uint8_t* s = k ? c.v_scales : c.k_scales;
-            if (sb % 16 == 0)
-                move_rows<uint4>(s, sb, from, to, (int)n);
-            else if (sb % 4 == 0)
-                move_rows<uint32_t>(s, sb, from, to, (int)n);
-            else
-                move_rows<uint8_t>(s, sb, from, to, (int)n);
-        }
+        if (c.d % 128 == 0)
+            move_rows<uint32_t>(c, from, to, (int)n);
+        else
+            move_rows<uint8_t>(c, from, to, (int)n);
     }
     __syncthreads();                                          // every wave has read the length
     if (threadIdx.x == 0) t.seq_lens[b] = (int32_t)(len + n);
