@@ -6,8 +6,8 @@
 //
 // A wave takes one key/value head and up to 16 * NR of the query rows that share it
 // (drafts times q_heads / kv_heads), and walks its tokens 32 at a time.  The waves of
-// a workgroup take HW neighbouring heads of the same tokens, which they stage
-// together through LDS (Stage, copy_tile).
+// a workgroup take HW neighbouring heads of the same tokens, and RG groups of rows,
+// and stage the tokens together through LDS (Stage, copy_tile).
 //
 //   S^T = K Q^T on v_mfma_f32_16x16x32_bf16: lane (c = lane % 16, g = lane / 16)
 //   reads the quarter g of token c's row (the order of a row's values among the
@@ -39,8 +39,8 @@
 // left out, leaving out a kind more saves: products 70, conversions 35, exponentials
 // 33, turning V 15, the meeting of the waves 10.
 // 64 / 8 heads of 128 values, kernel and join:
-//   64 sequences of 0 .. 8191 tokens, 8 drafts (287 MB)      115 + 13 us, 2.5 TB/s
-//   4 of 90001 .. 131072 tokens, 16 drafts (524 MB)          198 + 11 us, 2.5 TB/s
+//   64 sequences of 0 .. 8191 tokens, 8 drafts (287 MB)      113 + 13 us, 2.5 TB/s
+//   4 of 90001 .. 131072 tokens, 16 drafts (524 MB)          188 +  9 us, 2.7 TB/s
 //   one of 100000 tokens, 1 draft (109 MB)                    24 +  8 us, 4.5 TB/s
 //   one of 1500 tokens, 1 draft                              8.4 + 4.8 us, latency
 // Tried and slower: each wave loading its head in the matrix core's layout (first
@@ -59,8 +59,9 @@ constexpr int kTile = 32;                  // tokens per step
 // join: 8.4 + 4.8 us; with 4, 12.2 + 4.0; with 1, 7.8 + 5.2, but over 8000 tokens
 // 11.8 + 5.6 against 11.2 + 4.8.
 constexpr int kMinTiles = 2;
-// Waves of a full grid, two per SIMD.  The long contexts above take 198 + 11 us; with
-// 1024 waves 236 + 14, with 4096 228 + 20 (twice the partial results).
+// Waves of a full grid, two per SIMD.  The long contexts above, with one row group,
+// take 198 + 11 us; with 1024 waves 236 + 14, with 4096 228 + 20 (twice the partial
+// results).
 constexpr int kGridWaves = 2048;
 constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
 constexpr float kNone = -__builtin_inff();   // score of a hidden token
@@ -192,14 +193,12 @@ struct Place {
     int row[2];
 };
 
-// A workgroup's staging of a tile in LDS: HW neighbouring heads of 32 tokens, one
-// wave for each.  Rows are read from global memory in 16-byte chunks, neighbouring
+// A workgroup's staging of a tile in LDS: HW neighbouring heads of 32 tokens, a
+// region for each.  Rows are read from global memory in 16-byte chunks, neighbouring
 // lanes in neighbouring chunks of the heads' part of a row, straight into LDS: the
 // memory behind is bound by requests, and whole 128-byte lines make the fewest (a
-// head's part of a row alone is half a line at D = 128).  4 heads to a workgroup
-// where their number allows, else 2 or 1: of the cases above the first takes 115 us
-// with 4 and 116 with 1, the second 196 and 203 (8 heads: 119 and 198).  Every wave copies 1/HW
-// of the rows, of all heads, into a region of its own:
+// head's part of a row alone is half a line at D = 128).  Every region gets 1/HW of the
+// rows, of all heads:
 //   keys    32 rows of HW * D/32 chunks; chunk x of a row at x ^ key_turn(row), so
 //           that the 16 lanes that read one chunk of 16 rows meet different banks
 //   values  8 runs of 4 rows: run 4h + i has tokens 16h + 4g + i, g = 0 .. 3, which
@@ -213,8 +212,7 @@ struct Stage {
     static constexpr int kKeys = 16 * D, kValues = 16 * D, kWords = D == 256 ? 2 : 1;   // bytes, planes of a wave
     static constexpr int kBytes = kKeys + kValues + kWords * 256;
     static constexpr int kPlanes = HW * D >= 128 ? HW * D / 128 : 1;
-    static constexpr int kItems = kChunks / 2;                           // copies of keys, and of values, per wave
-    static constexpr int kCopies = 2 * kItems + kWords;
+    static constexpr int kItems = kChunks / 2;                           // copies of keys, and of values, per region
     __device__ static constexpr int key_turn(int row) {
         return kRow < 16 ? (row * kRow / 16) & (kRow - 1) : row & (kRow - 1) & 15;
     }
@@ -228,9 +226,9 @@ __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
 }
 // LDS reads issued so far have returned, in all waves of the workgroup.
-template <int HW>
+template <int kWaves>
 __device__ __forceinline__ void meet() {
-    if (HW > 1)
+    if (kWaves > 1)
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     else
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -284,41 +282,74 @@ __device__ __forceinline__ Lane<D, HW> lane_of(const TreeArgs& a, int head0, int
     return o;
 }
 
-// Starts a wave's copies of a tile into its region of the stage at lds (global
+// Starts a wave's copies of a tile into its head's region of the stage at lds (global
 // memory to LDS, lane l's 16 or 4 bytes to M0 + offset + l * size); awaited by
-// wait_copies.  Halves without a page read row 0 on (a row of the pool; hidden
-// later).  A wave's copies are one asm block behind one write of M0 (which needs a
-// wait state); the instruction's offset, -4096 to 4095, counts on the global side
-// as well, so each address is given less it.
-template <int D, int HW>
-__device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, const Lane<D, HW>& o, int wave, int lane,
+// wait_copies: everything with RG = 1; with two waves to a head the first one's keys
+// and scales, the second one's values.  Halves without a page read row 0 on (a row of
+// the pool; hidden later).  Copies are one asm block behind one write of M0 (which
+// needs a wait state); the instruction's offset, -4096 to 4095, counts on the global
+// side as well, so each address is given less it.
+template <int D, int HW, int RG>
+__device__ __forceinline__ void copy_tile(const TreeArgs& a, const Place& p, const Lane<D, HW>& o, int hw, int rg, int lane,
                                           uint32_t lds) {
-    const int row0 = max(p.row[0], 0), row1 = max(p.row[1], 0), mine = HW > 1 && wave < HW / 2 ? row0 : row1;
+    const int row0 = max(p.row[0], 0), row1 = max(p.row[1], 0), mine = HW > 1 && hw < HW / 2 ? row0 : row1;
     const uint8_t* scale = o.scale + (uint64_t)(uint32_t)(lane & 16 ? row1 : row0) * (uint32_t)a.scale_row;
     if constexpr (D == 64) {                              // HW = 1: both halves in one instruction
         const uint64_t at = (uint64_t)(uint32_t)(HW == 1 && !(lane & 32) ? row0 : mine) * (uint32_t)a.code_row;
-        asm volatile(
-            "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
-            "global_load_lds_dwordx4 %0, off\n\t"
-            "global_load_lds_dwordx4 %1, off offset:1024\n\t"
-            "global_load_lds_dword %2, off offset:2048" ::"v"(a.kc + at + o.key[0]),
-            "v"(a.vc + at + o.value[0] - 1024), "v"(scale - 2048), "s"(lds)
-            : "memory", "m0");
+        const uint8_t *key = a.kc + at + o.key[0], *value = a.vc + at + o.value[0];
+        if (RG == 1)
+            asm volatile(
+                "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, off\n\t"
+                "global_load_lds_dwordx4 %1, off offset:1024\n\t"
+                "global_load_lds_dword %2, off offset:2048" ::"v"(key),
+                "v"(value - 1024), "v"(scale - 2048), "s"(lds)
+                : "memory", "m0");
+        else if (rg == 0)
+            asm volatile(
+                "s_mov_b32 m0, %2\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, off\n\t"
+                "global_load_lds_dword %1, off offset:2048" ::"v"(key),
+                "v"(scale - 2048), "s"(lds)
+                : "memory", "m0");
+        else
+            asm volatile(
+                "s_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                "global_load_lds_dwordx4 %0, off offset:1024" ::"v"(value - 1024),
+                "s"(lds)
+                : "memory", "m0");
     } else {
         // HW = 1: the first half of the copies takes the tile's first half.
         const int64_t at0 = (int64_t)(HW == 1 ? row0 : mine) * a.code_row, at1 = HW == 1 ? (int64_t)row1 * a.code_row : at0;
         if constexpr (D == 128) {
-            asm volatile(
-                "s_mov_b32 m0, %9\n\ts_nop 0\n\t"
-                "global_load_lds_dwordx4 %0, %4 offset:-1024\n\t"
-                "global_load_lds_dwordx4 %1, %5\n\t"
-                "global_load_lds_dwordx4 %2, %6 offset:1024\n\t"
-                "global_load_lds_dwordx4 %3, %7 offset:2048\n\t"
-                "global_load_lds_dword %8, off offset:3*1024" ::"v"(o.key[0]),
-                "v"(o.key[1]), "v"(o.value[0]), "v"(o.value[1]), "s"(a.kc + at0 + 1024), "s"(a.kc + at1),
-                "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048), "v"(scale - 3 * 1024), "s"(lds + 1024)
-                : "memory", "m0");
+            if (RG == 1)
+                asm volatile(
+                    "s_mov_b32 m0, %9\n\ts_nop 0\n\t"
+                    "global_load_lds_dwordx4 %0, %4 offset:-1024\n\t"
+                    "global_load_lds_dwordx4 %1, %5\n\t"
+                    "global_load_lds_dwordx4 %2, %6 offset:1024\n\t"
+                    "global_load_lds_dwordx4 %3, %7 offset:2048\n\t"
+                    "global_load_lds_dword %8, off offset:3*1024" ::"v"(o.key[0]),
+                    "v"(o.key[1]), "v"(o.value[0]), "v"(o.value[1]), "s"(a.kc + at0 + 1024), "s"(a.kc + at1),
+                    "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048), "v"(scale - 3 * 1024), "s"(lds + 1024)
+                    : "memory", "m0");
+            else if (rg == 0)
+                asm volatile(
+                    "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+                    "global_load_lds_dwordx4 %0, %2 offset:-1024\n\t"
+                    "global_load_lds_dwordx4 %1, %3\n\t"
+                    "global_load_lds_dword %4, off offset:3*1024" ::"v"(o.key[0]),
+                    "v"(o.key[1]), "s"(a.kc + at0 + 1024), "s"(a.kc + at1), "v"(scale - 3 * 1024), "s"(lds + 1024)
+                    : "memory", "m0");
+            else
+                asm volatile(
+                    "s_mov_b32 m0, %4\n\ts_nop 0\n\t"
+                    "global_load_lds_dwordx4 %0, %2 offset:1024\n\t"
+                    "global_load_lds_dwordx4 %1, %3 offset:2048" ::"v"(o.value[0]),
+                    "v"(o.value[1]), "s"(a.vc + at0 - 1024), "s"(a.vc + at1 - 2048), "s"(lds + 1024)
+                    : "memory", "m0");
         } else {
+            static_assert(D != 256 || RG == 1);
             asm volatile(
                 "s_mov_b32 m0, %8\n\ts_nop 0\n\t"
                 "global_load_lds_dwordx4 %0, %4\n\t"
@@ -349,19 +380,19 @@ __device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
     return __builtin_amdgcn_perm(b, a, kHigh ? 0x07060302u : 0x05040100u);
 }
 
-template <int D, int NR, int HW>
-__global__ __launch_bounds__(64 * HW, D == 256 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
+template <int D, int NR, int HW, int RG>
+__global__ __launch_bounds__(64 * HW * RG, D == 256 ? 1 : 2) void attn_tree_kernel(const TreeArgs a) {
     constexpr int kSteps = D / 32, kOut = D / 16;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     using S = Stage<D, HW>;
     constexpr int kRegion = kStages * S::kBytes;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = a.kv_heads / HW;
-    const int head0 = __builtin_amdgcn_readfirstlane(blockIdx.y % groups) * HW, head = head0 + wave;
-    const int r0 = __builtin_amdgcn_readfirstlane(blockIdx.y / groups) * 16 * NR;
+    const int hw = wave % HW, rg = RG == 1 ? 0 : wave / HW;
+    const int head0 = __builtin_amdgcn_readfirstlane(blockIdx.y % groups) * HW, head = head0 + hw;
+    const int r0 = (__builtin_amdgcn_readfirstlane(blockIdx.y / groups) * RG + rg) * 16 * NR;
     __shared__ __attribute__((aligned(16))) uint8_t staging[HW * kRegion];
-    const uint32_t lds =
-        __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)staging) + wave * kRegion;
-    const Lane<D, HW> own = lane_of<D, HW>(a, head0, wave, lane);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)staging) + hw * kRegion;
+    const Lane<D, HW> own = lane_of<D, HW>(a, head0, hw, lane);
     Chunk chunk = chunk_at(a, 0, lane);
     const int64_t total = all_tiles(a, chunk, lane);
     const int shift = shift_of(a, total);
@@ -570,15 +601,19 @@ __global__ __launch_bounds__(64 * HW, D == 256 ? 1 : 2) void attn_tree_kernel(co
             Place at_stage[kStages];
             auto start = [&](int k) {
                 at_stage[k] = place();
-                copy_tile<D, HW>(a, at_stage[k], own, wave, lane, lds + k * S::kBytes);
+                copy_tile<D, HW, RG>(a, at_stage[k], own, hw, rg, lane, lds + k * S::kBytes);
             };
             auto turn = [&](int t, auto tag) {
                 constexpr int k = decltype(tag)::value;
-                if (t + 1 < t1)
-                    wait_copies<S::kCopies>();
-                else
+                if (t + 1 >= t1)
                     wait_copies<0>();
-                meet<HW>();
+                else if (RG == 1)
+                    wait_copies<2 * S::kItems + S::kWords>();
+                else if (rg == 0)
+                    wait_copies<S::kItems + S::kWords>();
+                else
+                    wait_copies<S::kItems>();
+                meet<HW * RG>();
                 if (t + 2 < t1) start((k + 2) % kStages);
                 compute(t, at_stage[k], k * S::kBytes);
             };
@@ -589,7 +624,7 @@ __global__ __launch_bounds__(64 * HW, D == 256 ? 1 : 2) void attn_tree_kernel(co
                 if (t + 1 < t1) turn(t + 1, Int<1>());
                 if (t + 2 < t1) turn(t + 2, Int<2>());
             }
-            meet<HW>();                                       // before the next sequence's copies
+            meet<HW * RG>();                                  // before the next sequence's copies
         }
         // A weight of 0 does not hide an infinite value, so the drafted tokens' blocks
         // with such values are left out above and added here, to the rows that see them.
@@ -779,25 +814,34 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_tree_join_kernel(cons
 
 // How the call is laid out, from its shapes alone.
 struct Layout {
-    int nr, waves, columns, shift;         // row tiles per wave, waves (heads) per workgroup, workgroups per range
+    int nr, heads, groups, columns, shift; // row tiles per wave, heads and row groups per workgroup, workgroups per range
 };
-// Two row tiles to a wave share the widened keys and values (above: 115 us, against
-// 162 with one); at 256 values their sums do not fit the registers.
+// Two row tiles to a wave share the widened keys and values (the cases at the top,
+// with one: 162 us and 284); at 256 values their sums do not fit the registers.  With
+// more rows than that, two waves of a workgroup take one head's tokens and share the
+// staged tiles.  A workgroup has at most 4 waves: the two cases take
+//   4 heads, 1 row group    114 + 13 us,  201 + 12 us
+//   2 heads, 2 row groups   113 + 13 us,  188 + 9 us
+//   4 heads, 2 row groups   118 + 13 us,  193 + 9 us
+//   1 head, 2 row groups    115 + 13 us,  195 + 10 us
+// (2 heads, 4 row groups: 195 + 9 us; 8 heads, 1 row group: 119 + 13, 198 + 10).
 Layout layout_of(int drafts, int q_heads, int kv_heads, int head_dim) {
     const int rows = drafts * (q_heads / kv_heads);
     Layout l;
     l.nr = rows > 16 && head_dim <= 128 ? 2 : 1;
-    l.waves = kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
-    l.columns = kv_heads / l.waves * ((rows + 16 * l.nr - 1) / (16 * l.nr));
+    l.groups = rows > 16 * l.nr && head_dim <= 128 ? 2 : 1;
+    l.heads = kv_heads % 4 == 0 && l.groups == 1 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
+    const int span = 16 * l.nr * l.groups;
+    l.columns = kv_heads / l.heads * ((rows + span - 1) / span);
     // 2^shift ranges (at least 8, so that a range's workgroups meet on one XCD)
     l.shift = 3;
-    while ((int64_t)l.columns * l.waves << (l.shift + 1) <= kGridWaves) ++l.shift;
+    while ((int64_t)l.columns * l.heads * l.groups << (l.shift + 1) <= kGridWaves) ++l.shift;
     return l;
 }
 
-template <int D, int NR, int HW>
+template <int D, int NR, int HW, int RG>
 hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
-    attn_tree_kernel<D, NR, HW><<<dim3(1u << l.shift, (unsigned)l.columns), 64 * HW, 0, s>>>(a);
+    attn_tree_kernel<D, NR, HW, RG><<<dim3(1u << l.shift, (unsigned)l.columns), 64 * HW * RG, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned row_tiles = (unsigned)(a.kv_heads * a.row_tiles);
@@ -810,9 +854,19 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
         attn_tree_join_kernel<D, D / 16, 1><<<dim3(row_tiles, (unsigned)a.batch), 4 * D, 0, s>>>(a);
     return hipGetLastError();
 }
-template <int D, int NR>
+template <int D, int NR, int RG>
 hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
-    return l.waves == 4 ? launch<D, NR, 4>(a, l, s) : l.waves == 2 ? launch<D, NR, 2>(a, l, s) : launch<D, NR, 1>(a, l, s);
+    if constexpr (RG == 1) {
+        if (l.heads == 4) return launch<D, NR, 4, RG>(a, l, s);
+    }
+    return l.heads == 2 ? launch<D, NR, 2, RG>(a, l, s) : launch<D, NR, 1, RG>(a, l, s);
+}
+template <int D>
+hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
+    if constexpr (D <= 128) {
+        if (l.nr == 2) return l.groups == 2 ? launch<D, 2, 2>(a, l, s) : launch<D, 2, 1>(a, l, s);
+    }
+    return launch<D, 1, 1>(a, l, s);
 }
 
 }  // namespace
@@ -839,9 +893,9 @@ hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
     a.flip = p.scale < 0 ? 0x80008000u : 0u;
     a.part = static_cast<float*>(p.ws), a.row_tiles = (a.rows + 15) / 16, a.shift = l.shift;
     switch (p.head_dim) {
-        case 64: return l.nr == 2 ? launch<64, 2>(a, l, s) : launch<64, 1>(a, l, s);
-        case 128: return l.nr == 2 ? launch<128, 2>(a, l, s) : launch<128, 1>(a, l, s);
-        default: return launch<256, 1>(a, l, s);
+        case 64: return launch<64>(a, l, s);
+        case 128: return launch<128>(a, l, s);
+        default: return launch<256>(a, l, s);
     }
 }
 
