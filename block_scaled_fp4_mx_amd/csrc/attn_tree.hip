@@ -46,6 +46,9 @@
 // Tried and slower: each wave loading its head in the matrix core's layout (first
 // case 128 us: half-line requests), 64 rows to a wave (154 us), three waves to a SIMD
 // (151 us, spills), 64 tokens a step (117 us), 1 row tile of 16 to a wave (162 us).
+// No faster: a tile's scores worked out beside the softmax of the one before (112 and
+// 190 us): the vector unit issues nearly all the time, the exponentials at a quarter
+// of its rate.
 #include <type_traits>
 
 #include "fp4_internal.h"
