@@ -47,8 +47,10 @@
 // case 128 us: half-line requests), 64 rows to a wave (154 us), three waves to a SIMD
 // (151 us, spills), 64 tokens a step (117 us), 1 row tile of 16 to a wave (162 us).
 // No faster: a tile's scores worked out beside the softmax of the one before (112 and
-// 190 us): the vector unit issues nearly all the time, the exponentials at a quarter
-// of its rate.
+// 190 us), three tiles in flight (113 and 191 us).  Counters of the second case: the
+// vector unit is issued to in 53% of the cycles (and holds exponentials longer), the
+// matrix core busy in 31%; a wave issues 45% of its time, waits 28% for a unit and 27%
+// for LDS and its workgroup.
 #include <type_traits>
 
 #include "fp4_internal.h"
