@@ -318,7 +318,11 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
     if (n == 0) return;
     if (accepted) {
         // The page of the first uncommitted row may be shared by forks since the rows
-        // were reserved: it is written unless another holder's tokens reach that far.
+        // were reserved: it is written unless another holder's tokens reach that far, or
+        // that holder commits in this call too.  Only one of them can have reserved rows
+        // there (a reservation copies a shared page), so the call is in error and neither
+        // writes.  A holder that commits counts by its accepted_lens, which stay as they
+        // are: its length is written by its own workgroup meanwhile.
         const int64_t last = len / ps;
         const int32_t first_page = len % ps ? t.page_table[b * t.max_pages + last] : -1;
         bool alone = true;
@@ -326,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
             bool seen = false;
             for (int64_t o = threadIdx.x; o < t.batch; o += kThreads)
                 seen |= o != b && last < held_pages(t, o) && t.page_table[o * t.max_pages + last] == first_page &&
-                        t.seq_lens[o] > len;
+                        (accepted_lens[o] > 0 || t.seq_lens[o] > len);
             alone = !__syncthreads_or(seen);
         }
         if (threadIdx.x < 64) {

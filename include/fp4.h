@@ -515,7 +515,9 @@ int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const
  * ignored; the end of a prompt's append).  Rows move between pages that the
  * sequence holds, onto rows that no other sequence sees (fp4_kv_reserve saw to
  * that, and a fork since then shares committed rows only), and the length never
- * passes its pages; an accepted index that points elsewhere moves nothing.
+ * passes its pages; an accepted index that points elsewhere moves nothing.  Of two
+ * sequences that hold one partly filled page, at most one can have reserved rows on
+ * it: if accepted_lens names both, rows on that page stay as they are.
  */
 int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
                    int64_t max_accepted, const int32_t* accepted_lens, void* stream);

@@ -180,17 +180,34 @@ class Pages:
                 self.table[b, p] = -1
             self.counts[b], self.lens[b] = self.pages_of(n), n
 
+    def may_write(self, b, page, lens, accepted_lens):
+        """Whether sequence b may move rows onto a page: it holds it alone, or it is the
+        page of its first uncommitted row, and no other holder's tokens reach as far,
+        nor does another holder commit in the same call."""
+        if self.refs[page] == 1:
+            return True
+        last = lens[b] // self.page_size
+        if lens[b] % self.page_size == 0 or self.table[b, last] != page:
+            return False
+        return not any(o != b and last < self.counts[o] and self.table[o, last] == page and
+                       (accepted_lens[o] > 0 or lens[o] > lens[b]) for o in range(len(self.table)))
+
     def compact(self, accepted, accepted_lens):
-        for b in range(len(self.table)):
-            n, room = int(self.lens[b]), int(self.counts[b]) * self.page_size - int(self.lens[b])
+        lens = [int(n) for n in self.lens]
+        for b, n in enumerate(lens):
+            room = int(self.counts[b]) * self.page_size - n
             m = max(int(accepted_lens[b]), 0)
             if accepted is not None:
                 m = min(m, accepted.shape[1])
             m = min(m, room)
-            for a in self.arrays if accepted is not None else []:
-                before = a.copy()
-                for i in range(m):
-                    j = int(accepted[b, i])
-                    if 0 <= j < room:
-                        a[self.row(b, n + i)] = before[self.row(b, n + j)]
+            moves = []
+            for i in range(m if accepted is not None else 0):
+                j = int(accepted[b, i])
+                if 0 <= j < room and j != i:
+                    to = self.row(b, n + i)
+                    if self.may_write(b, to // self.page_size, lens, accepted_lens):
+                        moves.append((self.row(b, n + j), to))
+            for a in self.arrays if moves else []:
+                source, to = np.array(moves).T
+                a[to] = a[source]
             self.lens[b] += m

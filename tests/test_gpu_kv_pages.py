@@ -182,6 +182,19 @@ def test_a_commit_without_a_reservation_moves_nothing_that_others_see():
     assert s.pages.seq_lens.tolist() == [6, 10]
 
 
+@pytest.mark.parametrize("forks", [2, 8, 70])
+def test_sharers_that_commit_unreserved_rows_in_one_call_move_nothing(forks):
+    """Each of them sees as far as the others, and all lengths grow in the call: whose
+    workgroup comes first may not matter."""
+    s = Both(11, forks, 4, 2 * forks, 16, 64)
+    s.write(s.reserve([10] + [0] * (forks - 1), 10), 1)
+    s.compact(None, [10] + [0] * (forks - 1))
+    s.fork([(0, i) for i in range(1, forks)])
+    before = [a.clone() for a in s.cache[:4]]
+    s.compact([[1 + (b + i) % 5 for i in range(3)] for b in range(forks)], [1 + b % 3 for b in range(forks)])
+    assert all(torch.equal(a, b) for a, b in zip(s.cache[:4], before))
+
+
 def test_ids_outside_are_not_followed():
     """Table entries outside the pool and counts outside the row: no access, no fault."""
     s = Both(8, 4, 4, 10, 16, 64)
