@@ -21,8 +21,8 @@ __all__ = [
     "fp4_dequant", "fp4_gemm", "fp4_quantize_mxfp8", "fp4_mx_to_mxfp8", "fp4_mx_dequant_fp8", "fp4_gemm_w4a8", "fp4_fake_quant",
     "fp4_ste_backward", "fp4_kv_append_mx", "fp4_moe_grouped_gemm", "fp4_moe_workspace_bytes", "MoeDebug",
     "fp4_qk_norm_rope", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
-    "fp4_kv_free", "fp4_kv_compact", "fp4_kv_copy_pages", "fp4_attn_tree_mx", "fp4_attn_tree_workspace_bytes",
-    "fp4_attn_prompt",
+    "fp4_kv_free", "fp4_kv_compact", "fp4_kv_compact_reserved", "fp4_kv_copy_pages", "fp4_attn_tree_mx",
+    "fp4_attn_tree_workspace_bytes", "fp4_attn_prompt",
     "fp4_abi_version", "LIB_PATH",
 ]
 
@@ -70,6 +70,7 @@ _SIGS = {
     "fp4_kv_fork": (_i32, [_vp, _vp, _i64, _i64, _vp]),
     "fp4_kv_free": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp]),
     "fp4_kv_compact": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp]),
+    "fp4_kv_compact_reserved": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp]),
     "fp4_kv_copy_pages": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp]),
     "fp4_attn_tree_mx": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _c.c_float, _vp,
                                 _i64, _vp, _sz, _vp]),
@@ -495,8 +496,16 @@ def fp4_kv_free(pages: KvPages, seqs, page_size: int, keep_lens=None, stream=Non
 
 def fp4_kv_compact(cache: KvCache, pages: KvPages, accepted, accepted_lens, stream=None):
     """Commits the drafted tokens accepted[b, :accepted_lens[b]] (None: the first
-    accepted_lens[b] reserved ones) behind every sequence."""
+    accepted_lens[b] reserved ones) behind every sequence; accepted_lens has to be 0
+    where nothing was reserved."""
     _check("fp4_kv_compact", _binding.fp4_kv_compact(cache, pages, accepted, accepted_lens, stream))
+
+
+def fp4_kv_compact_reserved(cache: KvCache, pages: KvPages, accepted, accepted_lens, slots, stream=None):
+    """fp4_kv_compact for the tokens of one fp4_kv_reserve, by the slots
+    [batch, max_new] that it gave them: commits what it granted, nothing after a refusal."""
+    _check("fp4_kv_compact_reserved",
+           _binding.fp4_kv_compact_reserved(cache, pages, accepted, accepted_lens, slots, stream))
 
 
 def fp4_kv_copy_pages(src: KvCache, dst: KvCache, src_pages, dst_pages, stream=None):

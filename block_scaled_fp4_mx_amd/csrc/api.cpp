@@ -144,6 +144,22 @@ int check_heads(int q_heads, int kv_heads, int head_dim) {
     return FP4_OK;
 }
 
+// slots: of the reservation whose rows are committed, or NULL.
+int kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted, int64_t max_accepted,
+               const int32_t* accepted_lens, const int32_t* slots, int64_t max_new, void* stream, const char* what) {
+    if (int e = check_cache(cache, false)) return e;
+    if (int e = check_pages(pages)) return e;
+    if (int e = check_same_pool(cache, pages)) return e;
+    FP4_REQUIRE(!accepted || (max_accepted >= 0 && max_accepted <= 64), FP4_ERR_INVALID,
+                "max_accepted=%lld outside [0, 64]", (long long)max_accepted);
+    if (pages->batch == 0 || cache->num_pages == 0 || cache->d == 0) return ok();
+    if (accepted) { FP4_SCALAR_PTR(accepted); }
+    FP4_SCALAR_PTR(accepted_lens);
+    return hip_status(fp4::launch_kv_compact(*cache, *pages, accepted, max_accepted, accepted_lens, slots, max_new,
+                                             static_cast<hipStream_t>(stream)),
+                      what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -640,17 +656,16 @@ int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const
 
 int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted, int64_t max_accepted,
                    const int32_t* accepted_lens, void* stream) {
-    if (int e = check_cache(cache, false)) return e;
-    if (int e = check_pages(pages)) return e;
-    if (int e = check_same_pool(cache, pages)) return e;
-    FP4_REQUIRE(!accepted || (max_accepted >= 0 && max_accepted <= 64), FP4_ERR_INVALID,
-                "max_accepted=%lld outside [0, 64]", (long long)max_accepted);
-    if (pages->batch == 0 || cache->num_pages == 0 || cache->d == 0) return ok();
-    if (accepted) { FP4_SCALAR_PTR(accepted); }
-    FP4_SCALAR_PTR(accepted_lens);
-    return hip_status(fp4::launch_kv_compact(*cache, *pages, accepted, max_accepted, accepted_lens,
-                                             static_cast<hipStream_t>(stream)),
-                      "fp4_kv_compact launch");
+    return kv_compact(cache, pages, accepted, max_accepted, accepted_lens, nullptr, 0, stream, "fp4_kv_compact launch");
+}
+
+int fp4_kv_compact_reserved(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
+                            int64_t max_accepted, const int32_t* accepted_lens, const int32_t* slots, int64_t max_new,
+                            void* stream) {
+    FP4_REQUIRE(max_new >= 0, FP4_ERR_INVALID, "negative max_new=%lld", (long long)max_new);
+    FP4_SCALAR_PTR(slots);
+    return kv_compact(cache, pages, accepted, max_accepted, accepted_lens, slots, max_new, stream,
+                      "fp4_kv_compact_reserved launch");
 }
 
 int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const int32_t* src_pages,

@@ -357,22 +357,32 @@ PyObject* kv_free(PyObject* const* v) {
     });
 }
 
+// kReserved: with the slots of a reservation.
+template <bool kReserved>
 PyObject* kv_compact(PyObject* const* v) {
-    Call call("fp4_kv_compact");
+    Call call(kReserved ? "fp4_kv_compact_reserved" : "fp4_kv_compact");
     Cache cache = cache_of(call, v[0], kCacheNames);
     Pages pages = pages_of(call, v[1]);
     const Tensor& lens = call("accepted_lens", v[3], kI32);
     const Tensor* accepted = call.optional("accepted", v[2], kI32);
+    const Tensor* slots = kReserved ? &call("slots", v[4], kI32) : nullptr;
     check_shapes(call, cache);
     check_shapes(call, pages);
     has_shape(call, "accepted_lens", &lens, {pages.c.batch});
     if (accepted && (accepted->dim() != 2 || accepted->size(0) != pages.c.batch))
         fail(PyExc_ValueError, "%s: accepted has shape %s, expected [%lld, max_accepted]", call.name(),
              text(accepted->sizes()).c_str(), (long long)pages.c.batch);
-    if (accepted && accepted->size(1) == 0) return PyLong_FromLong(0);       // nothing can be accepted
-    return call.go(v[4], [&](void* s) {
-        return fp4_kv_compact(&cache.c, &pages.c, pointer<int32_t>(accepted), accepted ? accepted->size(1) : 0,
-                              pointer<int32_t>(lens), s);
+    if (slots && (slots->dim() != 2 || slots->size(0) != pages.c.batch))
+        fail(PyExc_ValueError, "%s: slots has shape %s, expected [%lld, max_new]", call.name(), text(slots->sizes()).c_str(),
+             (long long)pages.c.batch);
+    if ((accepted && accepted->size(1) == 0) || (slots && slots->size(1) == 0))
+        return PyLong_FromLong(0);                        // nothing can be accepted, or was reserved
+    return call.go(v[kReserved ? 5 : 4], [&](void* s) {
+        const int32_t* which = pointer<int32_t>(accepted);
+        const int64_t most = accepted ? accepted->size(1) : 0;
+        return kReserved ? fp4_kv_compact_reserved(&cache.c, &pages.c, which, most, pointer<int32_t>(lens),
+                                                   pointer<int32_t>(slots), slots->size(1), s)
+                         : fp4_kv_compact(&cache.c, &pages.c, which, most, pointer<int32_t>(lens), s);
     });
 }
 
@@ -476,7 +486,8 @@ PyMethodDef methods[] = {
     method<kv_reserve, 7>("fp4_kv_reserve"),
     method<kv_fork, 4>("fp4_kv_fork"),
     method<kv_free, 5>("fp4_kv_free"),
-    method<kv_compact, 5>("fp4_kv_compact"),
+    method<kv_compact<false>, 5>("fp4_kv_compact"),
+    method<kv_compact<true>, 6>("fp4_kv_compact_reserved"),
     method<kv_copy_pages, 5>("fp4_kv_copy_pages"),
     method<attn_tree_mx, 10>("fp4_attn_tree_mx"),
     method<attn_prompt, 7>("fp4_attn_prompt"),

@@ -159,7 +159,8 @@ hipError_t launch_kv_fork(const fp4_kv_pages& t, const int32_t* pairs, int64_t n
 hipError_t launch_kv_free(const fp4_kv_pages& t, const int32_t* seqs, int64_t n, const int32_t* keep_lens,
                           int64_t page_size, hipStream_t s);
 hipError_t launch_kv_compact(const fp4_kv_cache& c, const fp4_kv_pages& t, const int32_t* accepted,
-                             int64_t max_accepted, const int32_t* accepted_lens, hipStream_t s);
+                             int64_t max_accepted, const int32_t* accepted_lens, const int32_t* slots, int64_t max_new,
+                             hipStream_t s);
 int64_t kv_copy_blocks(const fp4_kv_cache& c);
 hipError_t launch_kv_copy_pages(const fp4_kv_cache& src, const fp4_kv_cache& dst, const int32_t* src_pages,
                                 const int32_t* dst_pages, int64_t n, hipStream_t s);

@@ -305,24 +305,50 @@ __device__ __forceinline__ void move_rows(const fp4_kv_cache& c, const int64_t* 
     }
 }
 
+// Cache row of a position below the sequence's held pages; -1: no page of the pool.
+__device__ __forceinline__ int64_t row_of(const fp4_kv_pages& t, int64_t b, int64_t pos, int64_t ps) {
+    const int64_t page = t.page_table[b * t.max_pages + pos / ps];
+    return page >= 0 && page < t.num_pages ? page * ps + pos % ps : -1;
+}
+
 // One workgroup per sequence: moves the accepted rows (kept in registers between
-// the reads and the writes), then grows the length.
+// the reads and the writes), then grows the length.  With the slots of a reservation
+// it commits tokens up to the first whose slot is not its position's row: slots of a
+// refused reservation are -1, and those of one that has been committed, or whose page
+// has been copied or let go since, are other rows.  They are also what tells of a
+// short pool: the table alone cannot, the rest of a last page looks like reserved rows.
 __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_kv_pages t, const int32_t* accepted,
-                                                           int64_t max_accepted, const int32_t* accepted_lens) {
+                                                           int64_t max_accepted, const int32_t* accepted_lens,
+                                                           const int32_t* slots, int64_t max_new) {
     __shared__ int64_t from[64], to[64];
+    __shared__ int32_t granted;
     const int64_t b = blockIdx.x, ps = c.page_size;
     const int64_t len = max(t.seq_lens[b], 0), room = max(held_pages(t, b) * ps - len, (int64_t)0);
     int64_t n = max(accepted_lens[b], 0);
     if (accepted) n = min(n, max_accepted);
     n = min(n, room);
+    if (slots) {
+        n = min(n, max_new);
+        if (threadIdx.x == 0) granted = (int32_t)n;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+            const int64_t row = row_of(t, b, len + i, ps);
+            if (row < 0 || slots[b * max_new + i] != row) {
+                atomicMin(&granted, (int32_t)i);
+                break;
+            }
+        }
+        __syncthreads();
+        n = granted;
+    }
     if (n == 0) return;
     if (accepted) {
         // The page of the first uncommitted row may be shared by forks since the rows
         // were reserved: it is written unless another holder's tokens reach that far, or
         // that holder commits in this call too.  Only one of them can have reserved rows
         // there (a reservation copies a shared page), so the call is in error and neither
-        // writes.  A holder that commits counts by its accepted_lens, which stay as they
-        // are: its length is written by its own workgroup meanwhile.
+        // writes.  A holder that commits counts by its accepted_lens and its first slot,
+        // which stay as they are: its length is written by its own workgroup meanwhile.
         const int64_t last = len / ps;
         const int32_t first_page = len % ps ? t.page_table[b * t.max_pages + last] : -1;
         bool alone = true;
@@ -330,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
             bool seen = false;
             for (int64_t o = threadIdx.x; o < t.batch; o += kThreads)
                 seen |= o != b && last < held_pages(t, o) && t.page_table[o * t.max_pages + last] == first_page &&
-                        (accepted_lens[o] > 0 || t.seq_lens[o] > len);
+                        ((accepted_lens[o] > 0 && (!slots || slots[o * max_new] >= 0)) || t.seq_lens[o] > len);
             alone = !__syncthreads_or(seen);
         }
         if (threadIdx.x < 64) {
@@ -339,11 +365,10 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
             if (a >= 0 && a < room && a != i) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int64_t pos = len + (k ? i : a);
-                    const int64_t page = t.page_table[b * t.max_pages + pos / ps];
-                    if (page >= 0 && page < t.num_pages && (k == 0 || (page == first_page ? alone : t.page_refs[page] == 1)))
-                        row[k] = page * ps + pos % ps;
+                    const int64_t r = row_of(t, b, len + (k ? i : a), ps), page = r < 0 ? -1 : r / ps;
+                    if (page >= 0 && (k == 0 || (page == first_page ? alone : t.page_refs[page] == 1))) row[k] = r;
                 }
+                if (slots && (a >= max_new || slots[b * max_new + a] != row[0])) row[0] = -1;
             }
             from[i] = row[1] < 0 ? -1 : row[0];
             to[i] = row[1];
@@ -420,8 +445,9 @@ hipError_t launch_kv_free(const fp4_kv_pages& t, const int32_t* seqs, int64_t n,
 }
 
 hipError_t launch_kv_compact(const fp4_kv_cache& c, const fp4_kv_pages& t, const int32_t* accepted,
-                             int64_t max_accepted, const int32_t* accepted_lens, hipStream_t s) {
-    compact_kernel<<<(unsigned)t.batch, kThreads, 0, s>>>(c, t, accepted, max_accepted, accepted_lens);
+                             int64_t max_accepted, const int32_t* accepted_lens, const int32_t* slots, int64_t max_new,
+                             hipStream_t s) {
+    compact_kernel<<<(unsigned)t.batch, kThreads, 0, s>>>(c, t, accepted, max_accepted, accepted_lens, slots, max_new);
     return hipGetLastError();
 }
 

@@ -475,7 +475,8 @@ typedef struct fp4_kv_pages {
  *   (position seq_lens[b] + j) for j < new_tokens[b], else -1: the slots of
  *   fp4_kv_append_mx.  May be NULL with max_new 0.
  *   *n_short: int32, 0, or how many pages the pool or the table rows lack; then
- *   nothing is reserved for any sequence and every slot is -1.
+ *   nothing is reserved for any sequence and every slot is -1: the new tokens have no
+ *   rows, so attention over them and a commit of them have no meaning.
  * workspace: fp4_kv_reserve_workspace_bytes(batch, num_pages) bytes; calls (and
  * replays) that share one are ordered by the caller.
  */
@@ -518,9 +519,24 @@ int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const
  * passes its pages; an accepted index that points elsewhere moves nothing.  Of two
  * sequences that hold one partly filled page, at most one can have reserved rows on
  * it: if accepted_lens names both, rows on that page stay as they are.
+ * accepted_lens has to be 0 for a sequence whose reservation gave it no rows, and
+ * for all of them where *n_short was not 0: the unused rest of a last page cannot be
+ * told from reserved rows, and would be committed as it is.  fp4_kv_compact_reserved
+ * sees to that by itself.
  */
 int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
                    int64_t max_accepted, const int32_t* accepted_lens, void* stream);
+/*
+ * The same for the rows of one reservation, whose outcome it follows on the device:
+ * slots (int32 [batch, max_new], as that fp4_kv_reserve wrote them, not NULL).
+ * A sequence commits its tokens up to the first whose slot is not the row of its
+ * position, and an accepted index without such a slot moves nothing.  So nothing is
+ * committed for a sequence that the reservation gave no rows, for any sequence
+ * where it was refused, or from slots that have been committed before.
+ */
+int fp4_kv_compact_reserved(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
+                            int64_t max_accepted, const int32_t* accepted_lens, const int32_t* slots,
+                            int64_t max_new, void* stream);
 
 /*
  * Copies whole pages: for i in [0, n), page src_pages[i] of src to page

@@ -180,7 +180,7 @@ class Pages:
                 self.table[b, p] = -1
             self.counts[b], self.lens[b] = self.pages_of(n), n
 
-    def may_write(self, b, page, lens, accepted_lens):
+    def may_write(self, b, page, lens, commits):
         """Whether sequence b may move rows onto a page: it holds it alone, or it is the
         page of its first uncommitted row, and no other holder's tokens reach as far,
         nor does another holder commit in the same call."""
@@ -190,22 +190,28 @@ class Pages:
         if lens[b] % self.page_size == 0 or self.table[b, last] != page:
             return False
         return not any(o != b and last < self.counts[o] and self.table[o, last] == page and
-                       (accepted_lens[o] > 0 or lens[o] > lens[b]) for o in range(len(self.table)))
+                       (commits[o] or lens[o] > lens[b]) for o in range(len(self.table)))
 
-    def compact(self, accepted, accepted_lens):
+    def compact(self, accepted, accepted_lens, slots=None):
+        """slots: of the reservation that gave the rows; what it did not grant stays uncommitted."""
         lens = [int(n) for n in self.lens]
+        commits = [n > 0 and (slots is None or slots[o][0] >= 0) for o, n in enumerate(accepted_lens)]
         for b, n in enumerate(lens):
             room = int(self.counts[b]) * self.page_size - n
             m = max(int(accepted_lens[b]), 0)
             if accepted is not None:
                 m = min(m, accepted.shape[1])
             m = min(m, room)
+            if slots is not None:
+                rows = [self.row(b, n + i) for i in range(min(room, slots.shape[1]))]
+                given = [i < len(rows) and int(slots[b][i]) == rows[i] for i in range(slots.shape[1])]
+                m = min(m, (given + [False]).index(False))
             moves = []
             for i in range(m if accepted is not None else 0):
                 j = int(accepted[b, i])
-                if 0 <= j < room and j != i:
+                if 0 <= j < room and j != i and (slots is None or (j < len(given) and given[j])):
                     to = self.row(b, n + i)
-                    if self.may_write(b, to // self.page_size, lens, accepted_lens):
+                    if self.may_write(b, to // self.page_size, lens, commits):
                         moves.append((self.row(b, n + j), to))
             for a in self.arrays if moves else []:
                 source, to = np.array(moves).T

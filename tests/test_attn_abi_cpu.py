@@ -103,6 +103,33 @@ def test_page_operations_reject_bad_arguments():
     assert copy(_cache(), _cache(), None, None, 0, None) == OK
 
 
+def test_commit_of_a_reservation_rejects_bad_arguments():
+    def commit(cache=None, pages=None, accepted=FAKE, most=4, lens=FAKE, slots=FAKE, max_new=4):
+        return F.lib.fp4_kv_compact_reserved(cache or _cache(), pages or _pages(), accepted, most, lens, slots, max_new, None)
+
+    for kw, status in BAD_CACHES:
+        assert commit(cache=_cache(**kw)) == status, kw
+    for kw, status in BAD_PAGES:
+        assert commit(pages=_pages(**kw)) == status, kw
+    assert commit(slots=None) == INVALID and commit(slots=FAKE + 2) == ALIGN and commit(max_new=-1) == INVALID
+    assert commit(most=65) == INVALID and commit(lens=None) == INVALID and commit(pages=_pages(num_pages=11)) == INVALID
+    assert commit(pages=_pages(batch=0)) == OK
+
+
+def test_binding_checks_the_commit_of_a_reservation():
+    cache = F.KvCache(_u8(160, 32), _u8(160, 2), _u8(160, 32), _u8(160, 2), 16)
+    pages = F.KvPages(_int(3, 4), _int(3), _int(3), _int(10))
+    for bad in (_int(2, 4), _int(3), _int(12)):
+        with pytest.raises(ValueError, match="slots has shape"):
+            F.fp4_kv_compact_reserved(cache, pages, _int(3, 4), _int(3), bad)
+    with pytest.raises(TypeError, match="slots"):
+        F.fp4_kv_compact_reserved(cache, pages, None, _int(3), None)
+    with pytest.raises(TypeError, match="slots"):
+        F.fp4_kv_compact_reserved(cache, pages, None, _int(3), _int(3, 4).long())
+    with pytest.raises(ValueError, match="GPU"):
+        F.fp4_kv_compact_reserved(cache, pages, None, _int(3), _int(3, 4))
+
+
 def _u8(*s):
     return torch.zeros(s, dtype=torch.uint8)
 

@@ -61,6 +61,12 @@ class Both:
         self.host.compact(None if accepted is None else np.asarray(accepted), n)
         self.check()
 
+    def commit(self, accepted, n, slots):
+        """A commit that follows the reservation's slots."""
+        F.fp4_kv_compact_reserved(self.cache, self.pages, None if accepted is None else _i32(accepted), _i32(n), slots)
+        self.host.compact(None if accepted is None else np.asarray(accepted), n, slots.cpu().numpy())
+        self.check()
+
     def write(self, slots, seed):
         """Fills the reserved rows with other bytes, as an append would."""
         rng = np.random.default_rng(seed)
@@ -193,6 +199,81 @@ def test_sharers_that_commit_unreserved_rows_in_one_call_move_nothing(forks):
     before = [a.clone() for a in s.cache[:4]]
     s.compact([[1 + (b + i) % 5 for i in range(3)] for b in range(forks)], [1 + b % 3 for b in range(forks)])
     assert all(torch.equal(a, b) for a, b in zip(s.cache[:4], before))
+
+
+def _same(s, before):
+    return all(torch.equal(a, b) for a, b in zip((*s.cache[:4], *s.pages), before))
+
+
+def _copy(s):
+    return [a.clone() for a in (*s.cache[:4], *s.pages)]
+
+
+@pytest.mark.parametrize("accepted", [None, [[1, 2, 0]] * 3])
+def test_a_refused_reservation_commits_nothing(accepted):
+    """10 of 16 rows used, the pool full: the rest of the page is no reservation, of a
+    page held alone (sequence 2) or by two that commit in one call."""
+    s = Both(12, 3, 4, 2, 16, 64)
+    s.write(s.reserve([10, 0, 10], 10), 1)
+    s.compact(None, [10, 0, 10])
+    s.fork([(0, 1)])
+    before = _copy(s)
+    slots = s.reserve([3, 3, 30], 30)                   # two copies and two pages lack
+    assert (slots == -1).all()
+    s.commit(accepted, [3, 2, 3], slots)
+    assert _same(s, before) and s.pages.seq_lens.tolist() == [10, 10, 10]
+
+
+def test_only_what_the_reservation_granted_is_committed():
+    s = Both(13, 5, 8, 30, 16, 64)
+    prompts = [70, 16, 0, 5, 9]
+    slots = s.reserve(prompts, 40)                      # of sequence 0's rows 40 are in slots
+    s.write(slots, 1)
+    s.commit(None, [70, 20, 4, 5, 8], slots)            # more than was reserved, nothing reserved, fewer
+    assert s.pages.seq_lens.tolist() == [40, 16, 0, 5, 8]
+    before = _copy(s)
+    s.commit(None, [1, 1, 1, 1, 1], slots)              # the same slots again
+    assert _same(s, before)
+    slots = s.reserve([4, 20, 0, 12, 1], 20)
+    s.write(slots, 2)
+    acc = np.tile(np.arange(20)[::-1], (5, 1))          # 19, 18, ..: past the reserved ones in most
+    s.commit(acc, [3, 20, 2, 20, 1], slots)
+    assert s.pages.seq_lens.tolist() == [43, 36, 0, 17, 9]
+    slots = s.reserve([4, 4, 4, 4, 4], 4)
+    s.free([3], [3])                                    # its rows are let go between
+    before = _copy(s)
+    s.commit([[3, 1, 0, 2]] * 5, [0, 0, 0, 4, 0], slots)
+    assert _same(s, before)
+
+
+def test_steps_that_outgrow_the_pool_replayed():
+    """A captured step goes on being replayed when the pool is full: lengths and bytes
+    stay, and it takes up again when pages are free."""
+    s = Both(14, 3, 6, 9, 16, 64)
+    slots = s.reserve([30, 3, 17], 30)
+    s.write(slots, 1)
+    s.commit(None, [30, 3, 17], slots)
+    s.fork([(0, 1)])                                    # not done: sequence 1 holds pages
+    new, n = _i32([9, 5, 12]), _i32([3, 5, 2])
+    acc = _i32([[8, 0, 4, 1, 2], [0, 1, 2, 3, 4], [3, 7, 0, 0, 0]])
+    slots, short = torch.zeros((3, 12), dtype=torch.int32, device=DEV), _i32([0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        F.fp4_kv_reserve(s.cache, s.pages, new, slots, short, s.ws)
+        F.fp4_kv_compact_reserved(s.cache, s.pages, acc, n, slots)
+    lacks = []
+    for i in range(14):
+        if i == 11:
+            s.free([2])
+        graph.replay()
+        torch.cuda.synchronize()
+        want, lack = s.host.reserve([9, 5, 12], 12)
+        s.host.compact(acc.cpu().numpy(), [3, 5, 2], want)
+        assert np.array_equal(slots.cpu().numpy(), want) and short.item() == lack
+        s.check()
+        lacks.append(lack > 0)
+        torch.ones(1000, device=DEV).sum().item()
+    assert lacks[10] and not lacks[0] and not lacks[11]
 
 
 def test_ids_outside_are_not_followed():
