@@ -467,7 +467,8 @@ class KvCache(NamedTuple):
 class KvPages(NamedTuple):
     """The pages that the sequences of a batch hold: int32 page_table
     [batch, max_pages] (-1 = none), page_counts [batch], seq_lens [batch]
-    (committed tokens) and page_refs [num_pages] (holders; 0 = free)."""
+    (committed tokens) and page_refs [num_pages] (holders; 0 = free).  One state
+    belongs to one KvCache: a model keeps one for each layer's cache."""
     page_table: torch.Tensor
     page_counts: torch.Tensor
     seq_lens: torch.Tensor

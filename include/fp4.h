@@ -454,6 +454,13 @@ typedef struct fp4_kv_cache {
  * Page ids outside [0, num_pages), counts outside [0, max_pages] and sequence
  * ids outside [0, batch) are never followed.  Calls on one state are ordered by
  * the caller (one stream).  batch and the lists of ids are shorter than 2^20.
+ *
+ * One state belongs to one cache: fp4_kv_reserve copies a shared page's rows, and
+ * fp4_kv_compact moves accepted rows, in the cache they are given and update the
+ * state for it, so a second cache called with the same state would miss both.  A
+ * model with a cache for each layer keeps a state for each layer.  What the calls do
+ * to a state follows from the state and their arguments alone, so layers that take
+ * the same calls have the same tables, lengths and slots at every step.
  */
 typedef struct fp4_kv_pages {
     int32_t* page_table;

@@ -127,6 +127,26 @@ def _chain(batch, width):
     return np.array([[(1 << (i + 1)) - 1 for i in range(width)]] * batch, np.uint64)
 
 
+def test_layers_each_with_their_cache_and_page_state():
+    """Two layers take the same calls: each has its own rows (copies of shared pages and
+    moved drafts included; every step is checked against them), and their page states
+    stay equal."""
+    layers = [Server(4), Server(4)]
+    for i, s in enumerate(layers):
+        s.prompts(10 + i, [21, 7, 0, 0])
+        F.fp4_kv_fork(s.pages, _i32([[0, 2], [0, 3]]), PAGE)
+        s.host[2], s.host[3] = list(s.host[0]), list(s.host[0])
+    tree = np.array([[1, 3, 5, 11, 21]] * 4, np.uint64)
+    for step, (drafts, kept) in enumerate([([5, 5, 5, 5], [[0, 2, 4], [0], [0, 1, 3], []]),
+                                           ([5, 2, 5, 3], [[0, 1], [], [0, 2], [0, 2]]),
+                                           ([1, 1, 1, 1], [[0], [0], [0], [0]])]):
+        for i, s in enumerate(layers):
+            s.step(20 + 2 * step + i, drafts, tree[:, :max(drafts)], kept)
+        for a, b in zip(layers[0].pages, layers[1].pages):
+            assert torch.equal(a, b)
+    assert not torch.equal(layers[0].cache.k_codes, layers[1].cache.k_codes)
+
+
 def test_prompts_steps_forks_and_cuts():
     s = Server(5)
     s.prompts(1, [37, 16, 5, 0, 0])
