@@ -481,7 +481,8 @@ def fp4_kv_reserve_workspace_bytes(batch: int, num_pages: int) -> int:
 
 def fp4_kv_reserve(cache: KvCache, pages: KvPages, new_tokens, slots, n_short, workspace, stream=None):
     """Room for new_tokens[b] tokens behind every sequence; their cache rows in
-    slots [batch, max_new] (None: not wanted), -1 past new_tokens[b]."""
+    slots [batch, max_new] (None: not wanted), -1 past new_tokens[b].  Tokens of an
+    earlier reservation that are not committed have to be appended again."""
     _check("fp4_kv_reserve", _binding.fp4_kv_reserve(cache, pages, new_tokens, slots, n_short, workspace, stream))
 
 

@@ -477,7 +477,9 @@ typedef struct fp4_kv_pages {
  * the committed ones of every sequence: pages are taken free ones first by
  * index, for the sequences in order, so the result does not depend on timing.
  * A partly filled last page that other sequences hold too is copied first (its
- * committed rows) and the copy takes its place: copy on write.
+ * committed rows) and the copy takes its place: copy on write.  A reservation starts
+ * a step anew: tokens of an earlier one that are not committed yet are to be appended
+ * again, to the new slots (where a fork came between, the copy does not have them).
  *   slots: int32 [batch, max_new], the cache row of new token j of sequence b
  *   (position seq_lens[b] + j) for j < new_tokens[b], else -1: the slots of
  *   fp4_kv_append_mx.  May be NULL with max_new 0.
@@ -498,7 +500,7 @@ size_t fp4_kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages);
  * when an id is outside [0, batch), the target still holds pages, an earlier
  * pair names the same target, or the source is a target of this call.  Drafted
  * tokens that the source has not committed are not shared; it may commit them
- * afterwards.
+ * afterwards, before its next reservation.
  */
 int fp4_kv_fork(const fp4_kv_pages* pages, const int32_t* pairs, int64_t n, int64_t page_size, void* stream);
 

@@ -246,6 +246,32 @@ def test_only_what_the_reservation_granted_is_committed():
     assert _same(s, before)
 
 
+@pytest.mark.parametrize("committed", [10, 16, 30])
+def test_a_second_reservation_starts_the_step_anew(committed):
+    """Drafts reserved and appended before a fork, then reserved again: on a shared page
+    the slots are a copy's, so the old ones commit nothing, and the new ones what is
+    appended to them; elsewhere the slots are the same."""
+    s = Both(15, 3, 6, 16, 16, 64)
+    slots = s.reserve([committed, 0, 0], committed)
+    s.write(slots, 1)
+    s.commit(None, [committed, 0, 0], slots)
+    old = s.reserve([6, 0, 0], 6)
+    s.write(old, 2)
+    s.fork([(0, 1)])
+    new = s.reserve([6, 0, 0], 6)
+    assert torch.equal(old, new) == (committed % 16 == 0)
+    if committed % 16:
+        before = _copy(s)
+        s.commit([[5, 1, 0]] * 3, [3, 0, 0], old)
+        n = int(s.pages.seq_lens[0]) - committed
+        assert n == 0 and _same(s, before)
+    s.write(new, 3)
+    drafts = [a[new[0].long()].clone() for a in s.cache[:4]]
+    s.commit([[5, 1, 0]] * 3, [3, 0, 0], new)
+    for a, d in zip(s.cache, drafts):
+        assert torch.equal(a[new[0, :3].long()], d[[5, 1, 0]])
+
+
 def test_steps_that_outgrow_the_pool_replayed():
     """A captured step goes on being replayed when the pool is full: lengths and bytes
     stay, and it takes up again when pages are free."""
