@@ -81,6 +81,16 @@ bool rows_overlap(const void* a, int64_t pitch_a, int64_t width_a, const void* b
     return off < (uintptr_t)width_a || off + (uintptr_t)width_b > pitch;
 }
 
+// Whether a run of bytes shares one with an array of `rows` rows (it may lie between two rows).
+bool run_overlaps(const void* a, int64_t pitch, int64_t width, int64_t rows, const void* run, uint64_t bytes) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pr = reinterpret_cast<uintptr_t>(run);
+    const uintptr_t end = pa + (uintptr_t)((rows - 1) * pitch + width);
+    if (bytes == 0 || pr >= end || pr + bytes <= pa) return false;
+    if (pr <= pa) return true;
+    const uintptr_t row = (pr - pa) / (uintptr_t)pitch, off = (pr - pa) % (uintptr_t)pitch;
+    return off < (uintptr_t)width || (row + 1 < (uintptr_t)rows && off + bytes > (uintptr_t)pitch);
+}
+
 constexpr int64_t kMaxList = (int64_t)1 << 20;    // sequences of a batch, entries of a list of ids
 
 int check_page_size(int64_t page_size) {
@@ -581,6 +591,23 @@ int fp4_qk_norm_rope(const void* q, const void* k, int64_t tokens, int q_heads, 
                     "k_out overlaps q");
         FP4_REQUIRE(!rows_overlap(q_out, ld_qo * 2, wq * 2, k_out, ld_ko * 2, wk * 2, tokens), FP4_ERR_INVALID,
                     "q_out overlaps k_out");
+    }
+    const uint64_t weight_bytes = (uint64_t)head_dim * (weight_dtype == FP4_DT_F32 ? 4 : 2);
+    // Addresses end at 2^57: no table is longer.
+    const uint64_t places = (uint64_t)(max_positions < (int64_t)1 << 45 ? max_positions : (int64_t)1 << 45);
+    const struct {
+        const char* name;
+        const void* start;
+        uint64_t bytes;
+    } read[] = {{"q_weight", q_weight, q_weight ? weight_bytes : 0},
+                {"k_weight", k_weight, k_weight ? weight_bytes : 0},
+                {"cos_sin", cos_sin, rot_dim ? places * rot_dim * 4 : 0},
+                {"positions", positions, rot_dim ? (uint64_t)tokens * 4 : 0}};
+    for (const auto& r : read) {
+        FP4_REQUIRE(!q_heads || !run_overlaps(q_out, ld_qo * 2, wq * 2, tokens, r.start, r.bytes), FP4_ERR_INVALID,
+                    "q_out overlaps %s", r.name);
+        FP4_REQUIRE(!kv_heads || !run_overlaps(k_out, ld_ko * 2, wk * 2, tokens, r.start, r.bytes), FP4_ERR_INVALID,
+                    "k_out overlaps %s", r.name);
     }
     fp4::QkNorm p{};
     p.q = static_cast<const uint16_t*>(q);

@@ -412,8 +412,8 @@ size_t fp4_moe_workspace_bytes(fp4_format fmt, int64_t tokens, int64_t hidden, i
  * q_weight, k_weight: [head_dim] of weight_dtype, NULL = ones.
  * q [tokens, ld_q], k [tokens, ld_k], q_out [tokens, ld_qo], k_out [tokens,
  * ld_ko]: bf16.  Either output may be its own input (same pointer and leading
- * dimension); any other overlap of an output with an input or the other output
- * is FP4_ERR_INVALID.  q_heads or kv_heads may be 0 (its pointers are then
+ * dimension); any other overlap of an output with an input (weights, cos_sin and
+ * positions too) or the other output is FP4_ERR_INVALID.  q_heads or kv_heads may be 0 (its pointers are then
  * ignored).  The squares are summed in fp32: a head whose sum passes 3e38 (values
  * of 1e18 on) or whose values are no numbers comes out as the formula does there.
  * Errors: head_dim not a multiple of 16 in [16, 256], rot_dim not a multiple of

@@ -37,6 +37,33 @@ def test_norm_rope_rejections():
     assert _norm(hq=0, hk=0, q=None, k=None, qo=None, ko=None) == OK
 
 
+def test_norm_rope_outputs_over_what_all_heads_read():
+    """Weights, angles and positions are read by workgroups that others may be ahead of.
+    The defaults: q_out 4 rows of 512 bytes at 3 MiB, k_out 4 of 256 at 4 MiB, the
+    table 25600 bytes and the positions 16 at 1 MiB, the weights 128 bytes (bf16)."""
+    qo, ko = 3 * FAKE, 4 * FAKE
+
+    def overlap(what, **kw):
+        assert _norm(**kw) == INVALID and F.lib.fp4_last_error().decode() == what, kw
+
+    overlap("q_out overlaps q_weight", qw=qo)
+    overlap("q_out overlaps q_weight", qw=qo + 3 * 512 + 496)
+    overlap("q_out overlaps k_weight", kw=qo - 112)
+    overlap("q_out overlaps k_weight", kw=qo - 240, dt=1)
+    overlap("k_out overlaps k_weight", kw=ko + 16)
+    overlap("q_out overlaps cos_sin", table=qo - 25600 + 16)
+    overlap("k_out overlaps cos_sin", table=ko)
+    overlap("q_out overlaps positions", pos=qo + 4)
+    overlap("k_out overlaps positions", pos=ko - 12)
+    overlap("k_out overlaps cos_sin", table=ko - 16, places=1 << 62)
+    # rows of 512 bytes 1024 apart: the weights between two of them are no overlap, up to the next row they are
+    overlap("q_out overlaps q_weight", qw=qo + 1024 - 112, ld_qo=512)
+    # what does not overlap passes, down to the last pair of the check
+    for kw in (dict(qw=qo + 512, ld_qo=512), dict(qw=qo + 2048), dict(kw=qo - 128), dict(table=qo - 25600), dict(kw=ko + 1024),
+               dict(qw=qo + 3 * 1024 + 512, ld_qo=512)):
+        overlap("k_out overlaps positions", pos=ko + 1020, **kw)
+
+
 def _cache(**kw):
     v = dict(k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, num_pages=10, d=64, page_size=16) | kw
     return struct.pack("=4Q3q", *(v[n] or 0 for n in v))
