@@ -143,6 +143,12 @@ int check_same_pool(const fp4_kv_cache* cache, const fp4_kv_pages* pages) {
     return FP4_OK;
 }
 
+// The kernels work in powers of two, with scale * log2(e) in fp32.
+int check_scale(float scale) {
+    FP4_REQUIRE(std::fabs(scale) <= 0x1p127f, FP4_ERR_INVALID, "scale=%g is not finite or above 2^127", (double)scale);
+    return FP4_OK;
+}
+
 // Head counts and head_dim of the attention entry points.
 int check_heads(int q_heads, int kv_heads, int head_dim) {
     FP4_REQUIRE(q_heads > 0 && kv_heads > 0, FP4_ERR_INVALID, "q_heads=%d and kv_heads=%d must be positive", q_heads,
@@ -733,7 +739,7 @@ int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, con
                 (long long)max_pages);
     FP4_REQUIRE(batch < 65536 && max_pages < (int64_t)1 << 31, FP4_ERR_SHAPE, "batch=%lld or max_pages=%lld too large",
                 (long long)batch, (long long)max_pages);
-    FP4_REQUIRE(std::isfinite(scale), FP4_ERR_INVALID, "scale is not finite");
+    if (int e = check_scale(scale)) return e;
     if (batch == 0) return ok();
     FP4_PTR(q);
     FP4_PTR(out);
@@ -781,7 +787,7 @@ int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* 
     FP4_REQUIRE(fp4::attn_prompt_tiles(seqs, tokens, head_dim) < ((int64_t)1 << 23) / q_heads, FP4_ERR_SHAPE,
                 "tokens=%lld, seqs=%lld and q_heads=%d give too many row tiles (2^23)", (long long)tokens, (long long)seqs,
                 q_heads);
-    FP4_REQUIRE(std::isfinite(scale), FP4_ERR_INVALID, "scale is not finite");
+    if (int e = check_scale(scale)) return e;
     if (seqs == 0 || tokens == 0) return ok();
     const int64_t wq = (int64_t)q_heads * head_dim, wk = (int64_t)kv_heads * head_dim;
     FP4_PTR(q);

@@ -580,7 +580,8 @@ int fp4_kv_copy_pages(const fp4_kv_cache* src, const fp4_kv_cache* dst, const in
  * the shapes and lengths alone, so equal calls give equal bits.
  * Errors: head_dim not 64, 128 or 256, or cache->d != kv_heads * head_dim, or
  * q_heads not a multiple of kv_heads -> FP4_ERR_SHAPE; drafts outside [1, 64] ->
- * FP4_ERR_INVALID; scale not finite -> FP4_ERR_INVALID.
+ * FP4_ERR_INVALID; scale not finite or above 2^127 in magnitude -> FP4_ERR_INVALID.
+ * A magnitude below 7e-38 counts as 7e-38.
  */
 int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table,
                      int64_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
@@ -601,7 +602,8 @@ size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int
  * Errors: head_dim not 64, 128 or 256, q_heads not a multiple of kv_heads, ld_k
  * or ld_v of 2^24 or more, 2^30 tokens or more, or 2^23 row tiles (of 128 rows, 256
  * at head_dim 256; one more for every sequence) over all query heads ->
- * FP4_ERR_SHAPE; scale not finite -> FP4_ERR_INVALID.
+ * FP4_ERR_SHAPE; scale not finite or above 2^127 in magnitude -> FP4_ERR_INVALID.  A
+ * magnitude below 7e-38 counts as 7e-38.
  */
 int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int64_t seqs,
                     int64_t tokens, int q_heads, int kv_heads, int head_dim, int64_t ld_q, int64_t ld_k,

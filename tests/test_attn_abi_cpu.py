@@ -319,6 +319,15 @@ def test_attn_prompt_refuses_what_its_offsets_cannot_hold():
     assert b"row tiles" in F.lib.fp4_last_error()
 
 
+@pytest.mark.parametrize("call,batch", [(_tree, "batch"), (_prompt, "seqs")])
+def test_scales_that_fp32_cannot_hold_times_log2_e(call, batch):
+    """2^128 / log2(e) is 2.36e38: the kernels' factor would be infinite, and 0 times it no number."""
+    for scale in (2.5e38, -3.3e38, 1.8e38):
+        assert call(scale=scale) == INVALID and b"2^127" in F.lib.fp4_last_error()
+    for scale in (2.0 ** 127, -2.0 ** 127, 0.0, 1e-45):
+        assert call(scale=scale, **{batch: 0}) == OK
+
+
 def test_weights_of_absent_heads_are_ignored():
     """A dangling weight pointer of heads that a call has none of is no error: the
     call is refused for its own fault only (a table that is missing)."""
