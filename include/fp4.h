@@ -415,7 +415,9 @@ size_t fp4_moe_workspace_bytes(fp4_format fmt, int64_t tokens, int64_t hidden, i
  * dimension); any other overlap of an output with an input (weights, cos_sin and
  * positions too) or the other output is FP4_ERR_INVALID.  q_heads or kv_heads may be 0 (its pointers are then
  * ignored).  The squares are summed in fp32: a head whose sum passes 3e38 (values
- * of 1e18 on) or whose values are no numbers comes out as the formula does there.
+ * of 1e18 on) or whose values are no numbers comes out as the formula does there, and
+ * with an eps below 1e-36 so does one whose squares lose bits below 1e-38 (values
+ * under 1e-18).
  * Errors: head_dim not a multiple of 16 in [16, 256], rot_dim not a multiple of
  * 16 in [0, head_dim], 2^24 tokens or more -> FP4_ERR_SHAPE; eps negative or not finite -> FP4_ERR_INVALID.
  */
@@ -541,7 +543,8 @@ int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const i
  * A sequence commits its tokens up to the first whose slot is not the row of its
  * position, and an accepted index without such a slot moves nothing.  So nothing is
  * committed for a sequence that the reservation gave no rows, for any sequence
- * where it was refused, or from slots that have been committed before.
+ * where it was refused, or from slots that have been committed before (while the
+ * sequence has not been cut back since).
  */
 int fp4_kv_compact_reserved(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
                             int64_t max_accepted, const int32_t* accepted_lens, const int32_t* slots,
