@@ -108,7 +108,8 @@ def attn_tree_mx(qbits, kc, ks, vc, vs, page_size, table, seq_lens, kv_heads, sc
 
 class Pages:
     """The page state and the cache it speaks of, on the host.  arrays: the
-    cache's row arrays (codes and scales of keys and values)."""
+    cache's row arrays (codes and scales of keys and values).  Page ids outside the
+    pool, counts outside the table's rows and negative lengths are not followed."""
 
     def __init__(self, table, counts, lens, refs, page_size, arrays):
         self.table, self.counts, self.lens, self.refs = (np.array(a) for a in (table, counts, lens, refs))
@@ -117,8 +118,15 @@ class Pages:
     def pages_of(self, n):
         return -(-int(n) // self.page_size)
 
+    def held(self, b):
+        return min(max(int(self.counts[b]), 0), self.table.shape[1])
+
+    def inside(self, page):
+        return 0 <= page < len(self.refs)
+
     def row(self, b, pos):
-        return int(self.table[b, pos // self.page_size]) * self.page_size + pos % self.page_size
+        page = int(self.table[b, pos // self.page_size])
+        return page * self.page_size + pos % self.page_size if self.inside(page) else -1
 
     def reserve(self, new, max_new):
         """Returns (slots, short)."""
@@ -126,14 +134,15 @@ class Pages:
         slots = np.full((batch, max_new), -1, np.int32)
         jobs, short, wanted = [], 0, 0
         for b in range(batch):
-            n, add = int(self.lens[b]), max(int(new[b]), 0)
+            n, add = max(int(self.lens[b]), 0), max(int(new[b]), 0)
             if add == 0:
                 continue
             pages = self.pages_of(n + add)
             short += max(pages - width, 0)
             last = n // self.page_size
-            shared = n % self.page_size > 0 and last < self.counts[b] and self.refs[self.table[b, last]] > 1
-            need = max(min(pages, width) - int(self.counts[b]), 0)
+            shared = (n % self.page_size > 0 and last < self.held(b) and self.inside(self.table[b, last]) and
+                      self.refs[self.table[b, last]] > 1)
+            need = max(min(pages, width) - self.held(b), 0)
             wanted += need + shared
             jobs.append((b, n, add, last, shared, need))
         free = [p for p in range(len(self.refs)) if self.refs[p] == 0]
@@ -149,6 +158,7 @@ class Pages:
                 self.table[b, last] = page
                 self.refs[old] -= 1
                 self.refs[page] = 1
+            self.counts[b] = self.held(b)
             for _ in range(need):
                 page = free.pop(0)
                 self.table[b, self.counts[b]] = page
@@ -164,21 +174,24 @@ class Pages:
         for i, (s, t) in enumerate(pairs):
             if not (0 <= s < batch and 0 <= t < batch) or t in targets[:i] or s in targets or self.counts[t]:
                 continue
-            n = self.pages_of(self.lens[s])
+            n = min(self.pages_of(max(int(self.lens[s]), 0)), self.held(s))
             self.table[t, :n] = self.table[s, :n]
             for p in self.table[s, :n]:
-                self.refs[p] += 1
-            self.counts[t], self.lens[t] = n, self.lens[s]
+                if self.inside(p):
+                    self.refs[p] += 1
+            self.counts[t], self.lens[t] = n, min(max(int(self.lens[s]), 0), n * self.page_size)
 
     def free(self, seqs, keep=None):
         for i, b in enumerate(seqs):
             if not 0 <= b < len(self.table) or b in list(seqs[:i]):
                 continue
-            n = min(int(self.lens[b]), 0 if keep is None else max(int(keep[i]), 0))
-            for p in range(self.pages_of(n), int(self.counts[b])):
-                self.refs[self.table[b, p]] -= 1
+            n = min(max(int(self.lens[b]), 0), 0 if keep is None else max(int(keep[i]), 0))
+            kept = min(self.pages_of(n), self.held(b))
+            for p in range(kept, self.held(b)):
+                if self.inside(self.table[b, p]):
+                    self.refs[self.table[b, p]] -= 1
                 self.table[b, p] = -1
-            self.counts[b], self.lens[b] = self.pages_of(n), n
+            self.counts[b], self.lens[b] = kept, min(n, kept * self.page_size)
 
     def may_write(self, b, page, lens, commits):
         """Whether sequence b may move rows onto a page: it holds it alone, or it is the
@@ -189,31 +202,32 @@ class Pages:
         last = lens[b] // self.page_size
         if lens[b] % self.page_size == 0 or self.table[b, last] != page:
             return False
-        return not any(o != b and last < self.counts[o] and self.table[o, last] == page and
+        return not any(o != b and last < self.held(o) and self.table[o, last] == page and
                        (commits[o] or lens[o] > lens[b]) for o in range(len(self.table)))
 
     def compact(self, accepted, accepted_lens, slots=None):
         """slots: of the reservation that gave the rows; what it did not grant stays uncommitted."""
-        lens = [int(n) for n in self.lens]
+        lens = [max(int(n), 0) for n in self.lens]
         commits = [n > 0 and (slots is None or slots[o][0] >= 0) for o, n in enumerate(accepted_lens)]
         for b, n in enumerate(lens):
-            room = int(self.counts[b]) * self.page_size - n
+            room = max(self.held(b) * self.page_size - n, 0)
             m = max(int(accepted_lens[b]), 0)
             if accepted is not None:
                 m = min(m, accepted.shape[1])
             m = min(m, room)
             if slots is not None:
                 rows = [self.row(b, n + i) for i in range(min(room, slots.shape[1]))]
-                given = [i < len(rows) and int(slots[b][i]) == rows[i] for i in range(slots.shape[1])]
+                given = [i < len(rows) and int(slots[b][i]) == rows[i] >= 0 for i in range(slots.shape[1])]
                 m = min(m, (given + [False]).index(False))
             moves = []
             for i in range(m if accepted is not None else 0):
                 j = int(accepted[b, i])
                 if 0 <= j < room and j != i and (slots is None or (j < len(given) and given[j])):
-                    to = self.row(b, n + i)
-                    if self.may_write(b, to // self.page_size, lens, commits):
-                        moves.append((self.row(b, n + j), to))
+                    source, to = self.row(b, n + j), self.row(b, n + i)
+                    if source >= 0 and to >= 0 and self.may_write(b, to // self.page_size, lens, commits):
+                        moves.append((source, to))
             for a in self.arrays if moves else []:
                 source, to = np.array(moves).T
                 a[to] = a[source]
-            self.lens[b] += m
+            if m:
+                self.lens[b] = n + m

@@ -76,12 +76,16 @@ class Both:
             h[rows] = rng.integers(0, 256, (len(rows), h.shape[1]), dtype=np.uint8)
             t[torch.from_numpy(rows).long().to(DEV)] = torch.from_numpy(h[rows]).to(DEV)
 
+    whole = True            # False once a test has put something into the state that no call does
+
     def check(self):
         h = self.host
         for name, got, want in zip(F.KvPages._fields, self.pages, (h.table, h.counts, h.lens, h.refs)):
             assert np.array_equal(got.cpu().numpy(), want), name
         for got, want in zip(self.cache, h.arrays):
             assert np.array_equal(got.cpu().numpy(), want)
+        if not self.whole:
+            return
         # every reference is a table entry, and the other way round
         entries = [int(p) for row, n in zip(h.table, h.counts) for p in row[:n]]
         assert np.array_equal(np.bincount(entries, minlength=len(h.refs)), h.refs)
@@ -319,6 +323,33 @@ def test_ids_outside_are_not_followed():
     assert slots[0].tolist() == [-1, -1] and slots[1].tolist() == [-1, -1]
     for got, want in zip(s.cache[:1], s.host.arrays):
         assert got.shape == want.shape
+
+
+ODD = [("table", (0, 0), 1 << 30), ("table", (0, 2), 40), ("table", (1, 0), -7), ("table", (2, 1), -1),
+       ("table", (3, 0), -1 << 31), ("counts", 2, 99), ("counts", 2, -3), ("counts", 0, 1), ("counts", 3, 1 << 30),
+       ("lens", 1, -5), ("lens", 1, 60), ("lens", 4, (1 << 31) - 1), ("lens", 2, 0)]
+
+
+@pytest.mark.parametrize("field,at,value", ODD)
+def test_an_odd_entry_reaches_nothing_else(field, at, value):
+    """One table entry, count or length that no call leaves, then every call: all bytes of
+    the cache, references, counts, lengths, tables and slots are those of the host's
+    loops, which skip it; what other sequences have is untouched by it."""
+    s = Both(16, 6, 5, 40, 16, 64)
+    lens = [40, 9, 33, 16, 12, 0]
+    slots = s.reserve(lens, 40)
+    s.write(slots, 1)
+    s.commit(None, lens, slots)
+    getattr(s.host, field)[at] = value
+    s.pages[{"table": 0, "counts": 1, "lens": 2}[field]][at] = value
+    s.whole = False
+    s.fork([(0, 5), (1, 5), (2, 4)])
+    slots = s.reserve([3, 4, 5, 6, 7, 2], 7)
+    s.write(slots, 2)
+    s.commit([[2, 0, 1]] * 6, [2, 3, 1, 3, 2, 2], slots)
+    s.compact([[4, 1, 0]] * 6, [1, 2, 0, 1, 0, 0])
+    s.free([0, 3, 2], [17, 0, 20])
+    s.free([5, 1, 0, 4])
 
 
 @pytest.mark.parametrize("page_size,d,n,values", [(16, 32, 1, True), (48, 96, 7, True), (64, 1024, 33, True), (16, 512, 200, False)])
