@@ -305,9 +305,9 @@ __device__ __forceinline__ void move_rows(const fp4_kv_cache& c, const int64_t* 
     }
 }
 
-// Cache row of a position below the sequence's held pages; -1: no page of the pool.
-__device__ __forceinline__ int64_t row_of(const fp4_kv_pages& t, int64_t b, int64_t pos, int64_t ps) {
-    const int64_t page = t.page_table[b * t.max_pages + pos / ps];
+// Cache row of a position below the sequence's held pages, and its page; -1: no page of the pool.
+__device__ __forceinline__ int64_t row_of(const fp4_kv_pages& t, int64_t b, int64_t pos, int64_t ps, int64_t& page) {
+    page = t.page_table[b * t.max_pages + pos / ps];
     return page >= 0 && page < t.num_pages ? page * ps + pos % ps : -1;
 }
 
@@ -332,7 +332,8 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
         if (threadIdx.x == 0) granted = (int32_t)n;
         __syncthreads();
         for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-            const int64_t row = row_of(t, b, len + i, ps);
+            int64_t page;
+            const int64_t row = row_of(t, b, len + i, ps, page);
             if (row < 0 || slots[b * max_new + i] != row) {
                 atomicMin(&granted, (int32_t)i);
                 break;
@@ -365,8 +366,9 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
             if (a >= 0 && a < room && a != i) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int64_t r = row_of(t, b, len + (k ? i : a), ps), page = r < 0 ? -1 : r / ps;
-                    if (page >= 0 && (k == 0 || (page == first_page ? alone : t.page_refs[page] == 1))) row[k] = r;
+                    int64_t page;
+                    const int64_t r = row_of(t, b, len + (k ? i : a), ps, page);
+                    if (r >= 0 && (k == 0 || (page == first_page ? alone : t.page_refs[page] == 1))) row[k] = r;
                 }
                 if (slots && (a >= max_new || slots[b * max_new + a] != row[0])) row[0] = -1;
             }

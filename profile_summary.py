@@ -10,6 +10,9 @@ Writes into the profiles directory:
   mfma_lds_bench_stages.txt   matrix-core busy fraction, MFMA operations and
                               LDS bank conflicts per launch of the MFMA-bound
                               stages' kernels;
+  attention_kernels.txt       durations of the attention path's kernels in each
+                              listed case of perf/operators.py, and counters of
+                              the larger cases;
   traffic.json                the traffic and matrix-core figures for bench.py,
                               tagged with the digest of the kernel sources they
                               were taken on.
@@ -147,6 +150,7 @@ def main(raw, prof):
         out["mfma"] = keep["mfma"]
     with open(os.path.join(prof, "traffic.json"), "w") as f:
         json.dump(out, f, indent=1)
+    attention_summary(raw, prof, out.get("copy_calibration"))
 
 
 def traffic_summary(raw, prof):
@@ -239,6 +243,65 @@ def mfma_summary(raw, prof):
         f.write("\n".join(lines) + "\n")
     print("\n".join(lines))
     return res
+
+
+def attention_summary(raw, prof, calibration):
+    """Of each case's own run: calls, median and least duration by kernel and grid;
+    counters as means over the kernel's dispatches."""
+    lines, cases = [], []
+    for folder in sorted(glob.glob(os.path.join(raw, "att_*", "")), key=os.path.getmtime):
+        trace = glob.glob(os.path.join(folder, "**", "*kernel_trace.csv"), recursive=True)
+        if not trace:
+            continue
+        case = os.path.basename(os.path.dirname(folder))[len("att_"):]
+        cases.append(case)
+        kernels = {}
+        for r in sorted(csv.DictReader(open(trace[0])), key=lambda r: int(r["Start_Timestamp"])):
+            if "fp4::" in r["Kernel_Name"]:
+                key = (short(r["Kernel_Name"]).replace("void ", ""), "x".join(r[f"Grid_Size_{a}"] for a in "XYZ"),
+                       r["Workgroup_Size_X"])
+                kernels.setdefault(key, []).append((int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3)
+        for (name, grid, group), us in kernels.items():
+            lines.append(f"{case:18s} {name:38s} {grid:>14s} {group:>5s} {len(us):6d} {sorted(us)[len(us) // 2]:10.1f} {min(us):9.1f}")
+    if not lines:
+        return
+    counters = []
+    scale = {"FETCH_SIZE": 1024 * (calibration or {}).get("factor_fetch", 1.0),
+             "WRITE_SIZE": 1024 * (calibration or {}).get("factor_write", 1.0)}
+    for case in cases:
+        means = {}
+        for group, names in (("SQ_VALU_MFMA_BUSY_CYCLES", ("SQ_VALU_MFMA_BUSY_CYCLES", "SQ_INSTS_VALU", "SQ_LDS_BANK_CONFLICT",
+                                                           "SQ_LDS_IDX_ACTIVE", "GRBM_GUI_ACTIVE")),
+                             ("FETCH_SIZE", ("FETCH_SIZE",)), ("WRITE_SIZE", ("WRITE_SIZE",))):
+            for n in names:
+                values = {}
+                for name, _, v in read_counter(raw, case, n, folder=f"attpmc_{case}_{group}"):
+                    if "fp4::" in name:
+                        values.setdefault(short(name).replace("void ", ""), []).append(v)
+                for k, v in values.items():
+                    means.setdefault(k, {})[n] = sum(v) / len(v)
+        for k, m in means.items():
+            if len(m) != 7:
+                continue
+            busy = m["SQ_VALU_MFMA_BUSY_CYCLES"] / (m["GRBM_GUI_ACTIVE"] / XCCS * SIMDS)
+            counters.append(f"{case:18s} {k:38s} {100 * busy:8.1f}%  {m['SQ_INSTS_VALU']:10.3g}  {m['SQ_LDS_BANK_CONFLICT']:10.3g}"
+                            f" / {m['SQ_LDS_IDX_ACTIVE']:<10.3g} {m['FETCH_SIZE'] * scale['FETCH_SIZE'] / 1e6:9.1f}"
+                            f" {m['WRITE_SIZE'] * scale['WRITE_SIZE'] / 1e6:9.1f}")
+    with open(os.path.join(prof, "attention_kernels.txt"), "w") as f:
+        f.write("Kernels of the attention path on MI355X: each listed case of perf/operators.py traced by itself.\n")
+        f.write("command (per case): rocprofv3 --kernel-trace --stats --output-format csv -d <out>/att_<case> -o run -- "
+                "python3 perf/passes.py <case> 23\n")
+        f.write(f"kernel sources digest: {source_digest()}\n\n")
+        f.write(f"{'case':18s} {'kernel':38s} {'grid (threads)':>14s} {'group':>5s} {'calls':>6s} {'median us':>10s} {'min us':>9s}\n")
+        f.write("\n".join(lines) + "\n\n")
+        f.write("Counters per launch (python3 perf/passes.py <case> 5, one block a run).  MFMA busy: SQ_VALU_MFMA_BUSY_CYCLES of\n"
+                "1024 SIMDs over GRBM_GUI_ACTIVE / 8 XCDs; fetched and written: FETCH_SIZE and WRITE_SIZE, each scaled by what it\n"
+                "reads for a plain 256 MiB device copy.\n\n")
+        f.write(f"{'case':18s} {'kernel':38s} {'MFMA busy':>9s}  {'VALU insts':>10s}  {'LDS conflict / active cycles':>25s} "
+                f"{'read MB':>9s} {'wrote MB':>9s}\n")
+        f.write("\n".join(counters) + "\n")
+    print("\n".join(lines + counters))
+
 
 if __name__ == "__main__":
     main(sys.argv[1], sys.argv[2])
