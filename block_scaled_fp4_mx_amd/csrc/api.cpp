@@ -160,9 +160,10 @@ int check_heads(int q_heads, int kv_heads, int head_dim) {
     return FP4_OK;
 }
 
-// slots: of the reservation whose rows are committed, or NULL.
+// reserved: by the slots of a reservation.
 int kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted, int64_t max_accepted,
-               const int32_t* accepted_lens, const int32_t* slots, int64_t max_new, void* stream, const char* what) {
+               const int32_t* accepted_lens, bool reserved, const int32_t* slots, int64_t max_new, void* stream,
+               const char* what) {
     if (int e = check_cache(cache, false)) return e;
     if (int e = check_pages(pages)) return e;
     if (int e = check_same_pool(cache, pages)) return e;
@@ -171,6 +172,10 @@ int kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32
     if (pages->batch == 0 || cache->num_pages == 0 || cache->d == 0) return ok();
     if (accepted) { FP4_SCALAR_PTR(accepted); }
     FP4_SCALAR_PTR(accepted_lens);
+    if (reserved) {
+        FP4_SCALAR_PTR(slots);
+        if (max_new == 0) return ok();
+    }
     return hip_status(fp4::launch_kv_compact(*cache, *pages, accepted, max_accepted, accepted_lens, slots, max_new,
                                              static_cast<hipStream_t>(stream)),
                       what);
@@ -689,15 +694,15 @@ int fp4_kv_free(const fp4_kv_pages* pages, const int32_t* seqs, int64_t n, const
 
 int fp4_kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted, int64_t max_accepted,
                    const int32_t* accepted_lens, void* stream) {
-    return kv_compact(cache, pages, accepted, max_accepted, accepted_lens, nullptr, 0, stream, "fp4_kv_compact launch");
+    return kv_compact(cache, pages, accepted, max_accepted, accepted_lens, false, nullptr, 0, stream,
+                      "fp4_kv_compact launch");
 }
 
 int fp4_kv_compact_reserved(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted,
                             int64_t max_accepted, const int32_t* accepted_lens, const int32_t* slots, int64_t max_new,
                             void* stream) {
     FP4_REQUIRE(max_new >= 0, FP4_ERR_INVALID, "negative max_new=%lld", (long long)max_new);
-    FP4_SCALAR_PTR(slots);
-    return kv_compact(cache, pages, accepted, max_accepted, accepted_lens, slots, max_new, stream,
+    return kv_compact(cache, pages, accepted, max_accepted, accepted_lens, true, slots, max_new, stream,
                       "fp4_kv_compact_reserved launch");
 }
 

@@ -141,6 +141,8 @@ def test_commit_of_a_reservation_rejects_bad_arguments():
     assert commit(slots=None) == INVALID and commit(slots=FAKE + 2) == ALIGN and commit(max_new=-1) == INVALID
     assert commit(most=65) == INVALID and commit(lens=None) == INVALID and commit(pages=_pages(num_pages=11)) == INVALID
     assert commit(pages=_pages(batch=0)) == OK
+    assert commit(pages=_pages(batch=0), slots=None, lens=None, accepted=None) == OK      # nothing is read
+    assert commit(max_new=0) == OK                                                        # nothing was reserved
 
 
 def test_binding_checks_the_commit_of_a_reservation():
