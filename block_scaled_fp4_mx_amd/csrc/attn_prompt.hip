@@ -16,13 +16,16 @@
 // Weights are rounded to bf16 for the second product (they enter it with V's
 // 16-bit format); the rounded weights are what is summed, in fp32.
 //
-// Bound by the matrix core (4 D flop per visible pair and query head):
-//   16384 rows, 32 / 4 heads of 128 values: 1.94 ms, 1.13 PFLOP/s (a large library
-//   product reaches 1.37 on the same card); matrix cores busy 58% of the cycles, at
-//   a clock that falls to 1.75 GHz under this load, the rest the exponentials and
-//   sums, which two waves on a SIMD overlap in part;
-//   4 prompts of 7676 rows in all, 64 / 8 heads: 291 us, 0.84 PFLOP/s: a workgroup's
-//   queries and results (56 us of traffic in all) pass while it computes nothing;
+// Bound by the matrix core (4 D flop per visible pair and query head).  A call among
+// others:
+//   16384 rows, 32 / 4 heads of 128 values: 1.93 .. 2.05 ms from card to card, 1.07 ..
+//   1.14 PFLOP/s (a large library product reaches 1.37); matrix cores busy 59% of the
+//   cycles, at a clock that falls to 1.75 GHz under this load, the rest the exponentials
+//   and sums, which two waves on a SIMD overlap in part.  Heads of 64: 1.12 ms, 0.99
+//   PFLOP/s; of 256: 3.54 ms, 1.24 PFLOP/s;
+//   4 prompts of 7676 rows in all, 64 / 8 heads: 292 .. 295 us, 0.84 PFLOP/s (traced one
+//   call after another 290 .. 360), matrix cores busy 45%: a workgroup starts with a cold
+//   query and first tile, and has 17 tiles on average to make up for it;
 //   24 prompts of 3 .. 421 rows, 16 / 16 heads of 64: 13 us, one round of workgroups.
 // Tried and slower or alike: tiles loaded through registers into padded LDS rows (2.41
 // ms), interleaving the two halves' products, s_setprio around them.
@@ -33,8 +36,9 @@ namespace fp4 {
 namespace {
 
 // Waves of a workgroup, 32 query rows each.  8 waves (256 rows) at D = 256 keep two
-// waves per SIMD in 256 registers, where 4 take 420; below, 4 and 8 measured alike
-// (16384 rows: 2.04 and 1.97 ms; four documents of 8k rows in all: 341 and 357 us).
+// waves per SIMD in 256 registers (and 6 spilled ones), where 4 take 420; below, 4 and 8
+// measured alike (16384 rows: 2.04 and 1.97 ms; four documents of 8k rows in all: 341
+// and 357 us).
 constexpr int waves_of(int head_dim) { return head_dim == 256 ? 8 : 4; }
 constexpr float kSlack = 8.0f;
 constexpr float kNone = -__builtin_inff();   // score of a hidden token

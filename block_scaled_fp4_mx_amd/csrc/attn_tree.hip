@@ -31,26 +31,36 @@
 // a cut goes through leaves partial (m, sum, o) in the workspace, at most two
 // per range, and a second kernel joins them in order.
 //
-// What bounds it: a token's keys and values are 2 * (d/2 + d/32) bytes and are read
-// once for all query rows of a sequence, which HBM would do at 5 TB/s; the
-// instructions that widen FP4, turn V and take the exponentials cost more.  At 32
+// What bounds it: a token's keys and values are 2 * (d/2 + d/32) bytes, which HBM
+// would give at 5 TB/s, and are read once for up to 64 query rows of a key/value head
+// (16 at 256 values; more rows take more columns of workgroups, which read them
+// again).  With one token to a sequence that is the bound.  With drafts, the
+// instructions that widen FP4, turn V and take the exponentials cost more: at 32
 // rows a head a step of 32 tokens takes a wave about 320 instructions, 34 of them
-// matrix products.  Of the 169 us that the second case below takes with its copies
+// matrix products.  Of the 169 us that the long contexts below take with their copies
 // left out, leaving out a kind more saves: products 70, conversions 35, exponentials
 // 33, turning V 15, the meeting of the waves 10.
-// 64 / 8 heads of 128 values, kernel and join:
-//   64 sequences of 0 .. 8191 tokens, 8 drafts (287 MB)      113 + 13 us, 2.5 TB/s
-//   4 of 90001 .. 131072 tokens, 16 drafts (524 MB)          188 +  9 us, 2.7 TB/s
-//   one of 100000 tokens, 1 draft (109 MB)                    24 +  8 us, 4.5 TB/s
-//   one of 1500 tokens, 1 draft                              8.4 + 4.8 us, latency
+// Heads of 128 values, over several cards: a call among others, and kernel + join
+// traced one call after another, which add up to more:
+//   64 sequences of 0 .. 8191 tokens, 8 drafts,
+//     64 / 8 heads (287 MB)              112 .. 118 us, 2.5 TB/s   105 .. 120 + 13
+//   4 of 90001 .. 131072, 16 drafts,
+//     32 / 8 heads (524 MB)              183 .. 193 us, 2.8 TB/s   188 .. 225 + 10
+//   the same, 64 / 8 heads, two columns         345 us
+//   64 of 4096, 1 token, 64 / 8 heads (287 MB)   60 us, 4.8 TB/s         53 +  7
+//   one of 100000, 1 token, 64 / 8 (109 MB)      32 us, 3.4 TB/s         24 +  8
+//   one of 1500, 1 token, 64 / 8                 13 us, latency         8.8 + 5.2
+// In what follows "first" and "second" case are the first two of these, by the
+// kernels' least times.
 // Tried and slower: each wave loading its head in the matrix core's layout (first
 // case 128 us: half-line requests), 64 rows to a wave (154 us), three waves to a SIMD
 // (151 us, spills), 64 tokens a step (117 us), 1 row tile of 16 to a wave (162 us).
 // No faster: a tile's scores worked out beside the softmax of the one before (112 and
 // 190 us), three tiles in flight (113 and 191 us).  Counters of the second case: the
 // vector unit is issued to in 53% of the cycles (and holds exponentials longer), the
-// matrix core busy in 31%; a wave issues 45% of its time, waits 28% for a unit and 27%
-// for LDS and its workgroup.
+// matrix core busy in 30%; a wave issues 45% of its time, waits 28% for a unit and 27%
+// for LDS and its workgroup.  30% of the LDS cycles are bank conflicts, in both cases,
+// whose reads have not been told apart.
 #include <type_traits>
 
 #include "fp4_internal.h"
@@ -64,9 +74,9 @@ constexpr int kTile = 32;                  // tokens per step
 // join: 8.4 + 4.8 us; with 4, 12.2 + 4.0; with 1, 7.8 + 5.2, but over 8000 tokens
 // 11.8 + 5.6 against 11.2 + 4.8.
 constexpr int kMinTiles = 2;
-// Waves of a full grid, two per SIMD.  The long contexts above, with one row group,
-// take 198 + 11 us; with 1024 waves 236 + 14, with 4096 228 + 20 (twice the partial
-// results).
+// Waves of a full grid, two per SIMD (of which one fits at 256 values, where a wave
+// takes 264 registers and more).  The long contexts above, with one row group, take
+// 198 + 11 us; with 1024 waves 236 + 14, with 4096 228 + 20 (twice the partial results).
 constexpr int kGridWaves = 2048;
 constexpr float kSlack = 8.0f;             // scores may exceed the reference by 2^8
 constexpr float kNone = -__builtin_inff();   // score of a hidden token
@@ -147,7 +157,10 @@ __device__ __forceinline__ Chunk chunk_at(const TreeArgs& a, int first, int lane
     return c;
 }
 
-// All tiles of the batch; c: its first chunk.
+// All tiles of the batch; c: its first chunk.  Every workgroup of both kernels walks
+// the lengths so, 64 sequences a step, and the join has workgroups for each sequence:
+// the cost grows with the batch's square.  Sequences of 100 tokens, 1 token each: 64 of
+// them 16 us, 256 26, 512 60, 1024 162, 4096 1980 (116 us of bytes).
 __device__ __forceinline__ int64_t all_tiles(const TreeArgs& a, const Chunk& c, int lane) {
     int64_t n = c.all();
     for (int b = 64; b < a.batch; b += 64) n += chunk_at(a, b, lane).all();
@@ -852,7 +865,7 @@ hipError_t launch(const TreeArgs& a, const Layout& l, hipStream_t s) {
     const unsigned row_tiles = (unsigned)(a.kv_heads * a.row_tiles);
     // Many pieces of few rows (on average of the sequences, and so that all workgroups
     // are resident): 16 waves to a slice.  One sequence of 100000 tokens: 8 us, against
-    // 37 with a wave to a slice; 4 of 131072 with 16 drafts: 16 us against 11.
+    // 37 with a wave to a slice; the 4 long contexts with 16 drafts: 16 us against 11.
     if (1 << l.shift >= 16 * a.batch && (int64_t)row_tiles * a.batch * (D / 16) <= 512)
         attn_tree_join_kernel<D, 1, 16><<<dim3(row_tiles, (unsigned)a.batch, D / 16), 1024, 0, s>>>(a);
     else

@@ -11,9 +11,10 @@
 // All but copy_pages are bound by latency: a launch and two to four round trips to
 // memory.  64 sequences of 200 .. 4096 tokens in pages of 64 rows of 1024 values, 8
 // new tokens each: free 3.0 us, plan 6.3 (7.0 with the references asked for after the
-// sequences' needs), apply 2.6, compact 5.5 (7.7 with one array read after another).
-// 16 sequences forked into 8 each: fork 4.2; apply 4.5 where each child copies its last
-// page (6.3 with one workgroup to a sequence instead of 8).
+// sequences' needs), apply 2.5 .. 3.2, compact 5.6 (7.7 with one array read after
+// another), by a reservation's slots 6.2.  16 sequences forked into 8 each: fork 4.2;
+// apply 4.7 where each child copies its last page (6.3 with one workgroup to a sequence
+// instead of 8).
 #include "fp4_internal.h"
 
 namespace fp4 {
@@ -86,7 +87,8 @@ __device__ __forceinline__ int32_t held_pages(const fp4_kv_pages& t, int64_t b) 
 // One workgroup: what each sequence needs (in order), then the free pages in
 // ascending order up to that many.  The reference counts of a 32768-page pool
 // are 128 KiB, so one workgroup's read of them is short, and it stops at the
-// last page needed.
+// last page needed.  A pool of a million pages costs the same while low ones are free,
+// and 0.6 ms where only its last 4096 are.
 __global__ __launch_bounds__(kPlanThreads) void reserve_plan_kernel(fp4_kv_pages t, const int32_t* new_tokens,
                                                                     int64_t page_size, int32_t* n_short, ReserveWs ws) {
     __shared__ int64_t sums[2 * kPlanWaves];
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(fp4_kv_cache c, fp4_k
 // Whole pages: kThreads * kCopyUnits units of one pair to a workgroup; a pair's
 // units run through key codes, key scales, value codes, value scales.  Bound by
 // HBM; neither side is read again soon, so loads and stores pass the caches by.
-// 8192 pages of 64 rows of 1024 values (1.14 GB read and written): 225 us, 5.07 TB/s;
+// 8192 pages of 64 rows of 1024 values (1.14 GB read and written): 223 us, 5.1 TB/s;
 // 234 us with plain loads and stores, 338 us with those and 8 units to a lane.
 __global__ __launch_bounds__(kThreads) void copy_pages_kernel(fp4_kv_cache src, fp4_kv_cache dst,
                                                               const int32_t* src_pages, const int32_t* dst_pages,

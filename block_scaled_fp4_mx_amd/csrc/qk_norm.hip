@@ -13,9 +13,9 @@
 // raw input words are exchanged (4 words) and normalized again, which is less
 // than exchanging 8 fp32 results.
 //
-// 72 heads of 128 values: 8192 tokens (306 MB) 70 us, 4.4 TB/s; 64 tokens 3.6 us, one
+// 72 heads of 128 values: 8192 tokens (306 MB) 71 us, 4.3 TB/s; 64 tokens 3.5 us, one
 // round trip to memory.  4097 tokens of 24 heads of 96 values (39 MB, a quarter of the
-// lanes idle) 10.3 us, 3.8 TB/s.
+// lanes idle) 10.5 us, 3.7 TB/s.
 #include "fp4_internal.h"
 
 namespace fp4 {
