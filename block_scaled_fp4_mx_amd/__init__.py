@@ -20,7 +20,7 @@ __all__ = [
     "fp4_scale_max_workspace_bytes",
     "fp4_dequant", "fp4_gemm", "fp4_quantize_mxfp8", "fp4_mx_to_mxfp8", "fp4_mx_dequant_fp8", "fp4_gemm_w4a8", "fp4_fake_quant",
     "fp4_ste_backward", "fp4_kv_append_mx", "fp4_moe_grouped_gemm", "fp4_moe_workspace_bytes", "MoeDebug",
-    "fp4_qk_norm_rope", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
+    "fp4_qk_norm_rope", "fp4_kv_append_rope_mx", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
     "fp4_kv_free", "fp4_kv_compact", "fp4_kv_compact_reserved", "fp4_kv_copy_pages", "fp4_attn_tree_mx",
     "fp4_attn_tree_workspace_bytes", "fp4_attn_prompt",
     "fp4_abi_version", "LIB_PATH",
@@ -65,6 +65,8 @@ _SIGS = {
     "fp4_moe_workspace_bytes": (_sz, [_i32, _i64, _i64, _i32, _i32, _i64]),
     "fp4_qk_norm_rope": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _c.c_float, _vp, _i64, _i32,
                                 _i32, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "fp4_kv_append_rope_mx": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _i32,
+                                     _c.c_float, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp]),
     "fp4_kv_reserve": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "fp4_kv_reserve_workspace_bytes": (_sz, [_i64, _i64]),
     "fp4_kv_fork": (_i32, [_vp, _vp, _i64, _i64, _vp]),
@@ -473,6 +475,18 @@ class KvPages(NamedTuple):
     page_counts: torch.Tensor
     seq_lens: torch.Tensor
     page_refs: torch.Tensor
+
+
+def fp4_kv_append_rope_mx(q, k, v, cache: KvCache, slots, q_out=None, positions=None, cos_sin=None, norm=False, q_weight=None,
+                          k_weight=None, eps=1e-6, interleaved=False, stream=None):
+    """q [tokens, q_heads, head_dim] (None: none), k, v [tokens, kv_heads, head_dim]:
+    queries rotated into q_out (which may be q), keys rotated and values as they are
+    into the cache's rows slots int32 [tokens] (-1: not appended).  norm: with
+    fp4_qk_norm_rope's head norms, and then its bytes; cos_sin: fp32 [max_positions,
+    rot_dim]; None: no rotation."""
+    _check("fp4_kv_append_rope_mx",
+           _binding.fp4_kv_append_rope_mx(q, k, v, cache, slots, q_out, positions, cos_sin, norm, q_weight, k_weight, eps,
+                                          interleaved, stream))
 
 
 def fp4_kv_reserve_workspace_bytes(batch: int, num_pages: int) -> int:

@@ -645,6 +645,127 @@ int fp4_qk_norm_rope(const void* q, const void* k, int64_t tokens, int q_heads, 
     return hip_status(fp4::launch_qk_norm_rope(p, static_cast<hipStream_t>(stream)), "fp4_qk_norm_rope launch");
 }
 
+int fp4_kv_append_rope_mx(const void* q, const void* k, const void* v, int64_t tokens, int q_heads, int kv_heads,
+                          int head_dim, int64_t ld_q, int64_t ld_k, int64_t ld_v, int norm, const void* q_weight,
+                          const void* k_weight, fp4_dtype weight_dtype, float eps, const float* cos_sin,
+                          int64_t max_positions, int rot_dim, int interleaved, const int32_t* positions, void* q_out,
+                          int64_t ld_qo, const fp4_kv_cache* cache, const int32_t* slots, void* stream) {
+    FP4_REQUIRE(tokens >= 0 && q_heads >= 0, FP4_ERR_INVALID, "negative size tokens=%lld q_heads=%d", (long long)tokens,
+                q_heads);
+    FP4_REQUIRE(kv_heads >= 1, FP4_ERR_INVALID, "kv_heads=%d must be positive", kv_heads);
+    FP4_REQUIRE(weight_dtype == FP4_DT_BF16 || weight_dtype == FP4_DT_F32, FP4_ERR_INVALID, "bad dtype %d",
+                (int)weight_dtype);
+    FP4_REQUIRE(!norm || (eps >= 0.0f && std::isfinite(eps)), FP4_ERR_INVALID, "eps=%g is negative or not finite",
+                (double)eps);
+    FP4_REQUIRE(norm || (q_weight == nullptr && k_weight == nullptr), FP4_ERR_INVALID, "weights are given without norm");
+    FP4_REQUIRE(head_dim >= 32 && head_dim <= 256 && head_dim % 32 == 0, FP4_ERR_SHAPE,
+                "head_dim=%d is not a multiple of 32 in [32, 256]", head_dim);
+    FP4_REQUIRE(rot_dim >= 0 && rot_dim <= head_dim && rot_dim % 16 == 0, FP4_ERR_SHAPE,
+                "rot_dim=%d is not a multiple of 16 in [0, head_dim=%d]", rot_dim, head_dim);
+    FP4_REQUIRE(tokens < (int64_t)1 << 24, FP4_ERR_SHAPE, "tokens=%lld too large", (long long)tokens);
+    FP4_REQUIRE(q_heads <= 65536 && kv_heads <= 65536, FP4_ERR_SHAPE, "q_heads=%d kv_heads=%d too large", q_heads,
+                kv_heads);
+    if (int e = check_cache(cache, false)) return e;
+    const int64_t wq = (int64_t)q_heads * head_dim, wk = (int64_t)kv_heads * head_dim;
+    FP4_REQUIRE(cache->d == wk, FP4_ERR_SHAPE, "the cache has d=%lld, kv_heads * head_dim is %lld", (long long)cache->d,
+                (long long)wk);
+    const int64_t capacity = cache->num_pages * cache->page_size;
+    if (tokens == 0 || (q_heads == 0 && capacity == 0)) return ok();
+    const bool values = capacity && cache->v_codes;
+    if (q_heads) {
+        FP4_PTR(q);
+        FP4_PTR(q_out);
+        if (int e = check_ld(ld_q, wq, "ld_q")) return e;
+        if (int e = check_ld(ld_qo, wq, "ld_qo")) return e;
+    }
+    if (capacity) {
+        FP4_PTR(k);
+        if (int e = check_ld(ld_k, wk, "ld_k")) return e;
+    }
+    if (values) {
+        FP4_PTR(v);
+        if (int e = check_ld(ld_v, wk, "ld_v")) return e;
+    }
+    if (q_heads == 0) q_weight = nullptr;
+    FP4_REQUIRE(aligned16(q_weight), FP4_ERR_ALIGN, "q_weight is not 16-byte aligned");
+    FP4_REQUIRE(aligned16(k_weight), FP4_ERR_ALIGN, "k_weight is not 16-byte aligned");
+    FP4_SCALAR_PTR(slots);
+    if (rot_dim) {
+        FP4_PTR(cos_sin);
+        FP4_SCALAR_PTR(positions);
+        FP4_REQUIRE(max_positions >= 0, FP4_ERR_INVALID, "negative max_positions=%lld", (long long)max_positions);
+    }
+    FP4_REQUIRE(!q_heads || (q_out == q && ld_qo == ld_q) ||
+                    !rows_overlap(q_out, ld_qo * 2, wq * 2, q, ld_q * 2, wq * 2, tokens),
+                FP4_ERR_INVALID, "q_out overlaps q without being q itself");
+    FP4_REQUIRE(!q_heads || !capacity || !rows_overlap(q_out, ld_qo * 2, wq * 2, k, ld_k * 2, wk * 2, tokens),
+                FP4_ERR_INVALID, "q_out overlaps k");
+    FP4_REQUIRE(!q_heads || !values || !rows_overlap(q_out, ld_qo * 2, wq * 2, v, ld_v * 2, wk * 2, tokens),
+                FP4_ERR_INVALID, "q_out overlaps v");
+    const uint64_t weight_bytes = (uint64_t)head_dim * (weight_dtype == FP4_DT_F32 ? 4 : 2);
+    // Addresses end at 2^57: no table is longer.
+    const uint64_t places = (uint64_t)(max_positions < (int64_t)1 << 45 ? max_positions : (int64_t)1 << 45);
+    const uint64_t codes = (uint64_t)capacity * (uint64_t)(wk / 2), scales = (uint64_t)capacity * (uint64_t)(wk / 32);
+    struct Run {
+        const char* name;
+        const void* start;
+        uint64_t bytes;
+    };
+    // What is read besides the rows, then the cache, which is written.
+    const Run runs[] = {{"q_weight", q_weight, q_weight ? weight_bytes : 0},
+                        {"k_weight", k_weight, k_weight ? weight_bytes : 0},
+                        {"cos_sin", cos_sin, rot_dim ? places * rot_dim * 4 : 0},
+                        {"positions", positions, rot_dim ? (uint64_t)tokens * 4 : 0},
+                        {"slots", slots, (uint64_t)tokens * 4},
+                        {"k_codes", cache->k_codes, codes},
+                        {"k_scales", cache->k_scales, scales},
+                        {"v_codes", cache->v_codes, values ? codes : 0},
+                        {"v_scales", cache->v_scales, values ? scales : 0}};
+    constexpr int kRuns = sizeof(runs) / sizeof(runs[0]), kRead = 5;
+    for (int i = 0; i < kRuns; ++i) {
+        FP4_REQUIRE(!q_heads || !run_overlaps(q_out, ld_qo * 2, wq * 2, tokens, runs[i].start, runs[i].bytes),
+                    FP4_ERR_INVALID, "q_out overlaps %s", runs[i].name);
+        if (i < kRead || runs[i].bytes == 0) continue;
+        FP4_REQUIRE(!q_heads || !run_overlaps(q, ld_q * 2, wq * 2, tokens, runs[i].start, runs[i].bytes), FP4_ERR_INVALID,
+                    "%s overlaps q", runs[i].name);
+        FP4_REQUIRE(!run_overlaps(k, ld_k * 2, wk * 2, tokens, runs[i].start, runs[i].bytes), FP4_ERR_INVALID,
+                    "%s overlaps k", runs[i].name);
+        FP4_REQUIRE(!values || !run_overlaps(v, ld_v * 2, wk * 2, tokens, runs[i].start, runs[i].bytes), FP4_ERR_INVALID,
+                    "%s overlaps v", runs[i].name);
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(runs[i].start), y = reinterpret_cast<uintptr_t>(runs[j].start);
+            FP4_REQUIRE(runs[j].bytes == 0 || x >= y + runs[j].bytes || y >= x + runs[i].bytes, FP4_ERR_INVALID,
+                        "%s overlaps %s", runs[i].name, runs[j].name);
+        }
+    }
+    fp4::RopeAppend p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.tokens = tokens;
+    p.q_heads = q_heads;
+    p.kv_heads = kv_heads;
+    p.head_dim = head_dim;
+    p.ld_q = ld_q;
+    p.ld_k = ld_k;
+    p.ld_v = ld_v;
+    p.norm = norm != 0;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.w_f32 = weight_dtype == FP4_DT_F32;
+    p.eps = eps;
+    p.cos_sin = cos_sin;
+    p.max_positions = max_positions;
+    p.rot_dim = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.positions = positions;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.ld_qo = ld_qo;
+    p.cache = *cache;
+    p.slots = slots;
+    return hip_status(fp4::launch_kv_append_rope(p, static_cast<hipStream_t>(stream)), "fp4_kv_append_rope_mx launch");
+}
+
 size_t fp4_kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages) {
     return batch > 0 && num_pages >= 0 ? fp4::kv_reserve_workspace_bytes(batch, num_pages) : 0;
 }

@@ -312,6 +312,46 @@ PyObject* qk_norm_rope(PyObject* const* v) {
     });
 }
 
+PyObject* kv_append_rope_mx(PyObject* const* v) {
+    Call call("fp4_kv_append_rope_mx");
+    const char* fn = call.name();
+    const Tensor& k = call("k", v[1], kBF16, false);
+    Cache cache = cache_of(call, v[3], kCacheNames);
+    const Tensor* val = cache.vc ? &call("v", v[2], kBF16, false) : nullptr;
+    const Tensor* q = v[0] == Py_None ? nullptr : &call("q", v[0], kBF16, false);
+    const Tensor* qo = q ? &call("q_out", v[5], kBF16, false) : nullptr;
+    const Tensor& slots = call("slots", v[4], kI32);
+    const int norm = PyObject_IsTrue(v[8]), interleaved = PyObject_IsTrue(v[12]);
+    if (norm < 0 || interleaved < 0) throw PythonError();
+    const Tensor* qw = call.optional("q_weight", v[9], kWeight);
+    const Dtypes same = !qw ? kWeight : qw->scalar_type() == at::kFloat ? kF32 : kBF16;
+    const Tensor* kw = call.optional("k_weight", v[10], same);
+    const Tensor* table = call.optional("cos_sin", v[7], kF32);
+    const Tensor* where = table ? &call("positions", v[6], kI32) : nullptr;
+    const float eps = (float)number(v[11]);
+    const int64_t ld_k = heads_of(call, "k", k), ld_v = val ? heads_of(call, "v", *val) : 0, ld_q = q ? heads_of(call, "q", *q) : 0,
+                  ld_qo = q ? heads_of(call, "q_out", *qo) : 0;
+    const int64_t tokens = k.size(0), d = k.size(2);
+    check_shapes(call, cache);
+    has_shape(call, "v", val, k.sizes());
+    if (q && (q->size(0) != tokens || q->size(2) != d))
+        fail(PyExc_ValueError, "%s: q has shape %s, k %s", fn, text(q->sizes()).c_str(), text(k.sizes()).c_str());
+    if (q) has_shape(call, "q_out", qo, q->sizes());
+    has_shape(call, "slots", &slots, {tokens});
+    has_shape(call, "q_weight", qw, {d});
+    has_shape(call, "k_weight", kw, {d});
+    if (table && (table->dim() != 2 || where->dim() != 1 || where->size(0) != tokens))
+        fail(PyExc_ValueError, "%s: cos_sin must be [max_positions, rot_dim] and positions [tokens]", fn);
+    const bool f32 = (qw && qw->scalar_type() == at::kFloat) || (kw && kw->scalar_type() == at::kFloat);
+    return call.go(v[13], [&](void* s) {
+        return fp4_kv_append_rope_mx(pointer(q), pointer(k), pointer(val), tokens, q ? (int)q->size(1) : 0, (int)k.size(1),
+                                     (int)d, ld_q, ld_k, ld_v, norm, pointer(qw), pointer(kw),
+                                     f32 ? FP4_DT_F32 : FP4_DT_BF16, eps, pointer<float>(table), table ? table->size(0) : 0,
+                                     table ? (int)table->size(1) : 0, interleaved, pointer<int32_t>(where), pointer(qo), ld_qo,
+                                     &cache.c, pointer<int32_t>(slots), s);
+    });
+}
+
 PyObject* kv_reserve(PyObject* const* v) {
     Call call("fp4_kv_reserve");
     Cache cache = cache_of(call, v[0], kCacheNames);
@@ -483,6 +523,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {
     method<kv_append_mx, 8>("fp4_kv_append_mx"),
     method<qk_norm_rope, 11>("fp4_qk_norm_rope"),
+    method<kv_append_rope_mx, 14>("fp4_kv_append_rope_mx"),
     method<kv_reserve, 7>("fp4_kv_reserve"),
     method<kv_fork, 4>("fp4_kv_fork"),
     method<kv_free, 5>("fp4_kv_free"),

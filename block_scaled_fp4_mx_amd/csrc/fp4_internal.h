@@ -152,6 +152,27 @@ struct QkNorm {
 };
 hipError_t launch_qk_norm_rope(const QkNorm& p, hipStream_t s);
 
+struct RopeAppend {
+    const uint16_t *q, *k, *v;
+    int64_t tokens;
+    int q_heads, kv_heads, head_dim;
+    int64_t ld_q, ld_k, ld_v;
+    bool norm;
+    const void *q_weight, *k_weight;
+    int w_f32;
+    float eps;
+    const float* cos_sin;
+    int64_t max_positions;
+    int rot_dim;
+    bool interleaved;
+    const int32_t* positions;
+    uint16_t* q_out;
+    int64_t ld_qo;
+    fp4_kv_cache cache;
+    const int32_t* slots;
+};
+hipError_t launch_kv_append_rope(const RopeAppend& p, hipStream_t s);
+
 size_t kv_reserve_workspace_bytes(int64_t batch, int64_t num_pages);
 hipError_t launch_kv_reserve(const fp4_kv_cache& c, const fp4_kv_pages& t, const int32_t* new_tokens, int32_t* slots,
                              int64_t max_new, int32_t* n_short, void* ws, hipStream_t s);

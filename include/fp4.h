@@ -446,6 +446,32 @@ typedef struct fp4_kv_cache {
 } fp4_kv_cache;
 
 /*
+ * The step from a layer's projections to its cache in one pass: the rotation of
+ * fp4_qk_norm_rope on queries and keys, with its head norms where norm != 0 and
+ * without any otherwise, and fp4_kv_append_mx of the keys and values to a cache:
+ *   q_out[t] = bf16(R(position) n(q[t])),
+ *   row slots[t] of the keys = MXFP4(bf16(R(position) n(k[t]))), of the values = MXFP4(v[t]),
+ * n the norm or nothing.  With norm != 0 every byte is what fp4_qk_norm_rope and
+ * two fp4_kv_append_mx give.  Arguments are as there; without norm, q_weight and
+ * k_weight must be NULL and eps is ignored.
+ * A token whose position lies outside [0, max_positions) is padding: nothing of it is
+ * written.  One whose slot lies outside the cache is not appended, its query row is
+ * written.  Slots in range must be distinct.  rot_dim 0: nothing turns, cos_sin and
+ * positions ignored (may be NULL).  q_heads may be 0 (q and q_out ignored); a cache
+ * without values takes the keys alone (v ignored).  Inputs must be finite.
+ * q_out may be q itself (same pointer and leading dimension); any other overlap of
+ * q_out or the cache with an input or with one another is FP4_ERR_INVALID.
+ * Errors: head_dim not a multiple of 32 in [32, 256], rot_dim not a multiple of 16 in
+ * [0, head_dim], cache->d != kv_heads * head_dim, 2^24 tokens or more -> FP4_ERR_SHAPE;
+ * eps negative or not finite, weights without norm, kv_heads < 1 -> FP4_ERR_INVALID.
+ */
+int fp4_kv_append_rope_mx(const void* q, const void* k, const void* v, int64_t tokens, int q_heads, int kv_heads,
+                          int head_dim, int64_t ld_q, int64_t ld_k, int64_t ld_v, int norm, const void* q_weight,
+                          const void* k_weight, fp4_dtype weight_dtype, float eps, const float* cos_sin,
+                          int64_t max_positions, int rot_dim, int interleaved, const int32_t* positions, void* q_out,
+                          int64_t ld_qo, const fp4_kv_cache* cache, const int32_t* slots, void* stream);
+
+/*
  * Which pages the sequences of a batch hold (all device memory):
  *   page_table  int32 [batch, max_pages]  page of tokens i*page_size.., -1 = none
  *   page_counts int32 [batch]             entries of the row in use

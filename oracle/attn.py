@@ -40,6 +40,27 @@ def norm_rope(xbits, weight, eps, cos_sin, positions, interleaved):
     return out, size
 
 
+def turned_bf16(xbits, cos_sin, positions, interleaved):
+    """xbits uint16 [tokens, heads, d] (bf16) turned by the positions' angles, to bf16 bits:
+    each turned value is a cos -+ rn(b sin) with the inner product rounded to fp32 and the
+    whole to fp32 once more (a fused multiply-add), then to bf16.  float64 holds a cos and
+    its sum with the fp32 product exactly, or to 2^-52 where they are 2^21 apart.  Rows of
+    positions outside the table come back as they are."""
+    x = F.bf16_bits_to_f64(xbits)
+    out = x.astype(np.float32)
+    half = cos_sin.shape[1] // 2
+    live = (np.asarray(positions) >= 0) & (np.asarray(positions) < len(cos_sin))
+    row = np.where(live[:, None], cos_sin[np.where(live, positions, 0)], 0.0).astype(np.float32)[:, None]
+    c, s = row[..., :half].astype(np.float64), row[..., half:].astype(np.float64)
+    first = slice(0, 2 * half, 2) if interleaved else slice(0, half)
+    second = slice(1, 2 * half, 2) if interleaved else slice(half, 2 * half)
+    a, b = x[..., first], x[..., second]
+    for at, u, w, sign in ((first, a, b, -1.0), (second, b, a, 1.0)):
+        inner = (w * s).astype(np.float32).astype(np.float64)
+        out[..., at] = np.where(live[:, None, None], (u * c + sign * inner).astype(np.float32), out[..., at])
+    return F.fp32_to_bf16_bits_rne(out)
+
+
 # ---------------------------------------------------------------------- attention
 
 def attend(q, k, v, visible, scale):
