@@ -22,7 +22,8 @@ __all__ = [
     "fp4_ste_backward", "fp4_kv_append_mx", "fp4_moe_grouped_gemm", "fp4_moe_workspace_bytes", "MoeDebug",
     "fp4_qk_norm_rope", "fp4_kv_append_rope_mx", "KvCache", "KvPages", "fp4_kv_reserve", "fp4_kv_reserve_workspace_bytes", "fp4_kv_fork",
     "fp4_kv_free", "fp4_kv_compact", "fp4_kv_compact_reserved", "fp4_kv_copy_pages", "fp4_attn_tree_mx",
-    "fp4_attn_tree_workspace_bytes", "fp4_attn_prompt",
+    "fp4_attn_tree_workspace_bytes", "fp4_attn_shared_mx", "fp4_attn_shared_workspace_bytes", "fp4_kv_select_mx",
+    "fp4_kv_select_workspace_bytes", "fp4_attn_blocks_mx", "fp4_attn_blocks_workspace_bytes", "fp4_attn_prompt",
     "fp4_abi_version", "LIB_PATH",
 ]
 
@@ -77,6 +78,15 @@ _SIGS = {
     "fp4_attn_tree_mx": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _c.c_float, _vp,
                                 _i64, _vp, _sz, _vp]),
     "fp4_attn_tree_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "fp4_attn_shared_mx": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i32,
+                                  _c.c_float, _vp, _i64, _vp, _sz, _vp]),
+    "fp4_attn_shared_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, _i64]),
+    "fp4_kv_select_mx": (_i32, [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i32,
+                                _vp, _vp, _vp, _sz, _vp]),
+    "fp4_kv_select_workspace_bytes": (_sz, [_i64, _i32, _i32, _i64]),
+    "fp4_attn_blocks_mx": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i64, _i32, _i32, _i32, _i32,
+                                  _c.c_float, _vp, _i64, _vp, _sz, _vp]),
+    "fp4_attn_blocks_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
     "fp4_attn_prompt": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i64, _i64, _i64, _c.c_float, _vp, _i64,
                                _vp]),
 }
@@ -539,6 +549,47 @@ def fp4_attn_tree_mx(q, cache: KvCache, page_table, seq_lens, out, workspace, dr
     (bit j: sees drafted token j; None: tokens up to itself); scale None: head_dim ** -0.5."""
     _check("fp4_attn_tree_mx", _binding.fp4_attn_tree_mx(q, cache, page_table, seq_lens, out, workspace, draft_lens, tree_mask,
                                                          scale, stream))
+
+
+def fp4_attn_shared_workspace_bytes(batch: int, drafts: int, q_heads: int, head_dim: int, kv_heads: int, num_groups: int) -> int:
+    return lib.fp4_attn_shared_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads, num_groups)
+
+
+def fp4_attn_shared_mx(q, cache: KvCache, page_table, seq_lens, groups, prefix_lens, out, workspace, draft_lens=None,
+                       tree_mask=None, scale=None, stream=None):
+    """fp4_attn_tree_mx where the sequences [groups[g], groups[g + 1]) (int32
+    [num_groups + 1]) share their first prefix_lens[g] (int32 [num_groups]) tokens,
+    which are attended once for all of them."""
+    _check("fp4_attn_shared_mx", _binding.fp4_attn_shared_mx(q, cache, page_table, seq_lens, groups, prefix_lens, out, workspace,
+                                                             draft_lens, tree_mask, scale, stream))
+
+
+def fp4_kv_select_workspace_bytes(batch: int, drafts: int, lists: int, max_pages: int) -> int:
+    return lib.fp4_kv_select_workspace_bytes(batch, drafts, lists, max_pages)
+
+
+def fp4_kv_select_mx(q, index_codes, index_scales, page_table, seq_lens, page_size, block_ids, workspace, draft_lens=None,
+                     scores=None, n_first=0, n_recent=0, stream=None):
+    """q [batch, drafts, lists, dim] against an MXFP4 entry for every page (uint8
+    [num_pages, lists * dim/2] and [num_pages, lists * dim/32]): for each query token and
+    list the best of the sequence's complete blocks into block_ids int32 [batch, drafts,
+    lists, n_select], ascending, -1 behind them; their scores into scores (fp32, the same
+    shape).  The first n_first and last n_recent complete blocks are taken before others."""
+    _check("fp4_kv_select_mx", _binding.fp4_kv_select_mx(q, index_codes, index_scales, page_table, seq_lens, page_size, block_ids,
+                                                         workspace, draft_lens, scores, n_first, n_recent, stream))
+
+
+def fp4_attn_blocks_workspace_bytes(batch: int, drafts: int, q_heads: int, head_dim: int, kv_heads: int) -> int:
+    return lib.fp4_attn_blocks_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads)
+
+
+def fp4_attn_blocks_mx(q, cache: KvCache, page_table, seq_lens, block_ids, out, workspace, draft_lens=None, tree_mask=None,
+                       scale=None, stream=None):
+    """fp4_attn_tree_mx over the blocks (pages) that block_ids int32 [batch, drafts, 1 or
+    kv_heads, n_select] names for each query token, the tokens behind the last complete
+    block and the drafted ones."""
+    _check("fp4_attn_blocks_mx", _binding.fp4_attn_blocks_mx(q, cache, page_table, seq_lens, block_ids, out, workspace, draft_lens,
+                                                             tree_mask, scale, stream))
 
 
 def fp4_attn_prompt(q, k, v, cu_seqlens, out, scale=None, stream=None):

@@ -160,6 +160,80 @@ int check_heads(int q_heads, int kv_heads, int head_dim) {
     return FP4_OK;
 }
 
+// The arguments that the attention entry points over the cache have in common.
+struct CacheAttn {
+    const void* q;
+    int64_t ld_q;
+    const fp4_kv_cache* cache;
+    const int32_t* page_table;
+    int64_t max_pages;
+    const int32_t *seq_lens, *draft_lens;
+    const uint64_t* tree_mask;
+    int64_t batch;
+    int drafts, q_heads, kv_heads, head_dim;
+    float scale;
+    void* out;
+    int64_t ld_out;
+    void* workspace;
+    size_t workspace_bytes;
+};
+// What does not depend on there being a batch.
+int check_attn_sizes(const CacheAttn& c) {
+    if (int e = check_heads(c.q_heads, c.kv_heads, c.head_dim)) return e;
+    if (int e = check_cache(c.cache, true)) return e;
+    FP4_REQUIRE(c.cache->d == (int64_t)c.kv_heads * c.head_dim, FP4_ERR_SHAPE, "the cache has d=%lld, kv_heads * head_dim is %lld",
+                (long long)c.cache->d, (long long)c.kv_heads * c.head_dim);
+    FP4_REQUIRE(c.drafts >= 1 && c.drafts <= 64, FP4_ERR_INVALID, "drafts=%d outside [1, 64]", c.drafts);
+    FP4_REQUIRE(c.batch >= 0 && c.max_pages >= 0, FP4_ERR_INVALID, "negative size batch=%lld max_pages=%lld",
+                (long long)c.batch, (long long)c.max_pages);
+    FP4_REQUIRE(c.batch < 65536 && c.max_pages < (int64_t)1 << 31, FP4_ERR_SHAPE, "batch=%lld or max_pages=%lld too large",
+                (long long)c.batch, (long long)c.max_pages);
+    return check_scale(c.scale);
+}
+int check_attn_arrays(const CacheAttn& c) {
+    const int64_t width = (int64_t)c.q_heads * c.head_dim, ld_q = c.ld_q, ld_out = c.ld_out;
+    const void *q = c.q, *out = c.out;
+    const int32_t *page_table = c.page_table, *seq_lens = c.seq_lens;
+    FP4_PTR(q);
+    FP4_PTR(out);
+    if (int e = check_ld(ld_q, width, "ld_q")) return e;
+    if (int e = check_ld(ld_out, width, "ld_out")) return e;
+    if (c.max_pages) { FP4_SCALAR_PTR(page_table); }
+    FP4_SCALAR_PTR(seq_lens);
+    FP4_REQUIRE((reinterpret_cast<uintptr_t>(c.draft_lens) & 3u) == 0, FP4_ERR_ALIGN, "draft_lens is not 4-byte aligned");
+    FP4_REQUIRE((reinterpret_cast<uintptr_t>(c.tree_mask) & 7u) == 0, FP4_ERR_ALIGN, "tree_mask is not 8-byte aligned");
+    FP4_REQUIRE(!rows_overlap(out, ld_out * 2, width * 2, q, ld_q * 2, width * 2, c.batch * c.drafts), FP4_ERR_INVALID,
+                "out overlaps q");
+    return FP4_OK;
+}
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    FP4_REQUIRE(workspace != nullptr && bytes >= need, FP4_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                workspace ? bytes : (size_t)0);
+    FP4_REQUIRE(aligned16(workspace), FP4_ERR_ALIGN, "workspace is not 16-byte aligned");
+    return FP4_OK;
+}
+fp4::AttnTree attn_of(const CacheAttn& c) {
+    fp4::AttnTree p{};
+    p.q = static_cast<const uint16_t*>(c.q);
+    p.ld_q = c.ld_q;
+    p.cache = *c.cache;
+    p.page_table = c.page_table;
+    p.max_pages = c.max_pages;
+    p.seq_lens = c.seq_lens;
+    p.draft_lens = c.draft_lens;
+    p.tree_mask = c.tree_mask;
+    p.batch = c.batch;
+    p.drafts = c.drafts;
+    p.q_heads = c.q_heads;
+    p.kv_heads = c.kv_heads;
+    p.head_dim = c.head_dim;
+    p.scale = c.scale;
+    p.out = static_cast<uint16_t*>(c.out);
+    p.ld_out = c.ld_out;
+    p.ws = c.workspace;
+    return p;
+}
+
 // reserved: by the slots of a reservation.
 int kv_compact(const fp4_kv_cache* cache, const fp4_kv_pages* pages, const int32_t* accepted, int64_t max_accepted,
                const int32_t* accepted_lens, bool reserved, const int32_t* slots, int64_t max_new, void* stream,
@@ -855,51 +929,149 @@ int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, con
                      const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* tree_mask, int64_t batch,
                      int drafts, int q_heads, int kv_heads, int head_dim, float scale, void* out, int64_t ld_out,
                      void* workspace, size_t workspace_bytes, void* stream) {
-    if (int e = check_heads(q_heads, kv_heads, head_dim)) return e;
-    if (int e = check_cache(cache, true)) return e;
-    const int64_t width = (int64_t)q_heads * head_dim;
-    FP4_REQUIRE(cache->d == (int64_t)kv_heads * head_dim, FP4_ERR_SHAPE, "the cache has d=%lld, kv_heads * head_dim is %lld",
-                (long long)cache->d, (long long)kv_heads * head_dim);
-    FP4_REQUIRE(drafts >= 1 && drafts <= 64, FP4_ERR_INVALID, "drafts=%d outside [1, 64]", drafts);
-    FP4_REQUIRE(batch >= 0 && max_pages >= 0, FP4_ERR_INVALID, "negative size batch=%lld max_pages=%lld", (long long)batch,
-                (long long)max_pages);
-    FP4_REQUIRE(batch < 65536 && max_pages < (int64_t)1 << 31, FP4_ERR_SHAPE, "batch=%lld or max_pages=%lld too large",
-                (long long)batch, (long long)max_pages);
-    if (int e = check_scale(scale)) return e;
+    const CacheAttn c{q, ld_q, cache, page_table, max_pages, seq_lens, draft_lens, tree_mask, batch, drafts,
+                      q_heads, kv_heads, head_dim, scale, out, ld_out, workspace, workspace_bytes};
+    if (int e = check_attn_sizes(c)) return e;
     if (batch == 0) return ok();
+    if (int e = check_attn_arrays(c)) return e;
+    if (int e = check_workspace(workspace, workspace_bytes,
+                                fp4::attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads)))
+        return e;
+    return hip_status(fp4::launch_attn_tree(attn_of(c), static_cast<hipStream_t>(stream)), "fp4_attn_tree_mx launch");
+}
+
+size_t fp4_attn_shared_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads,
+                                       int64_t num_groups) {
+    if (batch <= 0 || batch >= 65536 || drafts < 1 || drafts > 64 || num_groups < 0 || num_groups >= kMaxList ||
+        check_heads(q_heads, kv_heads, head_dim) != FP4_OK || batch * drafts * (q_heads / kv_heads) >= (int64_t)1 << 31)
+        return 0;
+    return fp4::attn_shared_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads, (int)num_groups);
+}
+
+int fp4_attn_shared_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                       const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* tree_mask,
+                       const int32_t* groups, const int32_t* prefix_lens, int64_t num_groups, int64_t batch, int drafts,
+                       int q_heads, int kv_heads, int head_dim, float scale, void* out, int64_t ld_out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    const CacheAttn c{q, ld_q, cache, page_table, max_pages, seq_lens, draft_lens, tree_mask, batch, drafts,
+                      q_heads, kv_heads, head_dim, scale, out, ld_out, workspace, workspace_bytes};
+    if (int e = check_attn_sizes(c)) return e;
+    FP4_REQUIRE(num_groups >= 0, FP4_ERR_INVALID, "negative num_groups=%lld", (long long)num_groups);
+    FP4_REQUIRE(num_groups < kMaxList, FP4_ERR_SHAPE, "num_groups=%lld too large", (long long)num_groups);
+    FP4_REQUIRE(batch * drafts * (q_heads / kv_heads) < (int64_t)1 << 31, FP4_ERR_SHAPE,
+                "batch=%lld, drafts=%d and q_heads / kv_heads=%d give too many rows (2^31)", (long long)batch, drafts,
+                q_heads / kv_heads);
+    if (batch == 0) return ok();
+    if (int e = check_attn_arrays(c)) return e;
+    if (num_groups) {
+        FP4_SCALAR_PTR(groups);
+        FP4_SCALAR_PTR(prefix_lens);
+    }
+    if (int e = check_workspace(workspace, workspace_bytes,
+                                fp4::attn_shared_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads, (int)num_groups)))
+        return e;
+    fp4::AttnTree p = attn_of(c);
+    p.groups = groups;
+    p.prefix_lens = prefix_lens;
+    p.num_groups = (int)num_groups;
+    return hip_status(fp4::launch_attn_shared(p, static_cast<hipStream_t>(stream)), "fp4_attn_shared_mx launch");
+}
+
+size_t fp4_kv_select_workspace_bytes(int64_t batch, int drafts, int lists, int64_t max_pages) {
+    if (batch <= 0 || batch >= 65536 || drafts < 1 || drafts > 64 || lists < 1 || lists > 4096 || max_pages < 0 ||
+        max_pages >= (int64_t)1 << 31)
+        return 0;
+    return fp4::kv_select_workspace_bytes(batch, drafts, lists, max_pages);
+}
+
+int fp4_kv_select_mx(const void* q, int64_t ld_q, const uint8_t* index_codes, const uint8_t* index_scales, int64_t num_pages,
+                     int lists, int dim, const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
+                     const int32_t* draft_lens, int64_t page_size, int64_t batch, int drafts, int n_select, int n_first,
+                     int n_recent, int32_t* block_ids, float* scores, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    FP4_REQUIRE(batch >= 0 && max_pages >= 0 && num_pages >= 0, FP4_ERR_INVALID,
+                "negative size batch=%lld max_pages=%lld num_pages=%lld", (long long)batch, (long long)max_pages,
+                (long long)num_pages);
+    FP4_REQUIRE(n_select >= 0 && n_first >= 0 && n_recent >= 0, FP4_ERR_INVALID,
+                "negative size n_select=%d n_first=%d n_recent=%d", n_select, n_first, n_recent);
+    FP4_REQUIRE(drafts >= 1 && drafts <= 64, FP4_ERR_INVALID, "drafts=%d outside [1, 64]", drafts);
+    FP4_REQUIRE(lists >= 1, FP4_ERR_INVALID, "lists=%d must be positive", lists);
+    FP4_REQUIRE(dim >= 32 && dim <= 512 && dim % 32 == 0, FP4_ERR_SHAPE, "dim=%d is not a multiple of 32 in [32, 512]", dim);
+    if (int e = check_page_size(page_size)) return e;
+    FP4_REQUIRE(batch < 65536 && lists <= 4096 && n_select < kMaxList && page_size < (int64_t)1 << 31 &&
+                    max_pages < (int64_t)1 << 31 && num_pages < (int64_t)1 << 31 && batch * drafts * lists < (int64_t)1 << 23,
+                FP4_ERR_SHAPE,
+                "too large: batch=%lld drafts=%d lists=%d n_select=%d page_size=%lld max_pages=%lld num_pages=%lld",
+                (long long)batch, drafts, lists, n_select, (long long)page_size, (long long)max_pages, (long long)num_pages);
+    if (batch == 0 || n_select == 0) return ok();
+    const int64_t width = (int64_t)lists * dim;
     FP4_PTR(q);
-    FP4_PTR(out);
     if (int e = check_ld(ld_q, width, "ld_q")) return e;
-    if (int e = check_ld(ld_out, width, "ld_out")) return e;
+    if (num_pages) {
+        FP4_PTR(index_codes);
+        FP4_REQUIRE(index_scales != nullptr, FP4_ERR_INVALID, "index_scales is NULL");
+    }
     if (max_pages) { FP4_SCALAR_PTR(page_table); }
     FP4_SCALAR_PTR(seq_lens);
     FP4_REQUIRE((reinterpret_cast<uintptr_t>(draft_lens) & 3u) == 0, FP4_ERR_ALIGN, "draft_lens is not 4-byte aligned");
-    FP4_REQUIRE((reinterpret_cast<uintptr_t>(tree_mask) & 7u) == 0, FP4_ERR_ALIGN, "tree_mask is not 8-byte aligned");
-    FP4_REQUIRE(!rows_overlap(out, ld_out * 2, width * 2, q, ld_q * 2, width * 2, batch * drafts), FP4_ERR_INVALID,
-                "out overlaps q");
-    const size_t need = fp4::attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
-    FP4_REQUIRE(workspace != nullptr && workspace_bytes >= need, FP4_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu",
-                need, workspace ? workspace_bytes : (size_t)0);
-    FP4_REQUIRE(aligned16(workspace), FP4_ERR_ALIGN, "workspace is not 16-byte aligned");
-    fp4::AttnTree p{};
+    FP4_SCALAR_PTR(block_ids);
+    FP4_REQUIRE((reinterpret_cast<uintptr_t>(scores) & 3u) == 0, FP4_ERR_ALIGN, "scores is not 4-byte aligned");
+    const size_t need = fp4::kv_select_workspace_bytes(batch, drafts, lists, max_pages);
+    if (need) {
+        if (int e = check_workspace(workspace, workspace_bytes, need)) return e;
+    }
+    fp4::KvSelect p{};
     p.q = static_cast<const uint16_t*>(q);
     p.ld_q = ld_q;
-    p.cache = *cache;
+    p.codes = index_codes;
+    p.scales = index_scales;
+    p.num_pages = num_pages;
+    p.lists = lists;
+    p.dim = dim;
     p.page_table = page_table;
     p.max_pages = max_pages;
     p.seq_lens = seq_lens;
     p.draft_lens = draft_lens;
-    p.tree_mask = tree_mask;
+    p.page_size = page_size;
     p.batch = batch;
     p.drafts = drafts;
-    p.q_heads = q_heads;
-    p.kv_heads = kv_heads;
-    p.head_dim = head_dim;
-    p.scale = scale;
-    p.out = static_cast<uint16_t*>(out);
-    p.ld_out = ld_out;
+    p.n_select = n_select;
+    p.n_first = n_first;
+    p.n_recent = n_recent;
+    p.ids = block_ids;
+    p.out_scores = scores;
     p.ws = workspace;
-    return hip_status(fp4::launch_attn_tree(p, static_cast<hipStream_t>(stream)), "fp4_attn_tree_mx launch");
+    return hip_status(fp4::launch_kv_select(p, static_cast<hipStream_t>(stream)), "fp4_kv_select_mx launch");
+}
+
+size_t fp4_attn_blocks_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
+    if (batch <= 0 || drafts < 1 || drafts > 64 || check_heads(q_heads, kv_heads, head_dim) != FP4_OK) return 0;
+    return fp4::attn_blocks_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
+}
+
+int fp4_attn_blocks_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
+                       const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* tree_mask,
+                       const int32_t* block_ids, int lists, int n_select, int64_t batch, int drafts, int q_heads,
+                       int kv_heads, int head_dim, float scale, void* out, int64_t ld_out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    const CacheAttn c{q, ld_q, cache, page_table, max_pages, seq_lens, draft_lens, tree_mask, batch, drafts,
+                      q_heads, kv_heads, head_dim, scale, out, ld_out, workspace, workspace_bytes};
+    if (int e = check_attn_sizes(c)) return e;
+    FP4_REQUIRE(lists == 1 || lists == kv_heads, FP4_ERR_INVALID, "lists=%d is neither 1 nor kv_heads=%d", lists, kv_heads);
+    FP4_REQUIRE(n_select >= 0, FP4_ERR_INVALID, "negative n_select=%d", n_select);
+    FP4_REQUIRE(n_select < kMaxList && fp4::attn_blocks_columns(drafts, q_heads, kv_heads, head_dim, lists) <= 65535,
+                FP4_ERR_SHAPE, "n_select=%d, or drafts=%d of kv_heads=%d too large", n_select, drafts, kv_heads);
+    if (batch == 0) return ok();
+    if (int e = check_attn_arrays(c)) return e;
+    if (n_select) { FP4_SCALAR_PTR(block_ids); }
+    if (int e = check_workspace(workspace, workspace_bytes,
+                                fp4::attn_blocks_workspace_bytes(drafts, q_heads, head_dim, kv_heads)))
+        return e;
+    fp4::AttnTree p = attn_of(c);
+    p.block_ids = block_ids;
+    p.n_select = n_select;
+    p.lists = lists;
+    return hip_status(fp4::launch_attn_blocks(p, static_cast<hipStream_t>(stream)), "fp4_attn_blocks_mx launch");
 }
 
 int fp4_attn_prompt(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int64_t seqs, int64_t tokens,

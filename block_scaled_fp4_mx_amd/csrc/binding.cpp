@@ -440,36 +440,134 @@ PyObject* kv_copy_pages(PyObject* const* v) {
     });
 }
 
+// What the attention calls over the cache have in common.
+struct CacheAttn {
+    const Tensor *q, *out, *table, *lens, *ws, *draft_lens, *mask;
+    Cache cache;
+    int64_t ld_q, ld_out, batch, drafts, heads, d;
+};
+CacheAttn cache_attn(Call& call, PyObject* q, PyObject* cache, PyObject* table, PyObject* lens, PyObject* out, PyObject* ws,
+                     PyObject* draft_lens, PyObject* mask) {
+    CacheAttn x;
+    x.q = &call("q", q, kBF16, false);
+    x.out = &call("out", out, kBF16, false);
+    x.cache = cache_of(call, cache, kCacheNames);
+    x.table = &call("page_table", table, kI32);
+    x.lens = &call("seq_lens", lens, kI32);
+    x.ws = &call("workspace", ws, kU8);
+    x.draft_lens = call.optional("draft_lens", draft_lens, kI32);
+    x.mask = call.optional("tree_mask", mask, kI64);
+    return x;
+}
+void check_shapes(const Call& call, CacheAttn& x) {
+    const char* fn = call.name();
+    x.ld_q = drafted(call, "q", *x.q), x.ld_out = drafted(call, "out", *x.out);
+    x.batch = x.q->size(0), x.drafts = x.q->size(1), x.heads = x.q->size(2), x.d = x.q->size(3);
+    has_shape(call, "out", x.out, x.q->sizes());
+    check_shapes(call, x.cache);
+    if (!x.cache.vc) fail(PyExc_ValueError, "%s: the cache has no values", fn);
+    if (!x.d || !x.cache.c.d || x.cache.c.d % x.d)
+        fail(PyExc_ValueError, "%s: the cache's rows hold %lld values, not a multiple of head_dim %lld", fn,
+             (long long)x.cache.c.d, (long long)x.d);
+    if (x.table->dim() != 2 || x.table->size(0) != x.batch)
+        fail(PyExc_ValueError, "%s: page_table has shape %s, expected [%lld, max_pages]", fn, text(x.table->sizes()).c_str(),
+             (long long)x.batch);
+    has_shape(call, "seq_lens", x.lens, {x.batch});
+    has_shape(call, "draft_lens", x.draft_lens, {x.batch});
+    has_shape(call, "tree_mask", x.mask, {x.batch, x.drafts});
+}
+
 PyObject* attn_tree_mx(PyObject* const* v) {
     Call call("fp4_attn_tree_mx");
+    CacheAttn x = cache_attn(call, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+    check_shapes(call, x);
+    const float scale = scale_of(v[8], x.d);
+    return call.go(v[9], [&](void* s) {
+        return fp4_attn_tree_mx(pointer(x.q), x.ld_q, &x.cache.c, pointer<int32_t>(x.table), x.table->size(1),
+                                pointer<int32_t>(x.lens), pointer<int32_t>(x.draft_lens), pointer<uint64_t>(x.mask), x.batch,
+                                (int)x.drafts, (int)x.heads, (int)(x.cache.c.d / x.d), (int)x.d, scale, pointer(x.out), x.ld_out,
+                                pointer(x.ws), (size_t)x.ws->numel(), s);
+    });
+}
+
+PyObject* attn_shared_mx(PyObject* const* v) {
+    Call call("fp4_attn_shared_mx");
+    CacheAttn x = cache_attn(call, v[0], v[1], v[2], v[3], v[6], v[7], v[8], v[9]);
+    const Tensor& groups = call("groups", v[4], kI32);
+    const Tensor& prefix = call("prefix_lens", v[5], kI32);
+    check_shapes(call, x);
+    if (prefix.dim() != 1)
+        fail(PyExc_ValueError, "%s: prefix_lens has shape %s, expected [num_groups]", call.name(), text(prefix.sizes()).c_str());
+    has_shape(call, "groups", &groups, {prefix.size(0) + 1});
+    const float scale = scale_of(v[10], x.d);
+    return call.go(v[11], [&](void* s) {
+        return fp4_attn_shared_mx(pointer(x.q), x.ld_q, &x.cache.c, pointer<int32_t>(x.table), x.table->size(1),
+                                  pointer<int32_t>(x.lens), pointer<int32_t>(x.draft_lens), pointer<uint64_t>(x.mask),
+                                  pointer<int32_t>(groups), pointer<int32_t>(prefix), prefix.size(0), x.batch, (int)x.drafts,
+                                  (int)x.heads, (int)(x.cache.c.d / x.d), (int)x.d, scale, pointer(x.out), x.ld_out,
+                                  pointer(x.ws), (size_t)x.ws->numel(), s);
+    });
+}
+
+PyObject* kv_select_mx(PyObject* const* v) {
+    Call call("fp4_kv_select_mx");
     const char* fn = call.name();
     const Tensor& q = call("q", v[0], kBF16, false);
-    const Tensor& out = call("out", v[4], kBF16, false);
-    Cache cache = cache_of(call, v[1], kCacheNames);
-    const Tensor& table = call("page_table", v[2], kI32);
-    const Tensor& lens = call("seq_lens", v[3], kI32);
-    const Tensor& ws = call("workspace", v[5], kU8);
-    const Tensor* draft_lens = call.optional("draft_lens", v[6], kI32);
-    const Tensor* mask = call.optional("tree_mask", v[7], kI64);
-    const int64_t ld_q = drafted(call, "q", q), ld_out = drafted(call, "out", out);
-    const int64_t batch = q.size(0), drafts = q.size(1), heads = q.size(2), d = q.size(3);
-    has_shape(call, "out", &out, q.sizes());
-    check_shapes(call, cache);
-    if (!cache.vc) fail(PyExc_ValueError, "%s: the cache has no values", fn);
-    if (!d || !cache.c.d || cache.c.d % d)
-        fail(PyExc_ValueError, "%s: the cache's rows hold %lld values, not a multiple of head_dim %lld", fn, (long long)cache.c.d,
-             (long long)d);
+    const Tensor& codes = call("index_codes", v[1], kU8);
+    const Tensor& scales = call("index_scales", v[2], kU8);
+    const Tensor& table = call("page_table", v[3], kI32);
+    const Tensor& lens = call("seq_lens", v[4], kI32);
+    const int64_t page_size = integer(v[5]);
+    const Tensor& ids = call("block_ids", v[6], kI32);
+    const Tensor& ws = call("workspace", v[7], kU8);
+    const Tensor* draft_lens = call.optional("draft_lens", v[8], kI32);
+    const Tensor* scores = call.optional("scores", v[9], kF32);
+    const int64_t first = integer(v[10]), recent = integer(v[11]);
+    const int64_t ld_q = drafted(call, "q", q);
+    const int64_t batch = q.size(0), drafts = q.size(1), lists = q.size(2), dim = q.size(3);
+    if (codes.dim() != 2 || scales.dim() != 2 || codes.size(1) * 2 != lists * dim || scales.size(1) * 32 != lists * dim ||
+        codes.size(0) != scales.size(0))
+        fail(PyExc_ValueError, "%s: index_codes and index_scales have shapes %s and %s, expected [num_pages, %lld] and [num_pages, %lld]",
+             fn, text(codes.sizes()).c_str(), text(scales.sizes()).c_str(), (long long)(lists * dim / 2),
+             (long long)(lists * dim / 32));
     if (table.dim() != 2 || table.size(0) != batch)
         fail(PyExc_ValueError, "%s: page_table has shape %s, expected [%lld, max_pages]", fn, text(table.sizes()).c_str(),
              (long long)batch);
     has_shape(call, "seq_lens", &lens, {batch});
     has_shape(call, "draft_lens", draft_lens, {batch});
-    has_shape(call, "tree_mask", mask, {batch, drafts});
-    const float scale = scale_of(v[8], d);
-    return call.go(v[9], [&](void* s) {
-        return fp4_attn_tree_mx(pointer(q), ld_q, &cache.c, pointer<int32_t>(table), table.size(1), pointer<int32_t>(lens),
-                                pointer<int32_t>(draft_lens), pointer<uint64_t>(mask), batch, (int)drafts, (int)heads,
-                                (int)(cache.c.d / d), (int)d, scale, pointer(out), ld_out, pointer(ws), (size_t)ws.numel(), s);
+    if (ids.dim() != 4 || ids.size(0) != batch || ids.size(1) != drafts || ids.size(2) != lists)
+        fail(PyExc_ValueError, "%s: block_ids has shape %s, expected [%lld, %lld, %lld, n_select]", fn, text(ids.sizes()).c_str(),
+             (long long)batch, (long long)drafts, (long long)lists);
+    has_shape(call, "scores", scores, ids.sizes());
+    constexpr int64_t kMost = 0x7FFFFFFF;
+    if (first > kMost || recent > kMost || lists > kMost || drafts > kMost || ids.size(3) > kMost)
+        fail(PyExc_ValueError, "%s: a size is too large", fn);
+    return call.go(v[12], [&](void* s) {
+        return fp4_kv_select_mx(pointer(q), ld_q, pointer<uint8_t>(codes), pointer<uint8_t>(scales), codes.size(0), (int)lists,
+                                (int)dim, pointer<int32_t>(table), table.size(1), pointer<int32_t>(lens),
+                                pointer<int32_t>(draft_lens), page_size, batch, (int)drafts, (int)ids.size(3),
+                                (int)(first < 0 ? -1 : first), (int)(recent < 0 ? -1 : recent), pointer<int32_t>(ids),
+                                pointer<float>(scores), pointer(ws), (size_t)ws.numel(), s);
+    });
+}
+
+PyObject* attn_blocks_mx(PyObject* const* v) {
+    Call call("fp4_attn_blocks_mx");
+    CacheAttn x = cache_attn(call, v[0], v[1], v[2], v[3], v[5], v[6], v[7], v[8]);
+    const Tensor& ids = call("block_ids", v[4], kI32);
+    check_shapes(call, x);
+    const int64_t kv_heads = x.cache.c.d / x.d;
+    if (ids.dim() != 4 || ids.size(0) != x.batch || ids.size(1) != x.drafts || (ids.size(2) != 1 && ids.size(2) != kv_heads))
+        fail(PyExc_ValueError, "%s: block_ids has shape %s, expected [%lld, %lld, 1 or %lld, n_select]", call.name(),
+             text(ids.sizes()).c_str(), (long long)x.batch, (long long)x.drafts, (long long)kv_heads);
+    if (ids.size(3) > 0x7FFFFFFF) fail(PyExc_ValueError, "%s: a size is too large", call.name());
+    const float scale = scale_of(v[9], x.d);
+    return call.go(v[10], [&](void* s) {
+        return fp4_attn_blocks_mx(pointer(x.q), x.ld_q, &x.cache.c, pointer<int32_t>(x.table), x.table->size(1),
+                                  pointer<int32_t>(x.lens), pointer<int32_t>(x.draft_lens), pointer<uint64_t>(x.mask),
+                                  pointer<int32_t>(ids), (int)ids.size(2), (int)ids.size(3), x.batch, (int)x.drafts, (int)x.heads,
+                                  (int)kv_heads, (int)x.d, scale, pointer(x.out), x.ld_out, pointer(x.ws), (size_t)x.ws->numel(),
+                                  s);
     });
 }
 
@@ -531,6 +629,9 @@ PyMethodDef methods[] = {
     method<kv_compact<true>, 6>("fp4_kv_compact_reserved"),
     method<kv_copy_pages, 5>("fp4_kv_copy_pages"),
     method<attn_tree_mx, 10>("fp4_attn_tree_mx"),
+    method<attn_shared_mx, 12>("fp4_attn_shared_mx"),
+    method<kv_select_mx, 13>("fp4_kv_select_mx"),
+    method<attn_blocks_mx, 11>("fp4_attn_blocks_mx"),
     method<attn_prompt, 7>("fp4_attn_prompt"),
     {nullptr, nullptr, 0, nullptr},
 };

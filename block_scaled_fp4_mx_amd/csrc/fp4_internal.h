@@ -200,9 +200,38 @@ struct AttnTree {
     uint16_t* out;
     int64_t ld_out;
     void* ws;
+    // launch_attn_blocks
+    const int32_t* block_ids;
+    int n_select, lists;
+    // launch_attn_shared
+    const int32_t *groups, *prefix_lens;
+    int num_groups;
 };
 size_t attn_tree_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads);
 hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s);
+int64_t attn_blocks_columns(int drafts, int q_heads, int kv_heads, int head_dim, int lists);   // of workgroups
+size_t attn_blocks_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads);
+hipError_t launch_attn_blocks(const AttnTree& p, hipStream_t s);
+size_t attn_shared_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads, int groups);
+hipError_t launch_attn_shared(const AttnTree& p, hipStream_t s);
+
+struct KvSelect {
+    const uint16_t* q;
+    int64_t ld_q;
+    const uint8_t *codes, *scales;
+    int64_t num_pages;
+    int lists, dim;
+    const int32_t* page_table;
+    int64_t max_pages;
+    const int32_t *seq_lens, *draft_lens;
+    int64_t page_size, batch;
+    int drafts, n_select, n_first, n_recent;
+    int32_t* ids;
+    float* out_scores;
+    void* ws;
+};
+size_t kv_select_workspace_bytes(int64_t batch, int drafts, int lists, int64_t max_pages);
+hipError_t launch_kv_select(const KvSelect& p, hipStream_t s);
 
 struct AttnPrompt {
     const uint16_t *q, *k, *v;

@@ -619,6 +619,85 @@ int fp4_attn_tree_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, con
 size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
 
 /*
+ * fp4_attn_tree_mx for a batch whose sequences share prefixes (forks of a prompt): group
+ * g is the neighbouring sequences [groups[g], groups[g + 1]) (int32 [num_groups + 1],
+ * ascending; values are taken as within [0, batch]), and their first prefix_lens[g]
+ * (int32 [num_groups]) tokens are the same: the cache rows that the table of the group's
+ * first sequence names for them are read, once for the whole group.  Sequences outside
+ * every group, and those shorter than their group's prefix, are attended by their own
+ * table alone.  The result is fp4_attn_tree_mx's up to the order of the fp32 sums; the
+ * order depends on the shapes, lengths and groups alone.
+ * Everything else is as there.  num_groups 0: nothing is shared.
+ * workspace: fp4_attn_shared_workspace_bytes(...) bytes; calls (and replays) that share
+ * one are ordered by the caller.
+ * Errors: as there; num_groups negative -> FP4_ERR_INVALID; num_groups of 2^20 or more, or
+ * batch * drafts * q_heads / kv_heads of 2^31 or more -> FP4_ERR_SHAPE.
+ */
+int fp4_attn_shared_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                       const uint64_t* tree_mask, const int32_t* groups, const int32_t* prefix_lens,
+                       int64_t num_groups, int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim,
+                       float scale, void* out, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+size_t fp4_attn_shared_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads,
+                                       int64_t num_groups);
+
+/*
+ * Selects cache blocks by a cheap score ("DeepSeek-V4" article, section 3: the
+ * lightning indexer scores a query latent against every compressed cache entry at
+ * FP4).  A block is a page; the index holds an MXFP4 entry of dim values for every page
+ * of the pool and each of `lists` lists: index_codes [num_pages, lists * dim/2],
+ * index_scales [num_pages, lists * dim/32], list after list in a row
+ * (fp4_kv_append_mx with the page ids as slots fills them).
+ * q: bf16 [batch * drafts, ld_q], lists * dim values a token, quantized on the way as
+ * fp4_quantize_mx does.  For query token (b, i) and list l, over the complete blocks n
+ * of the sequence (n < seq_lens[b] / page_size, within the table's row, whose page id is
+ * in [0, num_pages)):
+ *   score(n) = sum over dim of q_hat[b, i, l] * entry_hat[page_table[b, n], l],
+ * in fp32, exact where the products' block scales of a row lie within 2^7 of one
+ * another (and dim <= 128; 2^5 at 512).  A score that is no number counts as -inf.
+ * block_ids: int32 [batch, drafts, lists, n_select], the n_select blocks of largest
+ * score in ascending order, of equal ones the lowest, then -1 where there are fewer.
+ * The first n_first and the last n_recent complete blocks are taken before any other,
+ * the lowest first where they are more than n_select.
+ * scores: fp32 of the same shape or NULL: the scores of the blocks in block_ids, -inf
+ * behind them.  Rows of i >= draft_lens[b] (int32 [batch], NULL = drafts for all) are
+ * left as they were.
+ * workspace: fp4_kv_select_workspace_bytes(...) bytes; calls (and replays) that share
+ * one are ordered by the caller.
+ * Errors: dim not a multiple of 32 in [32, 512], page_size not a multiple of 16, batch of
+ * 65536 or more, lists above 4096, n_select of 2^20 or more, batch * drafts * lists of
+ * 2^23 or more -> FP4_ERR_SHAPE; drafts outside [1, 64], lists < 1, a negative size -> FP4_ERR_INVALID.
+ */
+int fp4_kv_select_mx(const void* q, int64_t ld_q, const uint8_t* index_codes, const uint8_t* index_scales,
+                     int64_t num_pages, int lists, int dim, const int32_t* page_table, int64_t max_pages,
+                     const int32_t* seq_lens, const int32_t* draft_lens, int64_t page_size, int64_t batch, int drafts,
+                     int n_select, int n_first, int n_recent, int32_t* block_ids, float* scores, void* workspace,
+                     size_t workspace_bytes, void* stream);
+size_t fp4_kv_select_workspace_bytes(int64_t batch, int drafts, int lists, int64_t max_pages);
+
+/*
+ * fp4_attn_tree_mx over selected blocks: query token (b, i) sees, of the committed tokens
+ * of its sequence, the blocks (pages) that its list names and those behind the last
+ * complete block, and drafted tokens as there.  block_ids: int32 [batch, drafts, lists,
+ * n_select], lists 1 (all heads) or kv_heads (a list for each key/value head), as
+ * fp4_kv_select_mx writes them; of a list the first min(n_select, seq_lens[b] / page_size)
+ * entries are read, in any order; one outside [0, seq_lens[b] / page_size) names nothing,
+ * and a block that is named twice counts twice.
+ * Everything else is as there.  n_select 0: only what is behind the last complete block.
+ * workspace: fp4_attn_blocks_workspace_bytes(...) bytes; calls (and replays) that share
+ * one are ordered by the caller.
+ * Errors: as there; lists neither 1 nor kv_heads, n_select negative -> FP4_ERR_INVALID;
+ * n_select of 2^20 or more, more than 65535 columns of workgroups (drafts * kv_heads for
+ * up to 64 query heads each) -> FP4_ERR_SHAPE.
+ */
+int fp4_attn_blocks_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                       const uint64_t* tree_mask, const int32_t* block_ids, int lists, int n_select, int64_t batch,
+                       int drafts, int q_heads, int kv_heads, int head_dim, float scale, void* out, int64_t ld_out,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t fp4_attn_blocks_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
+
+/*
  * Causal attention over whole prompts, packed one after another:
  *   out_i = sum_{j <= i, j in i's sequence} softmax_j(scale * q_i . k_j) v_j,
  * softmax statistics and sums in fp32, weights rounded to bf16.

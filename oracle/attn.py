@@ -125,6 +125,58 @@ def attn_tree_mx(qbits, kc, ks, vc, vs, page_size, table, seq_lens, kv_heads, sc
     return out, size
 
 
+def block_scores(qbits, codes, scales, table, seq_lens, page_size):
+    """qbits uint16 [batch, drafts, lists, dim]; codes, scales: an MXFP4 entry of
+    lists * dim values for every page.  float64 [batch, drafts, lists, columns of the
+    table], NaN where a column is no complete block of the sequence in the pool."""
+    batch, drafts, lists, dim = qbits.shape
+    q = Q.mx_dequant_f64(*Q.mx_quantize(qbits.reshape(-1, dim))).reshape(qbits.shape)
+    out = np.full((batch, drafts, lists, table.shape[1]), np.nan)
+    for b in range(batch):
+        for n in range(min(max(int(seq_lens[b]), 0) // page_size, table.shape[1])):
+            page = int(table[b, n])
+            if 0 <= page < len(codes):
+                e = Q.mx_dequant_f64(codes[page:page + 1], scales[page:page + 1]).reshape(lists, dim)
+                out[b, :, :, n] = (q[b] * e).sum(-1)
+    return out
+
+
+def select_blocks(scores, complete, n_select, n_first=0, n_recent=0):
+    """One query's scores [columns] (NaN: no block) of `complete` blocks: the chosen blocks in
+    ascending order.  Blocks among the first n_first and the last n_recent come before
+    others, then larger scores, then lower blocks."""
+    blocks = [n for n in range(complete) if not np.isnan(scores[n])]
+    forced = lambda n: n < n_first or n >= complete - n_recent
+    return sorted(sorted(blocks, key=lambda n: (not forced(n), 0.0 if forced(n) else -scores[n], n))[:n_select])
+
+
+def attn_blocks_mx(qbits, kc, ks, vc, vs, page_size, table, seq_lens, kv_heads, scale, block_ids, draft_lens=None, tree_mask=None):
+    """attn_tree_mx over the listed blocks [batch, drafts, 1 or kv_heads, n], the tokens
+    behind the last complete block and the drafted ones."""
+    q = F.bf16_bits_to_f64(qbits)
+    batch, drafts, q_heads, d = q.shape
+    group = q_heads // kv_heads
+    out, size = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
+    for b in range(batch):
+        t = drafts if draft_lens is None else min(max(int(draft_lens[b]), 0), drafts)
+        n = max(int(seq_lens[b]), 0)
+        full = n // page_size
+        rows = cache_rows(table[b], page_size, len(kc) // page_size, n + t)
+        for i in range(t):
+            for h in range(kv_heads):
+                ids = block_ids[b, i, h if block_ids.shape[2] > 1 else 0][:full]
+                at = [m * page_size + j for m in ids if 0 <= m < full for j in range(page_size)]
+                at += range(full * page_size, n)
+                at += [n + j for j in range(t) if (j <= i if tree_mask is None else (int(tree_mask[b, i]) >> j) & 1)]
+                at = rows[np.array(at, np.int64)]
+                at = at[at >= 0]
+                k = Q.mx_dequant_f64(kc[at], ks[at]).reshape(-1, kv_heads, d)[:, h]
+                v = Q.mx_dequant_f64(vc[at], vs[at]).reshape(-1, kv_heads, d)[:, h]
+                heads = slice(h * group, (h + 1) * group)
+                out[b, i, heads], size[b, i, heads] = attend(q[b, i, heads], k, v, np.ones((group, len(at)), bool), scale)
+    return out, size
+
+
 # -------------------------------------------------------------------------- pages
 
 class Pages:
