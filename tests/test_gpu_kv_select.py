@@ -83,7 +83,12 @@ def test_many_drafts(drafts):
     Index(drafts, [700, 90], drafts, 2, 128, 16).check(5, draft_lens=[drafts, drafts // 2])
 
 
-@pytest.mark.parametrize("blocks", [511, 512, 513, 4000, 8191])
+@pytest.mark.parametrize("dim", [64, 160])
+def test_more_queries_than_compute_units(dim):
+    Index(dim, [16 * 90, 16 * 200 + 1, 30, 0, 16 * 130], 30, 2, dim, 16).check(20, draft_lens=[30, 17, 30, 1, 0])
+
+
+@pytest.mark.parametrize("blocks", [511, 512, 513, 1024, 1025, 2048, 2049, 4000, 8191])
 def test_many_blocks_in_registers(blocks):
     Index(blocks, [16 * blocks + 5, 100], 2, 1, 64, 16).check(50)
 
@@ -111,6 +116,15 @@ def test_ties_go_to_the_lowest_block():
     x.q[:] = 0x8000                                         # scores of -0 and 0 are equal
     x.codes[x.table[0, ::2]] ^= 0x88
     x.check(7)
+
+
+def test_many_scores_on_both_sides_of_the_threshold():
+    """A few far scores, so that all others lie in one part between the least and the largest."""
+    x = Index(15, [16 * 1800], 3, 1, 64, 16)
+    x.scales[x.table[0, [40, 900]]] += 14
+    x.scales[x.table[0, 1000:1040]] -= 14
+    for n in (1, 2, 3, 60, 1000):
+        x.check(n)
 
 
 def test_scores_without_a_number_come_last():
