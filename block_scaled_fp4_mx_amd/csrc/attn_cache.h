@@ -65,7 +65,7 @@ struct TreeArgs {
     // are not cut stand behind those of the ranges (slot 2 << shift on): in kOwn by
     // sequence, in kPrefix by row tiles (tile_base).
     const int32_t *groups, *prefix_lens;
-    int num_groups;
+    int num_groups, prefix_tile;           // prefix_tile: tokens of a step of the prefix's walk
 };
 
 __device__ __forceinline__ int drafts_of(const TreeArgs& a, int b) {
@@ -153,7 +153,7 @@ __device__ __forceinline__ Chunk<kMode> chunk_at(const TreeArgs& a, int first, i
         const int members = max(bound_of(a, g + 1) - c.token, 0);
         c.token *= a.drafts, c.tokens = members * a.drafts;
         c.len = c.seen = prefix_of(a, g), c.drafts = 0;
-        c.per = c.seen / kTile;
+        c.per = (c.seen + a.prefix_tile - 1) / a.prefix_tile;
         c.tiles = there ? (uint64_t)(((int64_t)members * a.rows + span - 1) / span) * (uint32_t)c.per : 0;
     } else {
         const int b = min(first + lane, a.batch - 1);
@@ -922,8 +922,9 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_join_kernel(const Tre
             const int k = group - all.first;
             start += (int64_t)(all.read(all.upto, k) - all.read(all.tiles, k));
             const int64_t row = (int64_t)(b - bound_of(pre, group)) * pre.rows + r0 + c, span = row / pre_span;
-            start += span * skip;                             // its span's first tile
-            const int x0 = (int)((((start + 1) << pre_shift) - 1) / cells), x1 = (int)((((start + skip) << pre_shift) - 1) / cells);
+            const int per = __builtin_amdgcn_readlane(all.per, k);
+            start += span * per;                              // its span's first tile
+            const int x0 = (int)((((start + 1) << pre_shift) - 1) / cells), x1 = (int)((((start + per) << pre_shift) - 1) / cells);
             const int slot0 = 2 * x0 + ((x0 * cells >> pre_shift) == start ? 0 : 1);
             int most = x1 - x0;
 #pragma unroll

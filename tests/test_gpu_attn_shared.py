@@ -91,6 +91,16 @@ def test_long_prefixes_split_over_workgroups(d, q_heads, kv_heads, drafts):
     Shared(d, [(5, 6000)], [6000, 6100, 6001, 7200, 6031], drafts, q_heads, kv_heads, d, 64).run()
 
 
+@pytest.mark.parametrize("d,q_heads,kv_heads,members", [(64, 6, 1, 40), (64, 4, 2, 40), (128, 4, 1, 70), (128, 4, 2, 40), (256, 3, 1, 40)])
+def test_many_rows_over_long_prefixes(d, q_heads, kv_heads, members):
+    """More rows than a workgroup has, and tiles and runs of pages that end anywhere."""
+    rng = np.random.default_rng(d)
+    x = Shared(d, [(members, 1500), (members, 97)], (1500 + rng.integers(0, 40, 2 * members)).tolist(), 1, q_heads, kv_heads, d, 48)
+    x.run()
+    x.table[:, 3], x.table[:, 17] = -1, 1 << 28             # not seen by any
+    x.run(scale=-0.2)
+
+
 def test_long_own_parts_and_whole_prefixes_in_one_range():
     """Ranges with several whole prefixes, and sequences that ranges cut."""
     lens = [64, 3000, 64, 40, 33, 2049, 70, 96, 100, 1000]
