@@ -39,7 +39,7 @@ hipError_t launch_attn_blocks(const AttnTree& p, hipStream_t s) {
     return with_head_dim(p.head_dim, [&](auto d) {
         constexpr int D = decltype(d)::value;
         const hipError_t e = launch_walk<kBlocks, D>(a, l, (unsigned)l.columns, s);
-        return e != hipSuccess ? e : launch_join<kBlocks, D>(a, {}, p.drafts, s);
+        return e != hipSuccess ? e : launch_join<kBlocks, D>(a, p.drafts, s);
     });
 }
 

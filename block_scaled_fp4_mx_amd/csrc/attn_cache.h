@@ -66,6 +66,11 @@ struct TreeArgs {
     // sequence, in kPrefix by row tiles (tile_base).
     const int32_t *groups, *prefix_lens;
     int num_groups, prefix_tile;           // prefix_tile: tokens of a step of the prefix's walk
+    // Where the pieces of a sequence's own tokens, or of a span of a group's rows, stand,
+    // for the join: {first slot, last range, group or -1, its first sequence} by sequence, {first
+    // slot, last range} by span_index.  The workgroups that begin and end them write it.
+    int4* own_pieces;
+    int2* span_pieces;
 };
 
 __device__ __forceinline__ int drafts_of(const TreeArgs& a, int b) {
@@ -90,6 +95,25 @@ __device__ __forceinline__ int64_t scalar(int64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
     const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
     return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// A value of the lanes that the DPP control word names, 0 where they have none.
+template <int kControl, int kRows>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kControl, kRows, 0xF, false);
+}
+template <int kControl, int kRows>
+__device__ __forceinline__ uint64_t moved(uint64_t v) {
+    return (uint64_t)moved<kControl, kRows>((uint32_t)(v >> 32)) << 32 | moved<kControl, kRows>((uint32_t)v);
+}
+// Sum of the values of a lane and those before it (a tenth of the time of exchanges
+// through LDS): within rows of 16 lanes, then the last lane of rows 0 and 2 into rows 1
+// and 3, then that of row 1 into rows 2 and 3.
+template <class T>
+__device__ __forceinline__ T sum_upto(T v) {
+    v += moved<0x111, 0xF>(v), v += moved<0x112, 0xF>(v), v += moved<0x114, 0xF>(v), v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);
+    return v + moved<0x143, 0xC>(v);
 }
 
 // Tokens of a group's prefix that are attended once for all: whole tiles, as far as the
@@ -131,7 +155,7 @@ struct Chunk {
     using Count = std::conditional_t<kMode == kPrefix, uint64_t, uint32_t>;
     int first, len, seen, drafts;
     int skip;                          // kBlocks: pages left out before the last incomplete one; kOwn: first tile
-    int token, tokens;                 // kPrefix: of the rows
+    int token, tokens;                 // kPrefix: of the rows; kOwn: the group and its first sequence
     int per;                           // kPrefix: tiles of a span
     Count tiles, upto;
     __device__ __forceinline__ static Count read(Count v, int k) {
@@ -172,16 +196,12 @@ __device__ __forceinline__ Chunk<kMode> chunk_at(const TreeArgs& a, int first, i
             if constexpr (kMode == kOwn) {
                 const int g = group_of(a, b, lane), p = g < 0 ? 0 : prefix_of(a, g);
                 c.skip = c.len >= p ? p / kTile : 0;
+                c.token = c.skip ? g : -1, c.tokens = c.skip ? bound_of(a, g) : 0;
                 if (c.tiles) c.tiles = max((int)c.tiles - c.skip, 1);
             }
         }
     }
-    c.upto = c.tiles;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        const typename Chunk<kMode>::Count o = __shfl_up(c.upto, m, 64);
-        if (lane >= m) c.upto += o;
-    }
+    c.upto = sum_upto(c.tiles);
     return c;
 }
 
@@ -451,27 +471,50 @@ __device__ __forceinline__ PartPlace prefix_place(const TreeArgs& a, bool whole,
     return {at * a.kv_heads + head, (ranges + tile_base_end(a)) * a.kv_heads};
 }
 
+// Place of a span of a group's rows in span_pieces (row: any of it).
+__device__ __forceinline__ int64_t span_index(const TreeArgs& a, int group, int first_sequence, int64_t row, int span) {
+    return (int64_t)first_sequence * a.rows / span + group + row / span;
+}
+// item: a sequence or a group; token, tokens: as its chunk has them; row: of the span.
+template <Mode kMode>
+__device__ __forceinline__ void note_piece(const TreeArgs& a, int slot, bool begins, bool ends, int item, int token, int tokens,
+                                           int64_t row, int span) {
+    if constexpr (kMode == kOwn) {
+        int4* to = a.own_pieces + item;
+        if (begins) to->x = slot, to->z = token, to->w = tokens;
+        if (ends) to->y = slot >> 1;
+    } else {
+        int2* to = a.span_pieces + span_index(a, item, token / a.drafts, row, span);
+        if (begins) to->x = slot;
+        if (ends) to->y = slot >> 1;
+    }
+}
+
+// LDS of a workgroup's walk.
+template <int D, int HW>
+constexpr int kStaging = HW * kStages * Stage<D, HW>::kBytes;
+
+// The walk of workgroup (block_x, block_y).
 template <Mode kMode, int D, int NR, int HW, int RG>
-__global__ __launch_bounds__(64 * HW * RG, D == 256 ? 1 : 2) void attn_walk_kernel(const TreeArgs a) {
+__device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int block_x, int block_y) {
     constexpr int kSteps = D / 32, kOut = D / 16;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     using S = Stage<D, HW>;
     constexpr int kRegion = kStages * S::kBytes;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), groups = a.kv_heads / HW;
     const int hw = wave % HW, rg = RG == 1 ? 0 : wave / HW;
-    const int head0 = __builtin_amdgcn_readfirstlane(blockIdx.y % groups) * HW, head = head0 + hw;
+    const int head0 = __builtin_amdgcn_readfirstlane(block_y % groups) * HW, head = head0 + hw;
     constexpr int kSpan = 16 * NR * RG;                       // rows of a workgroup
-    const int column = __builtin_amdgcn_readfirstlane(blockIdx.y / groups), spans = (a.rows + kSpan - 1) / kSpan;
+    const int column = __builtin_amdgcn_readfirstlane(block_y / groups), spans = (a.rows + kSpan - 1) / kSpan;
     const int plane = kMode == kBlocks ? column / spans : 0;
     int r0 = ((kMode == kBlocks ? column - plane * spans : column) * RG + rg) * 16 * NR;
-    __shared__ __attribute__((aligned(16))) uint8_t staging[HW * kRegion];
-    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)(uint8_t*)staging) + hw * kRegion;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)staging) + hw * kRegion;
     const Lane<D, HW> own = lane_of<D, HW>(a, head0, hw, lane);
     Chunk<kMode> chunk = chunk_at<kMode>(a, 0, lane, plane, kSpan);
     const int64_t total = all_tiles<kMode>(a, chunk, lane, plane, kSpan);
     const int shift = shift_of(a, total);
-    const int64_t lo = blockIdx.x * total >> shift, hi = (blockIdx.x + 1) * total >> shift;
-    if (blockIdx.x >> shift || lo == hi) return;
+    const int64_t lo = block_x * total >> shift, hi = (block_x + 1) * total >> shift;
+    if (block_x >> shift || lo == hi) return;
 
     // The sequence that holds tile lo, and the tiles before it.
     int64_t before = 0;
@@ -803,7 +846,7 @@ __global__ __launch_bounds__(64 * HW * RG, D == 256 ? 1 : 2) void attn_walk_kern
                         *reinterpret_cast<uint2*>(y + i * kOut + 2 * j) = make_uint2(w[j], w[j + 1]);
                 }
             } else if (r0 + 16 * n < (kMode == kPrefix ? row_tokens * a.group : a.rows)) {
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (at == lo ? 0 : 1);
+                const int64_t slot = 2 * (int64_t)block_x + (at == lo ? 0 : 1);
                 const PartPlace p = kMode == kPrefix ? prefix_place(a, whole, slot, tile0, r0 + 16 * n, kSpan, head)
                                                      : part_place<kMode>(a, whole, slot, b, plane, (r0 >> 4) + n, head);
                 v4f* y = reinterpret_cast<v4f*>(a.part) + p.tile * (4 * D) + lane;
@@ -813,63 +856,36 @@ __global__ __launch_bounds__(64 * HW * RG, D == 256 ? 1 : 2) void attn_walk_kern
                 if (g == 0) ml[p.tile * 16 + c] = make_float2(m[n], l);
             }
         }
+        if constexpr (kMode == kOwn || kMode == kPrefix) {
+            if (block_y == 0 && threadIdx.x == 0)
+                note_piece<kMode>(a, 2 * block_x + (at == lo ? 0 : 1), t0 == 0, t1 == tiles, b,
+                                  __builtin_amdgcn_readlane(chunk.token, at_lane), __builtin_amdgcn_readlane(chunk.tokens, at_lane), r0,
+                                  kSpan);
+        }
         at += t1 - t0;
         if (at - before == cells) before += cells, ++b;
     }
 }
 
-// Joins the partial results of the sequences that were cut: workgroup (x, y) takes
-// 16 rows of a head (x; kBlocks: of a head's drafted token) of sequence y, and of their
-// values the kPer slices from kPer * z on (slice i: the values i, i + D/16, ...).  A wave
-// reads a slice of a piece as it was written, 16 bytes a lane; kTeams of kPer waves take
-// the pieces in turn, and their sums are joined through LDS in team order.
-// kOwn: and the pieces of the group's prefix (pre: its walk), whose tiles of 16 rows begin
-// elsewhere: each lane finds its row's.
-struct NoPrefix {};
-struct PrefixWalk {
-    TreeArgs args;
-    int span;                          // rows of its workgroups
-};
-template <Mode kMode>
-using PrefixOf = std::conditional_t<kMode == kOwn, PrefixWalk, NoPrefix>;
-template <Mode kMode, int D, int kPer, int kTeams>
-__global__ __launch_bounds__(64 * kPer * kTeams) void attn_join_kernel(const TreeArgs a, const PrefixOf<kMode> walk) {
-    constexpr int kTeam = 64 * kPer, kBatch = 8, kOut = D / 16;
-    __shared__ v4f sums[kTeams > 1 ? kTeam * kTeams : 1];
-    __shared__ float2 stats[kTeams][16];
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const int b = blockIdx.y, row_tile = blockIdx.x % a.row_tiles, r0 = row_tile * 16;
-    const int planes = kMode == kBlocks ? a.drafts : 1, at_plane = blockIdx.x / a.row_tiles;
-    const int head = at_plane / planes, plane = at_plane - head * planes;
-    Chunk<kMode> chunk = chunk_at<kMode>(a, 0, lane, plane, 0);
-    const int64_t total = all_tiles<kMode>(a, chunk, lane, plane, 0);
-    const int shift = shift_of(a, total);
-    int64_t before = 0;
-    while (b - chunk.first >= 64) {
-        before += chunk.all();
-        chunk = chunk_at<kMode>(a, chunk.first + 64, lane, plane, 0);
-    }
-    const uint32_t tiles = chunk.read(chunk.tiles, b - chunk.first);
-    const int nd = __builtin_amdgcn_readlane(chunk.drafts, b - chunk.first);
-    const int skip = kMode == kOwn ? __builtin_amdgcn_readlane(chunk.skip, b - chunk.first) : 0;
-    before += chunk.read(chunk.upto, b - chunk.first) - tiles;
-    const int rows = kMode == kBlocks ? a.group : nd * a.group;
-    if (tiles == 0 || r0 >= rows) return;
-    // The ranges that hold its first and last tile: tile t lies in the last range
-    // whose start, x * total >> shift, is at most t.
-    const int first = (int)scalar((((before + 1) << shift) - 1) / total);
-    const int last = (int)scalar((((before + tiles) << shift) - 1) / total);
-    const bool whole = first == last;
-    if (whole && skip == 0) return;                           // one piece: written already
-    // The first piece is its range's second one unless the range starts with it.
-    const int first_slot = 2 * first + ((first * total >> shift) == before ? 0 : 1);
-    const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = kPer * blockIdx.z + (part >> 6);
+template <Mode kMode, int D, int NR, int HW, int RG>
+__global__ __launch_bounds__(64 * HW * RG, D == 256 ? 1 : 2) void attn_walk_kernel(const TreeArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t staging[kStaging<D, HW>];
+    walk<kMode, D, NR, HW, RG>(a, staging, blockIdx.x, blockIdx.y);
+}
 
+// A wave's part in joining partial results of 16 rows of one head: of their values slice
+// i (the values i, i + D/16, ...), lane (c, g) those of row c in quarter g, 16 bytes as
+// they were written.  kTeams teams take the pieces in turn; team order is the sum's.
+template <int D, int kTeams>
+struct Joined {
     float m = kFloor, l = 0.f;
     v4f acc = {0.f, 0.f, 0.f, 0.f};
-    // Adds the pieces first .. last (most: of all lanes), whose tile and the row in it
-    // place(x) gives.
-    auto add = [&](const float* parts, int64_t stats_at, int first, int last, int most, int row, auto place) {
+    // Adds the pieces first .. last (most: last - first, the largest of the wave's lanes);
+    // place(x): the tile of piece x, row: the lane's in it, stats_at: as PartPlace has it.
+    template <class Place>
+    __device__ __forceinline__ void add(const float* parts, int64_t stats_at, int team, int i, int g, int first, int last, int most,
+                                        int row, Place place) {
+        constexpr int kBatch = 8;
         const v4f* o = reinterpret_cast<const v4f*>(parts) + 64 * i + 16 * g + row;
         const float2* ml = reinterpret_cast<const float2*>(parts + stats_at * (16 * D)) + row;
         for (int x0 = first + team; x0 - first <= most; x0 += kBatch * kTeams) {
@@ -900,70 +916,39 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_join_kernel(const Tre
                 acc += v[k] * e;
             }
         }
-    };
-    const int64_t stats_at = part_place<kMode>(a, whole, 0, b, plane, row_tile, head).stats;
-    add(a.part, stats_at, first, last, last - first, c, [&](int x) {
-        const int64_t slot = x == first ? first_slot : 2 * (int64_t)x;
-        return part_place<kMode>(a, kMode == kOwn && whole, slot, b, plane, row_tile, head).tile;
-    });
-    if constexpr (kMode == kOwn) {
-        if (skip) {
-            const TreeArgs& pre = walk.args;
-            const int pre_span = walk.span;
-            const int group = __builtin_amdgcn_readfirstlane(group_of(pre, b, lane));
-            Chunk<kPrefix> all = chunk_at<kPrefix>(pre, 0, lane, 0, pre_span);
-            const int64_t cells = all_tiles<kPrefix>(pre, all, lane, 0, pre_span);
-            const int pre_shift = shift_of(pre, cells);
-            int64_t start = 0;
-            while (group - all.first >= 64) {
-                start += all.all();
-                all = chunk_at<kPrefix>(pre, all.first + 64, lane, 0, pre_span);
-            }
-            const int k = group - all.first;
-            start += (int64_t)(all.read(all.upto, k) - all.read(all.tiles, k));
-            const int64_t row = (int64_t)(b - bound_of(pre, group)) * pre.rows + r0 + c, span = row / pre_span;
-            const int per = __builtin_amdgcn_readlane(all.per, k);
-            start += span * per;                              // its span's first tile
-            const int x0 = (int)((((start + 1) << pre_shift) - 1) / cells), x1 = (int)((((start + per) << pre_shift) - 1) / cells);
-            const int slot0 = 2 * x0 + ((x0 * cells >> pre_shift) == start ? 0 : 1);
-            int most = x1 - x0;
-#pragma unroll
-            for (int n = 1; n < 16; n *= 2) most = max(most, __shfl_xor(most, n, 64));
-            const int64_t tile0 = tile_base(pre, group);
-            const int64_t row16 = row & ~15ll;
-            add(pre.part, prefix_place(pre, false, 0, 0, 0, pre_span, 0).stats, x0, r0 + c < rows ? x1 : x0 - 1, most,
-                (int)(row & 15), [&](int x) {
-                    return prefix_place(pre, x0 == x1, x == x0 ? slot0 : 2 * (int64_t)x, tile0, row16, pre_span, head).tile;
-                });
-        }
     }
+};
+// The teams' sums through LDS, and the rows r0 .. rows written where out_at(row) says; a
+// team has kPer waves, wave part / 64 of it slice i.
+template <int D, int kPer, int kTeams, class Out>
+__device__ __forceinline__ void finish_join(Joined<D, kTeams>& j, int team, int part, int i, int lane, int r0, int rows, Out out_at) {
+    constexpr int kTeam = 64 * kPer, kOut = D / 16;
+    const int c = lane & 15, g = lane >> 4;
+    __shared__ v4f sums[kTeams > 1 ? kTeam * kTeams : 1];
+    __shared__ float2 stats[kTeams][16];
     if constexpr (kTeams > 1) {
-        sums[threadIdx.x] = acc;
-        if (part < 16) stats[team][part] = make_float2(m, l);
+        sums[threadIdx.x] = j.acc;
+        if (part < 16) stats[team][part] = make_float2(j.m, j.l);
         __syncthreads();
         if (team == 0) {
             float top = kFloor;
 #pragma unroll
             for (int k = 0; k < kTeams; ++k) top = fmaxf(top, stats[k][c].x);
-            l = 0.f;
-            acc = v4f{0.f, 0.f, 0.f, 0.f};
+            j.l = 0.f;
+            j.acc = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kTeams; ++k) {
                 const float e = exp2_hw(stats[k][c].x - top);
-                l += stats[k][c].y * e;
-                acc += sums[part + k * kTeam] * e;
+                j.l += stats[k][c].y * e;
+                j.acc += sums[part + k * kTeam] * e;
             }
         }
     }
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    auto out_at = [&](int row) {
-        const int t = kMode == kBlocks ? plane : row / a.group, h = kMode == kBlocks ? row : row % a.group;
-        return a.out + ((int64_t)b * a.drafts + t) * a.ld_out + ((int64_t)head * a.group + h) * D;
-    };
+    const float inv = j.l > 0.f ? 1.0f / j.l : 0.f;
     if constexpr (kPer == kOut) {                             // whole rows go out through LDS in 16-byte parts
         __shared__ __attribute__((aligned(16))) uint16_t out_rows[16][D + 8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) out_rows[c][g * (D / 4) + k * kOut + i] = (uint16_t)pack2(acc[k] * inv, 0.f);
+        for (int k = 0; k < 4; ++k) out_rows[c][g * (D / 4) + k * kOut + i] = (uint16_t)pack2(j.acc[k] * inv, 0.f);
         __syncthreads();
         const int chunks = D / 8, r = threadIdx.x / chunks, at = threadIdx.x % chunks * 8;
         if (r < 16 && r0 + r < rows)
@@ -971,8 +956,51 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_join_kernel(const Tre
     } else if (team == 0 && r0 + c < rows) {
         uint16_t* y = out_at(r0 + c) + g * (D / 4) + i;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k * kOut] = (uint16_t)pack2(acc[k] * inv, 0.f);
+        for (int k = 0; k < 4; ++k) y[k * kOut] = (uint16_t)pack2(j.acc[k] * inv, 0.f);
     }
+}
+
+// Joins the partial results of the sequences that were cut: workgroup (x, y) takes
+// 16 rows of a head (x; kBlocks: of a head's drafted token) of sequence y, and of their
+// values the kPer slices from kPer * z on.
+template <Mode kMode, int D, int kPer, int kTeams>
+__global__ __launch_bounds__(64 * kPer * kTeams) void attn_join_kernel(const TreeArgs a) {
+    constexpr int kTeam = 64 * kPer;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int b = blockIdx.y, row_tile = blockIdx.x % a.row_tiles, r0 = row_tile * 16;
+    const int planes = kMode == kBlocks ? a.drafts : 1, at_plane = blockIdx.x / a.row_tiles;
+    const int head = at_plane / planes, plane = at_plane - head * planes;
+    Chunk<kMode> chunk = chunk_at<kMode>(a, 0, lane, plane, 0);
+    const int64_t total = all_tiles<kMode>(a, chunk, lane, plane, 0);
+    const int shift = shift_of(a, total);
+    int64_t before = 0;
+    while (b - chunk.first >= 64) {
+        before += chunk.all();
+        chunk = chunk_at<kMode>(a, chunk.first + 64, lane, plane, 0);
+    }
+    const uint32_t tiles = chunk.read(chunk.tiles, b - chunk.first);
+    const int nd = __builtin_amdgcn_readlane(chunk.drafts, b - chunk.first);
+    before += chunk.read(chunk.upto, b - chunk.first) - tiles;
+    const int rows = kMode == kBlocks ? a.group : nd * a.group;
+    if (tiles == 0 || r0 >= rows) return;
+    // The ranges that hold its first and last tile: tile t lies in the last range
+    // whose start, x * total >> shift, is at most t.
+    const int first = (int)scalar((((before + 1) << shift) - 1) / total);
+    const int last = (int)scalar((((before + tiles) << shift) - 1) / total);
+    if (first == last) return;                                // one piece: written already
+    // The first piece is its range's second one unless the range starts with it.
+    const int first_slot = 2 * first + ((first * total >> shift) == before ? 0 : 1);
+    const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = kPer * blockIdx.z + (part >> 6);
+
+    Joined<D, kTeams> joined;
+    joined.add(a.part, part_place<kMode>(a, false, 0, b, plane, row_tile, head).stats, team, i, g, first, last, last - first, c,
+               [&](int x) {
+                   return part_place<kMode>(a, false, x == first ? first_slot : 2 * (int64_t)x, b, plane, row_tile, head).tile;
+               });
+    finish_join<D, kPer>(joined, team, part, i, lane, r0, rows, [&](int row) {
+        const int t = kMode == kBlocks ? plane : row / a.group, h = kMode == kBlocks ? row : row % a.group;
+        return a.out + ((int64_t)b * a.drafts + t) * a.ld_out + ((int64_t)head * a.group + h) * D;
+    });
 }
 
 // How the call is laid out, from its shapes alone.
@@ -1036,15 +1064,15 @@ hipError_t launch_walk(const TreeArgs& a, const Layout& l, unsigned columns, hip
     });
 }
 template <Mode kMode, int D>
-hipError_t launch_join(const TreeArgs& a, const PrefixOf<kMode>& walk, int planes, hipStream_t s) {
+hipError_t launch_join(const TreeArgs& a, int planes, hipStream_t s) {
     const unsigned row_tiles = (unsigned)(a.kv_heads * planes * a.row_tiles);
     // Many pieces of few rows (on average of the sequences, and so that all workgroups
     // are resident): 16 waves to a slice.  One sequence of 100000 tokens: 8 us, against
     // 37 with a wave to a slice; the 4 long contexts with 16 drafts: 16 us against 11.
     if (1 << a.shift >= 16 * a.batch && (int64_t)row_tiles * a.batch * (D / 16) <= 512)
-        attn_join_kernel<kMode, D, 1, 16><<<dim3(row_tiles, (unsigned)a.batch, D / 16), 1024, 0, s>>>(a, walk);
+        attn_join_kernel<kMode, D, 1, 16><<<dim3(row_tiles, (unsigned)a.batch, D / 16), 1024, 0, s>>>(a);
     else
-        attn_join_kernel<kMode, D, D / 16, 1><<<dim3(row_tiles, (unsigned)a.batch), 4 * D, 0, s>>>(a, walk);
+        attn_join_kernel<kMode, D, D / 16, 1><<<dim3(row_tiles, (unsigned)a.batch), 4 * D, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -41,20 +41,19 @@ struct Wide {
     __device__ static constexpr int value_turn(int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); }
 };
 
+// Workgroup (block_x, head) of the prefix's many rows.
 template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void attn_prefix_kernel(const TreeArgs a) {
+__device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_lds, int block_x, int head) {
     using S = Wide<D, W>;
     constexpr int kRows = S::kRows, kTokens = S::kTokens, kSteps = D / 16, kOut = D / 32, kSub = kTokens / 32;
     constexpr int kBatch = kSteps < 8 ? kSteps : 8, kGroups = kTokens / 16;
-    __shared__ __attribute__((aligned(16))) uint8_t tiles_lds[2 * 2 * S::kTile];        // keys, values; twice
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
-    const int head = __builtin_amdgcn_readfirstlane(blockIdx.y);
 
     Chunk<kPrefix> chunk = chunk_at<kPrefix>(a, 0, lane, 0, kRows);
     const int64_t total = all_tiles<kPrefix>(a, chunk, lane, 0, kRows);
     const int shift = shift_of(a, total);
-    const int64_t lo = blockIdx.x * total >> shift, hi = (blockIdx.x + 1) * total >> shift;
-    if (blockIdx.x >> shift || lo == hi) return;
+    const int64_t lo = block_x * total >> shift, hi = (block_x + 1) * total >> shift;
+    if (block_x >> shift || lo == hi) return;
     int64_t before = 0;
     while (before + (int64_t)chunk.all() <= lo) {
         before += chunk.all();
@@ -252,7 +251,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_prefix_kernel(const TreeArgs a
         if (row0 + (c & 16) < rows) {
             // As the walk's lanes hold a tile of 16 rows: value g * D/4 + k * D/16 + i of row c
             // at [i][g][c], component k.
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (at == lo ? 0 : 1);
+            const int64_t slot = 2 * (int64_t)block_x + (at == lo ? 0 : 1);
             const PartPlace p = prefix_place(a, t0 == 0 && t1 == tiles, slot, tile_base(a, group), row0 + (c & 16), kRows, head);
             v4f* y = reinterpret_cast<v4f*>(a.part) + p.tile * (4 * D) + (c & 15);
             if constexpr (D == 128) {
@@ -292,78 +291,161 @@ __global__ __launch_bounds__(64 * W, 2) void attn_prefix_kernel(const TreeArgs a
             float2* ml = reinterpret_cast<float2*>(a.part + p.stats * (16 * D));
             if (h == 0) ml[p.tile * 16 + (c & 15)] = make_float2(m, l);
         }
+        if (head == 0 && threadIdx.x == 0)
+            note_piece<kPrefix>(a, 2 * block_x + (at == lo ? 0 : 1), t0 == 0, t1 == tiles, group, token0, 0, span * kRows, kRows);
         at += t1 - t0;
         if (at - before == cells) before += cells, ++group;
     }
 }
 
-// How the prefix is attended: by the walk, with as many rows to a workgroup as a group
-// has on average, or by attn_prefix_kernel.  Spans of rows are laid end to end, so that
-// columns are heads alone.
-struct PrefixLayout {
-    Layout walk;
-    int waves;                             // of attn_prefix_kernel; 0: the walk
-    int span, shift;
+// Both kinds of work in one launch: the first own_blocks workgroups take the sequences' own
+// tokens, by the walk <NR, HW, RG>, the others the prefixes, by the same walk (W = 0) or
+// attend_prefix.  (64 samples of 16384 tokens: 62 us; the prefixes first 65; half of them
+// first 72, as the others then start late; two launches 68.)
+struct Split {
+    int own_blocks, own_shift, prefix_shift;
 };
-PrefixLayout prefix_layout(int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim, int groups) {
-    const int64_t rows = batch * drafts * (q_heads / kv_heads) / groups;
-    PrefixLayout l;
-    l.walk = layout_of((int)(rows > 65536 ? 65536 : rows < 1 ? 1 : rows), kv_heads, head_dim);
-    l.waves = rows > 128 || (head_dim == 256 && rows > 64) ? 8 : rows > 64 ? 4 : 0;
-    l.span = l.waves ? 32 * l.waves : 16 * l.walk.nr * l.walk.groups;
-    const int columns = l.waves ? kv_heads : kv_heads / l.walk.heads;
-    const int waves = l.waves ? l.waves : l.walk.heads * l.walk.groups;
-    l.shift = 3;
-    while ((int64_t)columns * waves << (l.shift + 1) <= kGridWaves) ++l.shift;
-    l.walk.shift = l.shift, l.walk.columns = columns;
+template <int D, int W>
+constexpr int kPrefixLds = W ? 4 * Wide<D, W ? W : 1>::kTile : 0;    // keys and values, twice
+template <int D, int W, int NR, int HW, int RG>
+constexpr int kThreadsOf = W ? 64 * W : 64 * HW * RG;
+template <int D, int W, int NR, int HW, int RG>
+__global__ __launch_bounds__((kThreadsOf<D, W, NR, HW, RG>), D == 256 && W == 0 ? 1 : 2) void attn_shared_kernel(
+    const TreeArgs pre, const TreeArgs own, const Split split) {
+    constexpr int kLds = kPrefixLds<D, W> > kStaging<D, HW> ? kPrefixLds<D, W> : kStaging<D, HW>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    const int i = (int)blockIdx.x - split.own_blocks;
+    if (i < 0) {
+        if (W && __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= HW * RG) return;
+        walk<kOwn, D, NR, HW, RG>(own, lds, blockIdx.x & ((1 << split.own_shift) - 1), blockIdx.x >> split.own_shift);
+        return;
+    }
+    const int x = i & ((1 << split.prefix_shift) - 1), y = i >> split.prefix_shift;
+    if constexpr (W != 0)
+        attend_prefix<D, W>(pre, lds, x, y);
+    else
+        walk<kPrefix, D, NR, HW, RG>(pre, lds, x, y);
+}
+
+// Joins the pieces of a sequence's own tokens and of its group's prefix: workgroup (x, y)
+// takes 16 rows of a head (x) of sequence y, and of their values the kPer slices from kPer
+// * z on.  The prefix's tiles of 16 rows begin elsewhere: each lane finds its row's.
+template <int D, int kPer, int kTeams>
+__global__ __launch_bounds__(64 * kPer * kTeams) void attn_shared_join_kernel(const TreeArgs a, const TreeArgs pre, int span) {
+    constexpr int kTeam = 64 * kPer;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int b = blockIdx.y, row_tile = blockIdx.x % a.row_tiles, r0 = row_tile * 16, head = blockIdx.x / a.row_tiles;
+    const int4 own = a.own_pieces[b];                         // not written for a sequence without drafted tokens
+    const int rows = drafts_of(a, b) * a.group;
+    if (r0 >= rows) return;
+    const int first = own.x >> 1, last = own.y;
+    const bool whole = first == last, shares = own.z >= 0;
+    if (whole && !shares) return;                             // one piece: written already
+    const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = kPer * blockIdx.z + (part >> 6);
+
+    Joined<D, kTeams> joined;
+    if (shares) {
+        const int64_t row = (int64_t)(b - own.w) * pre.rows + r0 + c;
+        const bool live = r0 + c < rows;
+        const int2 of = pre.span_pieces[span_index(pre, own.z, own.w, live ? row : row - c, span)];
+        const int x0 = of.x >> 1, x1 = of.y;
+        int most = x1 - x0;
+#pragma unroll
+        for (int n = 1; n < 16; n *= 2) most = max(most, __shfl_xor(most, n, 64));
+        const int64_t tile0 = (int64_t)own.w * pre.rows / 16 + own.z, row16 = row & ~15ll;
+        joined.add(pre.part, prefix_place(pre, false, 0, 0, 0, span, 0).stats, team, i, g, x0, live ? x1 : x0 - 1, most, (int)(row & 15),
+                   [&](int x) {
+                       return prefix_place(pre, x0 == x1, x == x0 ? of.x : 2 * (int64_t)x, tile0, row16, span, head).tile;
+                   });
+    }
+    joined.add(a.part, part_place<kOwn>(a, whole, 0, b, 0, row_tile, head).stats, team, i, g, first, last, last - first, c, [&](int x) {
+        return part_place<kOwn>(a, whole, x == first ? own.x : 2 * (int64_t)x, b, 0, row_tile, head).tile;
+    });
+    finish_join<D, kPer>(joined, team, part, i, lane, r0, rows, [&](int row) {
+        return a.out + ((int64_t)b * a.drafts + row / a.group) * a.ld_out + ((int64_t)head * a.group + row % a.group) * D;
+    });
+}
+
+// How the call is laid out, from its shapes alone.  The prefixes are attended by the walk,
+// laid out for as many rows as a group has on average, or by attend_prefix; spans of rows
+// are laid end to end, so that columns are heads alone.
+struct SharedLayout {
+    Layout own;
+    int waves;                             // of attend_prefix; 0: the walk, laid out as own
+    int span, prefix_shift, prefix_columns;
+};
+SharedLayout shared_layout(int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim, int groups) {
+    const int own_rows = drafts * (q_heads / kv_heads);
+    const int64_t rows = batch * own_rows / groups;
+    SharedLayout l;
+    l.waves = rows <= 64 ? 0 : head_dim == 256 ? 8 : 4;
+    l.own = layout_of(l.waves ? own_rows : (int)(rows < own_rows ? own_rows : rows), kv_heads, head_dim);
+    if (!l.waves) {                        // the columns of the sequences' own rows
+        const int span = 16 * l.own.nr * l.own.groups;
+        l.own.columns = kv_heads / l.own.heads * ((own_rows + span - 1) / span);
+    }
+    l.span = l.waves ? 32 * l.waves : 16 * l.own.nr * l.own.groups;
+    l.prefix_columns = l.waves ? kv_heads : kv_heads / l.own.heads;
+    const int waves = l.waves ? l.waves : l.own.heads * l.own.groups;
+    l.prefix_shift = 3;
+    while ((int64_t)l.prefix_columns * waves << (l.prefix_shift + 1) <= kGridWaves) ++l.prefix_shift;
     return l;
 }
 
-int64_t prefix_tiles(const PrefixLayout& l, int64_t batch, int rows, int kv_heads, int groups) {
-    return (((int64_t)2 << l.shift) * (l.span / 16) + batch * rows / 16 + groups) * kv_heads;
+int64_t own_tiles(const SharedLayout& l, int64_t batch, int rows, int kv_heads) {
+    return (((int64_t)2 << l.own.shift) + batch) * kv_heads * ((rows + 15) / 16);
 }
-int64_t own_tiles(const Layout& l, int64_t batch, int rows, int kv_heads) {
-    return (((int64_t)2 << l.shift) + batch) * kv_heads * ((rows + 15) / 16);
+int64_t prefix_tiles(const SharedLayout& l, int64_t batch, int rows, int kv_heads, int groups) {
+    return (((int64_t)2 << l.prefix_shift) * (l.span / 16) + batch * rows / 16 + groups) * kv_heads;
 }
+int64_t spans(const SharedLayout& l, int64_t batch, int rows, int groups) { return batch * rows / l.span + groups; }
 
 }  // namespace
 
+// In this order: own_pieces, span_pieces, the own tokens' partial results, the prefixes'.
 size_t attn_shared_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads, int groups) {
+    if (groups == 0) return attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
     const int rows = drafts * (q_heads / kv_heads);
-    const size_t own = part_bytes(own_tiles(layout_of(rows, kv_heads, head_dim), batch, rows, kv_heads), head_dim);
-    if (groups == 0) return own;
-    return own + part_bytes(prefix_tiles(prefix_layout(batch, drafts, q_heads, kv_heads, head_dim, groups), batch, rows,
-                                         kv_heads, groups), head_dim);
+    const SharedLayout l = shared_layout(batch, drafts, q_heads, kv_heads, head_dim, groups);
+    return (size_t)batch * sizeof(int4) + (size_t)((spans(l, batch, rows, groups) + 1) / 2) * sizeof(int4) +
+           part_bytes(own_tiles(l, batch, rows, kv_heads) + prefix_tiles(l, batch, rows, kv_heads, groups), head_dim);
 }
 
 hipError_t launch_attn_shared(const AttnTree& p, hipStream_t s) {
     if (p.num_groups == 0) return launch_attn_tree(p, s);
     const int rows = p.drafts * (p.q_heads / p.kv_heads);
-    const Layout l = layout_of(rows, p.kv_heads, p.head_dim);
-    const PrefixLayout lp = prefix_layout(p.batch, p.drafts, p.q_heads, p.kv_heads, p.head_dim, p.num_groups);
-    TreeArgs own = cache_args(p, l), pre = cache_args(p, lp.walk);
-    own.groups = pre.groups = p.groups;
-    own.prefix_lens = pre.prefix_lens = p.prefix_lens;
-    own.num_groups = pre.num_groups = p.num_groups;
-    pre.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) +
-                                        part_bytes(own_tiles(l, p.batch, rows, p.kv_heads), p.head_dim));
+    const SharedLayout l = shared_layout(p.batch, p.drafts, p.q_heads, p.kv_heads, p.head_dim, p.num_groups);
+    TreeArgs own = cache_args(p, l.own);
+    own.groups = p.groups, own.prefix_lens = p.prefix_lens, own.num_groups = p.num_groups;
+    own.own_pieces = static_cast<int4*>(p.ws);
+    own.span_pieces = reinterpret_cast<int2*>(own.own_pieces + p.batch);
+    own.part = reinterpret_cast<float*>(own.own_pieces + p.batch + (spans(l, p.batch, rows, p.num_groups) + 1) / 2);
+    TreeArgs pre = own;
+    pre.part = own.part + part_bytes(own_tiles(l, p.batch, rows, p.kv_heads), p.head_dim) / sizeof(float);
+    pre.shift = l.prefix_shift;
+    Split split;
+    split.own_shift = l.own.shift, split.prefix_shift = l.prefix_shift;
+    split.own_blocks = l.own.columns << l.own.shift;
+    const unsigned blocks = (unsigned)(split.own_blocks + (l.prefix_columns << l.prefix_shift));
     return with_head_dim(p.head_dim, [&](auto d) {
-        constexpr int D = decltype(d)::value;
-        pre.prefix_tile = lp.waves ? Wide<D, 8>::kTokens : kTile;
-        hipError_t e;
-        if (lp.waves == 0) {
-            e = launch_walk<kPrefix, D>(pre, lp.walk, (unsigned)lp.walk.columns, s);
-        } else {
-            const dim3 grid(1u << lp.shift, (unsigned)p.kv_heads);
-            if (lp.waves == 8) {
-                attn_prefix_kernel<D, 8><<<grid, 512, 0, s>>>(pre);
-            } else {
-                if constexpr (D < 256) attn_prefix_kernel<D, 4><<<grid, 256, 0, s>>>(pre);
-            }
-            e = hipGetLastError();
-        }
-        if (e == hipSuccess) e = launch_walk<kOwn, D>(own, l, (unsigned)l.columns, s);
-        return e != hipSuccess ? e : launch_join<kOwn, D>(own, {pre, lp.span}, 1, s);
+        constexpr int D = decltype(d)::value, kW = D == 256 ? 8 : 4;
+        hipError_t e = with_layout<D>(l.own, [&](auto nr, auto hw, auto rg) {
+            constexpr int kNR = decltype(nr)::value, kHW = decltype(hw)::value, kRG = decltype(rg)::value;
+            pre.prefix_tile = l.waves ? Wide<D, kW>::kTokens : kTile;
+            if (l.waves)
+                attn_shared_kernel<D, kW, kNR, kHW, kRG><<<blocks, kThreadsOf<D, kW, kNR, kHW, kRG>, 0, s>>>(pre, own, split);
+            else
+                attn_shared_kernel<D, 0, kNR, kHW, kRG><<<blocks, kThreadsOf<D, 0, kNR, kHW, kRG>, 0, s>>>(pre, own, split);
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+        const unsigned row_tiles = (unsigned)(p.kv_heads * own.row_tiles);
+        // Few rows, and so few workgroups: 16 waves to a slice, as in launch_join.
+        if ((int64_t)row_tiles * p.batch * (D / 16) <= 512)
+            attn_shared_join_kernel<D, 1, 16><<<dim3(row_tiles, (unsigned)p.batch, D / 16), 1024, 0, s>>>(own, pre, l.span);
+        else
+            attn_shared_join_kernel<D, D / 16, 1><<<dim3(row_tiles, (unsigned)p.batch), 4 * D, 0, s>>>(own, pre, l.span);
+        return hipGetLastError();
     });
 }
 

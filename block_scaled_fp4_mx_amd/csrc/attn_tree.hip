@@ -76,7 +76,7 @@ hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s) {
     return with_head_dim(p.head_dim, [&](auto d) {
         constexpr int D = decltype(d)::value;
         const hipError_t e = launch_walk<kTree, D>(a, l, (unsigned)l.columns, s);
-        return e != hipSuccess ? e : launch_join<kTree, D>(a, {}, 1, s);
+        return e != hipSuccess ? e : launch_join<kTree, D>(a, 1, s);
     });
 }
 
