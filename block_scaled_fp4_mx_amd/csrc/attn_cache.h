@@ -53,16 +53,16 @@ struct TreeArgs {
     uint32_t flip;                         // sign bits of Q, set for a negative scale
     uint16_t* out;
     int64_t ld_out;
-    // Partial results [2 << shift][kv_heads][row tiles]: of 16 rows, the sums as the
+    // Partial results [2 * ranges][kv_heads][row tiles]: of 16 rows, the sums as the
     // lanes hold them ([D/16][64] of 4 values), then (m, sum) of each row.
     float* part;
-    int row_tiles, shift;
+    int row_tiles, shift, ranges;          // ranges: 1 << shift, or (kPrefix, kOwn) at most
     // kBlocks: lists [batch][drafts][lists][select] of blocks; the planes of workgroups
     // are the drafted tokens, and rows is one's, group.
     const int32_t* ids;
     int select, lists;
     // kPrefix, kOwn: group g is the sequences [groups[g], groups[g + 1]).  Pieces that
-    // are not cut stand behind those of the ranges (slot 2 << shift on): in kOwn by
+    // are not cut stand behind those of the ranges (slot 2 * ranges on): in kOwn by
     // sequence, in kPrefix by row tiles (tile_base).
     const int32_t *groups, *prefix_lens;
     int num_groups, prefix_tile;           // prefix_tile: tokens of a step of the prefix's walk
@@ -458,7 +458,7 @@ template <Mode kMode>
 __device__ __forceinline__ PartPlace part_place(const TreeArgs& a, bool whole, int64_t slot, int b, int plane, int row_tile,
                                                 int head) {
     const int planes = kMode == kBlocks ? a.drafts : 1;
-    const int64_t ranges = (int64_t)2 << a.shift, at = kMode == kOwn && whole ? ranges + b : slot;
+    const int64_t ranges = 2 * (int64_t)a.ranges, at = kMode == kOwn && whole ? ranges + b : slot;
     return {((at * a.kv_heads + head) * planes + plane) * a.row_tiles + row_tile,
             (ranges + (kMode == kOwn ? a.batch : 0)) * a.kv_heads * planes * a.row_tiles};
 }
@@ -466,7 +466,7 @@ __device__ __forceinline__ PartPlace part_place(const TreeArgs& a, bool whole, i
 // piece of a range has those of its span.
 __device__ __forceinline__ PartPlace prefix_place(const TreeArgs& a, bool whole, int64_t slot, int64_t tile0, int64_t row,
                                                   int span, int head) {
-    const int64_t ranges = ((int64_t)2 << a.shift) * (span / 16);
+    const int64_t ranges = 2 * (int64_t)a.ranges * (span / 16);
     const int64_t at = whole ? ranges + tile0 + row / 16 : slot * (span / 16) + row % span / 16;
     return {at * a.kv_heads + head, (ranges + tile_base_end(a)) * a.kv_heads};
 }
@@ -494,9 +494,17 @@ __device__ __forceinline__ void note_piece(const TreeArgs& a, int slot, bool beg
 template <int D, int HW>
 constexpr int kStaging = HW * kStages * Stage<D, HW>::kBytes;
 
-// The walk of workgroup (block_x, block_y).
-template <Mode kMode, int D, int NR, int HW, int RG>
-__device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int block_x, int block_y) {
+// A workgroup's tiles, and the first 64 sequences (groups).
+template <Mode kMode>
+struct Range {
+    Chunk<kMode> chunk;
+    int64_t lo, hi;
+};
+
+// The walk of workgroup (block_x, block_y): column block_y, range block_x (range_at(plane,
+// span) gives it).
+template <Mode kMode, int D, int NR, int HW, int RG, class RangeAt>
+__device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int block_x, int block_y, RangeAt range_at) {
     constexpr int kSteps = D / 32, kOut = D / 16;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     using S = Stage<D, HW>;
@@ -510,11 +518,10 @@ __device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int bl
     int r0 = ((kMode == kBlocks ? column - plane * spans : column) * RG + rg) * 16 * NR;
     const uint32_t lds = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_bytes)staging) + hw * kRegion;
     const Lane<D, HW> own = lane_of<D, HW>(a, head0, hw, lane);
-    Chunk<kMode> chunk = chunk_at<kMode>(a, 0, lane, plane, kSpan);
-    const int64_t total = all_tiles<kMode>(a, chunk, lane, plane, kSpan);
-    const int shift = shift_of(a, total);
-    const int64_t lo = block_x * total >> shift, hi = (block_x + 1) * total >> shift;
-    if (block_x >> shift || lo == hi) return;
+    const Range<kMode> range = range_at(plane, kSpan);
+    const int64_t lo = range.lo, hi = range.hi;
+    if (lo == hi) return;
+    Chunk<kMode> chunk = range.chunk;
 
     // The sequence that holds tile lo, and the tiles before it.
     int64_t before = 0;
@@ -870,7 +877,14 @@ __device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int bl
 template <Mode kMode, int D, int NR, int HW, int RG>
 __global__ __launch_bounds__(64 * HW * RG, D == 256 ? 1 : 2) void attn_walk_kernel(const TreeArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t staging[kStaging<D, HW>];
-    walk<kMode, D, NR, HW, RG>(a, staging, blockIdx.x, blockIdx.y);
+    walk<kMode, D, NR, HW, RG>(a, staging, blockIdx.x, blockIdx.y, [&](int plane, int span) {
+        const int lane = threadIdx.x & 63;
+        Range<kMode> r{chunk_at<kMode>(a, 0, lane, plane, span), 0, 0};
+        const int64_t total = all_tiles<kMode>(a, r.chunk, lane, plane, span);
+        const int shift = shift_of(a, total);
+        if (blockIdx.x >> shift == 0) r.lo = blockIdx.x * total >> shift, r.hi = (blockIdx.x + 1) * total >> shift;
+        return r;
+    });
 }
 
 // A wave's part in joining partial results of 16 rows of one head: of their values slice
@@ -888,6 +902,7 @@ struct Joined {
         constexpr int kBatch = 8;
         const v4f* o = reinterpret_cast<const v4f*>(parts) + 64 * i + 16 * g + row;
         const float2* ml = reinterpret_cast<const float2*>(parts + stats_at * (16 * D)) + row;
+#pragma unroll 1
         for (int x0 = first + team; x0 - first <= most; x0 += kBatch * kTeams) {
             float2 s[kBatch];
             v4f v[kBatch];
@@ -1090,7 +1105,7 @@ inline TreeArgs cache_args(const AttnTree& p, const Layout& l) {
     // Never 0: a hidden score is -inf and has to stay that when scaled.
     a.scale2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
     a.flip = p.scale < 0 ? 0x80008000u : 0u;
-    a.part = static_cast<float*>(p.ws), a.row_tiles = (a.rows + 15) / 16, a.shift = l.shift;
+    a.part = static_cast<float*>(p.ws), a.row_tiles = (a.rows + 15) / 16, a.shift = l.shift, a.ranges = 1 << l.shift;
     return a;
 }
 // Bytes of tiles of 16 rows' sums and (m, sum).

@@ -30,6 +30,7 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 // chunk x of row r at x ^ turn: key_turn keeps the 16 lanes that read one chunk of 16
 // rows in different banks, value_turn the 4 rows of 64 bytes that half the lanes of a
 // transposing read take.
+constexpr int kWideWaves = 8;              // of a workgroup that attends a prefix of many rows
 template <int D, int W>
 struct Wide {
     static constexpr int kRows = 32 * W;                     // query rows of a workgroup
@@ -43,17 +44,15 @@ struct Wide {
 
 // Workgroup (block_x, head) of the prefix's many rows.
 template <int D, int W>
-__device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_lds, int block_x, int head) {
+__device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_lds, int block_x, int head, const Range<kPrefix>& range) {
     using S = Wide<D, W>;
     constexpr int kRows = S::kRows, kTokens = S::kTokens, kSteps = D / 16, kOut = D / 32, kSub = kTokens / 32;
     constexpr int kBatch = kSteps < 8 ? kSteps : 8, kGroups = kTokens / 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
 
-    Chunk<kPrefix> chunk = chunk_at<kPrefix>(a, 0, lane, 0, kRows);
-    const int64_t total = all_tiles<kPrefix>(a, chunk, lane, 0, kRows);
-    const int shift = shift_of(a, total);
-    const int64_t lo = block_x * total >> shift, hi = (block_x + 1) * total >> shift;
-    if (block_x >> shift || lo == hi) return;
+    const int64_t lo = range.lo, hi = range.hi;
+    if (lo == hi) return;
+    Chunk<kPrefix> chunk = range.chunk;
     int64_t before = 0;
     while (before + (int64_t)chunk.all() <= lo) {
         before += chunk.all();
@@ -298,13 +297,24 @@ __device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_
     }
 }
 
-// Both kinds of work in one launch: the first own_blocks workgroups take the sequences' own
-// tokens, by the walk <NR, HW, RG>, the others the prefixes, by the same walk (W = 0) or
-// attend_prefix.  (64 samples of 16384 tokens: 62 us; the prefixes first 65; half of them
-// first 72, as the others then start late; two launches 68.)
+// Both kinds of work in one launch of workgroups that are all resident: the first ones
+// take the sequences' own tokens, by the walk <NR, HW, RG>, the others the prefixes, by the
+// same walk (W = 0) or attend_prefix, each kind as many as its tiles are of all.  (With a
+// round of workgroups for each kind, 64 samples of 16384 tokens took 62 us.)
 struct Split {
-    int own_blocks, own_shift, prefix_shift;
+    int own_columns, prefix_columns;       // workgroups to a range
 };
+// Tile x * total / ranges, the same for all who ask.
+__device__ __forceinline__ int64_t tile_at(int x, int64_t total, int ranges) {
+    return x == ranges ? total : (int64_t)((double)x * (double)total / (double)ranges);
+}
+// Ranges of at most `most`, of kMinTiles tiles and more.
+__device__ __forceinline__ int ranges_of(int64_t tiles, int64_t most) {
+    return tiles == 0 ? 0 : (int)min(max(tiles / kMinTiles, (int64_t)1), max(most, (int64_t)1));
+}
+// What a tile of the own tokens costs a workgroup, of what one of the prefix does.
+constexpr double own_cost(int waves) { return waves ? 0.4 : 1.0; }
+
 template <int D, int W>
 constexpr int kPrefixLds = W ? 4 * Wide<D, W ? W : 1>::kTile : 0;    // keys and values, twice
 template <int D, int W, int NR, int HW, int RG>
@@ -313,18 +323,37 @@ template <int D, int W, int NR, int HW, int RG>
 __global__ __launch_bounds__((kThreadsOf<D, W, NR, HW, RG>), D == 256 && W == 0 ? 1 : 2) void attn_shared_kernel(
     const TreeArgs pre, const TreeArgs own, const Split split) {
     constexpr int kLds = kPrefixLds<D, W> > kStaging<D, HW> ? kPrefixLds<D, W> : kStaging<D, HW>;
+    constexpr int kSpan = W ? 32 * W : 16 * NR * RG;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-    const int i = (int)blockIdx.x - split.own_blocks;
-    if (i < 0) {
+    const int lane = threadIdx.x & 63;
+    Range<kOwn> mine{chunk_at<kOwn>(own, 0, lane, 0, 0), 0, 0};
+    Range<kPrefix> shared{chunk_at<kPrefix>(pre, 0, lane, 0, kSpan), 0, 0};
+    const int64_t own_total = all_tiles<kOwn>(own, mine.chunk, lane, 0, 0);
+    const int64_t prefix_total = all_tiles<kPrefix>(pre, shared.chunk, lane, 0, kSpan);
+    const double own_work = (double)own_total * split.own_columns * own_cost(W), work = own_work + (double)prefix_total * split.prefix_columns;
+    if (work == 0) return;
+    const int blocks = gridDim.x;
+    // The prefix's share, in eights, so that the heads of one range meet on one XCD; the rest
+    // goes to the own tokens.
+    int prefix_ranges = ranges_of(prefix_total, (int64_t)((blocks - split.own_columns) * (1.0 - own_work / work)) / split.prefix_columns);
+    prefix_ranges = min(prefix_ranges >= 8 ? prefix_ranges & ~7 : prefix_ranges, pre.ranges);
+    const int own_ranges = min(ranges_of(own_total, (blocks - prefix_ranges * split.prefix_columns) / split.own_columns), own.ranges);
+    int i = blockIdx.x;
+    if (i < own_ranges * split.own_columns) {
         if (W && __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= HW * RG) return;
-        walk<kOwn, D, NR, HW, RG>(own, lds, blockIdx.x & ((1 << split.own_shift) - 1), blockIdx.x >> split.own_shift);
+        const int x = i % own_ranges;
+        mine.lo = tile_at(x, own_total, own_ranges), mine.hi = tile_at(x + 1, own_total, own_ranges);
+        walk<kOwn, D, NR, HW, RG>(own, lds, x, i / own_ranges, [&](int, int) { return mine; });
         return;
     }
-    const int x = i & ((1 << split.prefix_shift) - 1), y = i >> split.prefix_shift;
+    i -= own_ranges * split.own_columns;
+    if (i >= prefix_ranges * split.prefix_columns) return;
+    const int x = i % prefix_ranges, y = i / prefix_ranges;
+    shared.lo = tile_at(x, prefix_total, prefix_ranges), shared.hi = tile_at(x + 1, prefix_total, prefix_ranges);
     if constexpr (W != 0)
-        attend_prefix<D, W>(pre, lds, x, y);
+        attend_prefix<D, W>(pre, lds, x, y, shared);
     else
-        walk<kPrefix, D, NR, HW, RG>(pre, lds, x, y);
+        walk<kPrefix, D, NR, HW, RG>(pre, lds, x, y, [&](int, int) { return shared; });
 }
 
 // Joins the pieces of a sequence's own tokens and of its group's prefix: workgroup (x, y)
@@ -345,17 +374,22 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_shared_join_kernel(co
 
     Joined<D, kTeams> joined;
     if (shares) {
-        const int64_t row = (int64_t)(b - own.w) * pre.rows + r0 + c;
+        // Rows of a group are below 2^31: 32-bit divisions.
+        const uint32_t row = (uint32_t)(b - own.w) * (uint32_t)pre.rows + r0 + c, first_row = row - c;
         const bool live = r0 + c < rows;
-        const int2 of = pre.span_pieces[span_index(pre, own.z, own.w, live ? row : row - c, span)];
-        const int x0 = of.x >> 1, x1 = of.y;
+        const uint32_t its_span = (live ? row : first_row) / (uint32_t)span;
+        const int2 of = pre.span_pieces[(uint32_t)own.w * (uint32_t)pre.rows / (uint32_t)span + own.z + its_span];
+        const int x0 = of.x >> 1, x1 = of.y, per_slot = span / 16;
         int most = x1 - x0;
 #pragma unroll
         for (int n = 1; n < 16; n *= 2) most = max(most, __shfl_xor(most, n, 64));
-        const int64_t tile0 = (int64_t)own.w * pre.rows / 16 + own.z, row16 = row & ~15ll;
+        // Tiles of a piece, or of the group's uncut spans: from there on, the row's.
+        const int64_t in_slot = (row - its_span * (uint32_t)span) / 16;
+        const int64_t uncut = prefix_place(pre, true, 0, (int64_t)own.w * pre.rows / 16 + own.z, row / 16 * 16, span, head).tile;
         joined.add(pre.part, prefix_place(pre, false, 0, 0, 0, span, 0).stats, team, i, g, x0, live ? x1 : x0 - 1, most, (int)(row & 15),
                    [&](int x) {
-                       return prefix_place(pre, x0 == x1, x == x0 ? of.x : 2 * (int64_t)x, tile0, row16, span, head).tile;
+                       const int64_t slot = x == x0 ? of.x : 2 * (int64_t)x;
+                       return x0 == x1 ? uncut : (slot * per_slot + in_slot) * pre.kv_heads + head;
                    });
     }
     joined.add(a.part, part_place<kOwn>(a, whole, 0, b, 0, row_tile, head).stats, team, i, g, first, last, last - first, c, [&](int x) {
@@ -372,31 +406,32 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_shared_join_kernel(co
 struct SharedLayout {
     Layout own;
     int waves;                             // of attend_prefix; 0: the walk, laid out as own
-    int span, prefix_shift, prefix_columns;
+    int span, prefix_columns, blocks;
+    int own_ranges() const { return blocks / own.columns; }
+    int prefix_ranges() const { return blocks / prefix_columns; }
 };
 SharedLayout shared_layout(int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim, int groups) {
     const int own_rows = drafts * (q_heads / kv_heads);
     const int64_t rows = batch * own_rows / groups;
     SharedLayout l;
-    l.waves = rows <= 64 ? 0 : head_dim == 256 ? 8 : 4;
+    l.waves = rows <= 64 ? 0 : kWideWaves;
     l.own = layout_of(l.waves ? own_rows : (int)(rows < own_rows ? own_rows : rows), kv_heads, head_dim);
-    if (!l.waves) {                        // the columns of the sequences' own rows
-        const int span = 16 * l.own.nr * l.own.groups;
-        l.own.columns = kv_heads / l.own.heads * ((own_rows + span - 1) / span);
-    }
-    l.span = l.waves ? 32 * l.waves : 16 * l.own.nr * l.own.groups;
+    const int own_span = 16 * l.own.nr * l.own.groups;
+    l.own.columns = kv_heads / l.own.heads * ((own_rows + own_span - 1) / own_span);
+    l.span = l.waves ? 32 * l.waves : own_span;
     l.prefix_columns = l.waves ? kv_heads : kv_heads / l.own.heads;
-    const int waves = l.waves ? l.waves : l.own.heads * l.own.groups;
-    l.prefix_shift = 3;
-    while ((int64_t)l.prefix_columns * waves << (l.prefix_shift + 1) <= kGridWaves) ++l.prefix_shift;
+    // All resident where the columns allow it.
+    l.blocks = kGridWaves / (l.waves ? l.waves : l.own.heads * l.own.groups);
+    const int least = 2 * (l.own.columns + l.prefix_columns);
+    if (l.blocks < least) l.blocks = least;
     return l;
 }
 
 int64_t own_tiles(const SharedLayout& l, int64_t batch, int rows, int kv_heads) {
-    return (((int64_t)2 << l.own.shift) + batch) * kv_heads * ((rows + 15) / 16);
+    return (2 * (int64_t)l.own_ranges() + batch) * kv_heads * ((rows + 15) / 16);
 }
 int64_t prefix_tiles(const SharedLayout& l, int64_t batch, int rows, int kv_heads, int groups) {
-    return (((int64_t)2 << l.prefix_shift) * (l.span / 16) + batch * rows / 16 + groups) * kv_heads;
+    return (2 * (int64_t)l.prefix_ranges() * (l.span / 16) + batch * rows / 16 + groups) * kv_heads;
 }
 int64_t spans(const SharedLayout& l, int64_t batch, int rows, int groups) { return batch * rows / l.span + groups; }
 
@@ -422,13 +457,11 @@ hipError_t launch_attn_shared(const AttnTree& p, hipStream_t s) {
     own.part = reinterpret_cast<float*>(own.own_pieces + p.batch + (spans(l, p.batch, rows, p.num_groups) + 1) / 2);
     TreeArgs pre = own;
     pre.part = own.part + part_bytes(own_tiles(l, p.batch, rows, p.kv_heads), p.head_dim) / sizeof(float);
-    pre.shift = l.prefix_shift;
-    Split split;
-    split.own_shift = l.own.shift, split.prefix_shift = l.prefix_shift;
-    split.own_blocks = l.own.columns << l.own.shift;
-    const unsigned blocks = (unsigned)(split.own_blocks + (l.prefix_columns << l.prefix_shift));
+    own.ranges = l.own_ranges(), pre.ranges = l.prefix_ranges();
+    const Split split{l.own.columns, l.prefix_columns};
+    const unsigned blocks = (unsigned)l.blocks;
     return with_head_dim(p.head_dim, [&](auto d) {
-        constexpr int D = decltype(d)::value, kW = D == 256 ? 8 : 4;
+        constexpr int D = decltype(d)::value, kW = kWideWaves;
         hipError_t e = with_layout<D>(l.own, [&](auto nr, auto hw, auto rg) {
             constexpr int kNR = decltype(nr)::value, kHW = decltype(hw)::value, kRG = decltype(rg)::value;
             pre.prefix_tile = l.waves ? Wide<D, kW>::kTokens : kTile;
