@@ -312,8 +312,9 @@ __device__ __forceinline__ int64_t tile_at(int x, int64_t total, int ranges) {
 __device__ __forceinline__ int ranges_of(int64_t tiles, int64_t most) {
     return tiles == 0 ? 0 : (int)min(max(tiles / kMinTiles, (int64_t)1), max(most, (int64_t)1));
 }
-// What a tile of the own tokens costs a workgroup, of what one of the prefix does.
-constexpr double own_cost(int waves) { return waves ? 0.4 : 1.0; }
+// What a tile of the own tokens costs a workgroup, of what one of the prefix does (heads of
+// 128: 1.0 and 2.6 us).  0.33 to 0.5 take 68 to 73 us for 64 samples, 30 to 34 for sessions.
+constexpr double own_cost(int waves) { return waves ? 0.37 : 1.0; }
 
 template <int D, int W>
 constexpr int kPrefixLds = W ? 4 * Wide<D, W ? W : 1>::kTile : 0;    // keys and values, twice
@@ -333,10 +334,9 @@ __global__ __launch_bounds__((kThreadsOf<D, W, NR, HW, RG>), D == 256 && W == 0 
     const double own_work = (double)own_total * split.own_columns * own_cost(W), work = own_work + (double)prefix_total * split.prefix_columns;
     if (work == 0) return;
     const int blocks = gridDim.x;
-    // The prefix's share, in eights, so that the heads of one range meet on one XCD; the rest
-    // goes to the own tokens.
-    int prefix_ranges = ranges_of(prefix_total, (int64_t)((blocks - split.own_columns) * (1.0 - own_work / work)) / split.prefix_columns);
-    prefix_ranges = min(prefix_ranges >= 8 ? prefix_ranges & ~7 : prefix_ranges, pre.ranges);
+    // The prefix's share; the rest goes to the own tokens.
+    const int prefix_ranges = min(
+        ranges_of(prefix_total, (int64_t)((blocks - split.own_columns) * (1.0 - own_work / work)) / split.prefix_columns), pre.ranges);
     const int own_ranges = min(ranges_of(own_total, (blocks - prefix_ranges * split.prefix_columns) / split.own_columns), own.ranges);
     int i = blockIdx.x;
     if (i < own_ranges * split.own_columns) {
@@ -348,7 +348,7 @@ __global__ __launch_bounds__((kThreadsOf<D, W, NR, HW, RG>), D == 256 && W == 0 
     }
     i -= own_ranges * split.own_columns;
     if (i >= prefix_ranges * split.prefix_columns) return;
-    const int x = i % prefix_ranges, y = i / prefix_ranges;
+    const int x = i / split.prefix_columns, y = i % split.prefix_columns;
     shared.lo = tile_at(x, prefix_total, prefix_ranges), shared.hi = tile_at(x + 1, prefix_total, prefix_ranges);
     if constexpr (W != 0)
         attend_prefix<D, W>(pre, lds, x, y, shared);
