@@ -1046,7 +1046,7 @@ int fp4_kv_select_mx(const void* q, int64_t ld_q, const uint8_t* index_codes, co
 
 size_t fp4_attn_blocks_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
     if (batch <= 0 || drafts < 1 || drafts > 64 || check_heads(q_heads, kv_heads, head_dim) != FP4_OK) return 0;
-    return fp4::attn_blocks_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
+    return fp4::attn_blocks_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads);
 }
 
 int fp4_attn_blocks_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, const int32_t* page_table, int64_t max_pages,
@@ -1065,7 +1065,7 @@ int fp4_attn_blocks_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, c
     if (int e = check_attn_arrays(c)) return e;
     if (n_select) { FP4_SCALAR_PTR(block_ids); }
     if (int e = check_workspace(workspace, workspace_bytes,
-                                fp4::attn_blocks_workspace_bytes(drafts, q_heads, head_dim, kv_heads)))
+                                fp4::attn_blocks_workspace_bytes(batch, drafts, q_heads, head_dim, kv_heads)))
         return e;
     fp4::AttnTree p = attn_of(c);
     p.block_ids = block_ids;

@@ -22,13 +22,15 @@ int64_t attn_blocks_columns(int drafts, int q_heads, int kv_heads, int head_dim,
     return blocks_layout(drafts, q_heads, kv_heads, head_dim, lists > 1).columns;
 }
 
-size_t attn_blocks_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads) {
+// The partial results, then span_pieces.
+size_t attn_blocks_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads) {
     int shift = 0;
     for (bool apart : {false, true}) {
         const Layout l = blocks_layout(drafts, q_heads, kv_heads, head_dim, apart);
         shift = l.shift > shift ? l.shift : shift;
     }
-    return part_bytes(((int64_t)2 << shift) * kv_heads * drafts * ((q_heads / kv_heads + 15) / 16), head_dim);
+    return part_bytes(((int64_t)2 << shift) * kv_heads * drafts * ((q_heads / kv_heads + 15) / 16), head_dim) +
+           (size_t)batch * drafts * sizeof(int2);
 }
 
 hipError_t launch_attn_blocks(const AttnTree& p, hipStream_t s) {
@@ -36,6 +38,8 @@ hipError_t launch_attn_blocks(const AttnTree& p, hipStream_t s) {
     TreeArgs a = cache_args(p, l);
     a.rows = a.group, a.row_tiles = (a.group + 15) / 16;
     a.ids = p.block_ids, a.select = p.n_select, a.lists = p.lists;
+    a.span_pieces = reinterpret_cast<int2*>(a.part + part_bytes(((int64_t)2 << l.shift) * p.kv_heads * p.drafts * a.row_tiles, p.head_dim) /
+                                                         sizeof(float));
     return with_head_dim(p.head_dim, [&](auto d) {
         constexpr int D = decltype(d)::value;
         const hipError_t e = launch_walk<kBlocks, D>(a, l, (unsigned)l.columns, s);

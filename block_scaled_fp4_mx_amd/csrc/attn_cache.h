@@ -68,7 +68,8 @@ struct TreeArgs {
     int num_groups, prefix_tile;           // prefix_tile: tokens of a step of the prefix's walk
     // Where the pieces of a sequence's own tokens, or of a span of a group's rows, stand,
     // for the join: {first slot, last range, group or -1, its first sequence} by sequence, {first
-    // slot, last range} by span_index.  The workgroups that begin and end them write it.
+    // slot, last range} by span_index (kBlocks: by sequence and drafted token).  The
+    // workgroups that begin and end them write it.
     int4* own_pieces;
     int2* span_pieces;
 };
@@ -475,11 +476,16 @@ __device__ __forceinline__ PartPlace prefix_place(const TreeArgs& a, bool whole,
 __device__ __forceinline__ int64_t span_index(const TreeArgs& a, int group, int first_sequence, int64_t row, int span) {
     return (int64_t)first_sequence * a.rows / span + group + row / span;
 }
-// item: a sequence or a group; token, tokens: as its chunk has them; row: of the span.
+// item: a sequence or a group; token, tokens: as its chunk has them (kBlocks: the drafted
+// token); row: of the span.
 template <Mode kMode>
 __device__ __forceinline__ void note_piece(const TreeArgs& a, int slot, bool begins, bool ends, int item, int token, int tokens,
                                            int64_t row, int span) {
-    if constexpr (kMode == kOwn) {
+    if constexpr (kMode == kBlocks) {
+        int2* to = a.span_pieces + ((int64_t)item * a.drafts + token);
+        if (begins) to->x = slot;
+        if (ends) to->y = slot >> 1;
+    } else if constexpr (kMode == kOwn) {
         int4* to = a.own_pieces + item;
         if (begins) to->x = slot, to->z = token, to->w = tokens;
         if (ends) to->y = slot >> 1;
@@ -863,7 +869,10 @@ __device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int bl
                 if (g == 0) ml[p.tile * 16 + c] = make_float2(m[n], l);
             }
         }
-        if constexpr (kMode == kOwn || kMode == kPrefix) {
+        if constexpr (kMode == kBlocks) {
+            if (block_y == plane * spans * groups && threadIdx.x == 0)
+                note_piece<kMode>(a, 2 * block_x + (at == lo ? 0 : 1), t0 == 0, t1 == tiles, b, plane, 0, 0, kSpan);
+        } else if constexpr (kMode == kOwn || kMode == kPrefix) {
             if (block_y == 0 && threadIdx.x == 0)
                 note_piece<kMode>(a, 2 * block_x + (at == lo ? 0 : 1), t0 == 0, t1 == tiles, b,
                                   __builtin_amdgcn_readlane(chunk.token, at_lane), __builtin_amdgcn_readlane(chunk.tokens, at_lane), r0,
@@ -985,26 +994,32 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_join_kernel(const Tre
     const int b = blockIdx.y, row_tile = blockIdx.x % a.row_tiles, r0 = row_tile * 16;
     const int planes = kMode == kBlocks ? a.drafts : 1, at_plane = blockIdx.x / a.row_tiles;
     const int head = at_plane / planes, plane = at_plane - head * planes;
-    Chunk<kMode> chunk = chunk_at<kMode>(a, 0, lane, plane, 0);
-    const int64_t total = all_tiles<kMode>(a, chunk, lane, plane, 0);
-    const int shift = shift_of(a, total);
-    int64_t before = 0;
-    while (b - chunk.first >= 64) {
-        before += chunk.all();
-        chunk = chunk_at<kMode>(a, chunk.first + 64, lane, plane, 0);
+    int rows, first, last, first_slot;
+    if constexpr (kMode == kBlocks) {
+        const int2 pieces = a.span_pieces[(int64_t)b * a.drafts + plane];     // not written without drafted tokens
+        rows = plane < drafts_of(a, b) ? a.group : 0;
+        first = pieces.x >> 1, last = pieces.y, first_slot = pieces.x;
+    } else {
+        Chunk<kMode> chunk = chunk_at<kMode>(a, 0, lane, plane, 0);
+        const int64_t total = all_tiles<kMode>(a, chunk, lane, plane, 0);
+        const int shift = shift_of(a, total);
+        int64_t before = 0;
+        while (b - chunk.first >= 64) {
+            before += chunk.all();
+            chunk = chunk_at<kMode>(a, chunk.first + 64, lane, plane, 0);
+        }
+        const uint32_t tiles = chunk.read(chunk.tiles, b - chunk.first);
+        rows = __builtin_amdgcn_readlane(chunk.drafts, b - chunk.first) * a.group;
+        before += chunk.read(chunk.upto, b - chunk.first) - tiles;
+        if (tiles == 0) return;
+        // The ranges that hold its first and last tile: tile t lies in the last range
+        // whose start, x * total >> shift, is at most t.
+        first = (int)scalar((((before + 1) << shift) - 1) / total);
+        last = (int)scalar((((before + tiles) << shift) - 1) / total);
+        // The first piece is its range's second one unless the range starts with it.
+        first_slot = 2 * first + ((first * total >> shift) == before ? 0 : 1);
     }
-    const uint32_t tiles = chunk.read(chunk.tiles, b - chunk.first);
-    const int nd = __builtin_amdgcn_readlane(chunk.drafts, b - chunk.first);
-    before += chunk.read(chunk.upto, b - chunk.first) - tiles;
-    const int rows = kMode == kBlocks ? a.group : nd * a.group;
-    if (tiles == 0 || r0 >= rows) return;
-    // The ranges that hold its first and last tile: tile t lies in the last range
-    // whose start, x * total >> shift, is at most t.
-    const int first = (int)scalar((((before + 1) << shift) - 1) / total);
-    const int last = (int)scalar((((before + tiles) << shift) - 1) / total);
-    if (first == last) return;                                // one piece: written already
-    // The first piece is its range's second one unless the range starts with it.
-    const int first_slot = 2 * first + ((first * total >> shift) == before ? 0 : 1);
+    if (r0 >= rows || first == last) return;                  // one piece: written already
     const int team = threadIdx.x / kTeam, part = threadIdx.x % kTeam, i = kPer * blockIdx.z + (part >> 6);
 
     Joined<D, kTeams> joined;

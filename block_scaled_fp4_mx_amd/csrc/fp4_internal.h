@@ -210,7 +210,7 @@ struct AttnTree {
 size_t attn_tree_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads);
 hipError_t launch_attn_tree(const AttnTree& p, hipStream_t s);
 int64_t attn_blocks_columns(int drafts, int q_heads, int kv_heads, int head_dim, int lists);   // of workgroups
-size_t attn_blocks_workspace_bytes(int drafts, int q_heads, int head_dim, int kv_heads);
+size_t attn_blocks_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads);
 hipError_t launch_attn_blocks(const AttnTree& p, hipStream_t s);
 size_t attn_shared_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads, int groups);
 hipError_t launch_attn_shared(const AttnTree& p, hipStream_t s);

@@ -14,6 +14,10 @@
 // never go to memory as bf16.  A lane owns 8 consecutive values, 4, 8, 16 or 32 lanes
 // a head; a block of 32 is 4 neighbouring lanes, whose largest magnitude takes two
 // quad exchanges.  A workgroup takes one token: its angles are read once.
+//
+// 64 + 8 + 8 heads of 128 values: 8192 tokens (315 MB) 59 us, 5.3 TB/s, what a large copy
+// reaches; 64 tokens 3.1 us, one round trip to memory.  4097 tokens of 20 + 4 + 4 heads of
+// 96 (41 MB, a quarter of the lanes idle) 8.9 us, 4.6 TB/s.
 #include "fp4_internal.h"
 #include "quant_device.h"
 
@@ -191,6 +195,31 @@ void launch(const Args& a, int64_t tokens, bool interleaved, bool norm, hipStrea
         rope_append_kernel<kLanes, kHeads, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
+template <int kLanes>
+void launch(const Args& a, int64_t tokens, bool interleaved, bool norm, hipStream_t s) {
+    constexpr int kGroups = kThreads / kLanes;
+    const int slots = (a.heads + kGroups - 1) / kGroups;
+    // Many tokens: the number of heads to a lane group that leaves the fewest groups without
+    // one, the larger of two that leave as many (8192 tokens of 80 heads 59 us with five, 63
+    // with one or two; 2048 of 48 heads 9.1 with three, 9.7 with one).  Few: two, so that
+    // the heads spread over the CUs (512 tokens of 80 heads 5.6 us, 6.0 with five).
+    int per = slots < 2 ? 1 : 2;
+    if (slots >= 2 && tokens * a.heads >= (int64_t)kGroups * 4 * 1024) {
+        int least = 1 << 30;
+        for (int k = 2; k <= 5; ++k) {
+            const int all = (a.heads + kGroups * k - 1) / (kGroups * k) * k;
+            if (all <= least) least = all, per = k;
+        }
+    }
+    switch (per) {
+        case 1: return launch<kLanes, 1>(a, tokens, interleaved, norm, s);
+        case 2: return launch<kLanes, 2>(a, tokens, interleaved, norm, s);
+        case 3: return launch<kLanes, 3>(a, tokens, interleaved, norm, s);
+        case 4: return launch<kLanes, 4>(a, tokens, interleaved, norm, s);
+        default: return launch<kLanes, 5>(a, tokens, interleaved, norm, s);
+    }
+}
+
 }  // namespace
 
 hipError_t launch_kv_append_rope(const RopeAppend& p, hipStream_t s) {
@@ -209,13 +238,13 @@ hipError_t launch_kv_append_rope(const RopeAppend& p, hipStream_t s) {
     if (a.heads == 0) return hipSuccess;
     const int lanes = p.head_dim / 8;
     if (lanes <= 4)
-        launch<4, 1>(a, p.tokens, p.interleaved, p.norm, s);
+        launch<4>(a, p.tokens, p.interleaved, p.norm, s);
     else if (lanes <= 8)
-        launch<8, 1>(a, p.tokens, p.interleaved, p.norm, s);
+        launch<8>(a, p.tokens, p.interleaved, p.norm, s);
     else if (lanes <= 16)
-        launch<16, 1>(a, p.tokens, p.interleaved, p.norm, s);
+        launch<16>(a, p.tokens, p.interleaved, p.norm, s);
     else
-        launch<32, 1>(a, p.tokens, p.interleaved, p.norm, s);
+        launch<32>(a, p.tokens, p.interleaved, p.norm, s);
     return hipGetLastError();
 }
 
