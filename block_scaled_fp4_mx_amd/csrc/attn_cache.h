@@ -131,21 +131,28 @@ __device__ __forceinline__ int64_t tile_base(const TreeArgs& a, int g) {
 __device__ __forceinline__ int64_t tile_base_end(const TreeArgs& a) {
     return (int64_t)a.batch * a.rows / 16 + a.num_groups;
 }
-// The group of each lane's sequence b (ascending by lane), -1: none.  The bounds are
-// read 64 at a time, and searched by lane exchange.
-__device__ __forceinline__ int group_of(const TreeArgs& a, int b, int lane) {
-    int n = 0;                                            // bounds up to b
+// Of each lane's sequence b (ascending by lane): its group (-1: none), the group's first
+// sequence and prefix.  The bounds are read 64 at a time, with the prefixes beside them,
+// and searched by lane exchange.
+struct Member {
+    int group, first, prefix;
+};
+__device__ __forceinline__ Member member_of(const TreeArgs& a, int b, int lane) {
+    int n = 0, first = 0, next = 0, prefix = 0;           // n: bounds up to b
     for (int j = 0; j <= a.num_groups; j += 64) {
         const int v = j + lane <= a.num_groups ? bound_of(a, j + lane) : 0x7FFFFFFF;
+        const int p = j + lane < a.num_groups ? prefix_of(a, j + lane) : 0;
         int at = 0;
 #pragma unroll
         for (int m = 32; m; m /= 2) at += __shfl(v, at + m - 1, 64) <= b ? m : 0;
         at += at == 63 && __shfl(v, 63, 64) <= b ? 1 : 0;
-        n = at ? j + at : n;
+        const int from = max(at - 1, 0), first_here = __shfl(v, from, 64), prefix_here = __shfl(p, from, 64);
+        const int next_here = __shfl(v, min(at, 63), 64);
+        if (at == 0 && n == j) next = next_here;          // the bound behind the last one of the 64 before
+        if (at) n = j + at, first = first_here, prefix = prefix_here, next = next_here;
         if (__all(at < 64)) break;
     }
-    const int g = min(max(n - 1, 0), a.num_groups - 1);
-    return g >= 0 && bound_of(a, g) <= b && b < bound_of(a, g + 1) ? g : -1;    // bounds that do not ascend name no group
+    return n > 0 && n <= a.num_groups && first <= b && b < next ? Member{n - 1, first, prefix} : Member{-1, 0, 0};
 }
 
 // 64 sequences of the batch (kPrefix: groups) from first on, one to a lane, with the
@@ -195,9 +202,9 @@ __device__ __forceinline__ Chunk<kMode> chunk_at(const TreeArgs& a, int first, i
             c.seen = tokens_of(a, c.len, c.drafts);
             c.tiles = first + lane < a.batch ? tiles_of(c.seen, c.drafts) : 0;
             if constexpr (kMode == kOwn) {
-                const int g = group_of(a, b, lane), p = g < 0 ? 0 : prefix_of(a, g);
-                c.skip = c.len >= p ? p / kTile : 0;
-                c.token = c.skip ? g : -1, c.tokens = c.skip ? bound_of(a, g) : 0;
+                const Member x = member_of(a, b, lane);
+                c.skip = c.len >= x.prefix ? x.prefix / kTile : 0;
+                c.token = c.skip ? x.group : -1, c.tokens = c.skip ? x.first : 0;
                 if (c.tiles) c.tiles = max((int)c.tiles - c.skip, 1);
             }
         }

@@ -10,7 +10,7 @@
 // both.  The prefix is cut at whole tiles of 32 tokens; what is left of it goes with
 // each sequence's own tokens, as all of a sequence does that is shorter than the prefix.
 //
-// For many rows (attn_prefix_kernel) a workgroup takes 32 rows a wave of up to 8 waves.
+// For many rows (attend_prefix) a workgroup takes 32 rows a wave of up to 8 waves.
 // A tile of keys and values is widened to bf16 once for all of them, on its way from
 // global memory through registers to LDS (a lane has one block of 32 codes and its
 // scale), and the products are v_mfma_f32_32x32x16_bf16:
@@ -40,6 +40,13 @@ struct Wide {
     static constexpr int kItems = (2 * kBlocks + 64 * W - 1) / (64 * W);        // of a lane
     __device__ static constexpr int key_turn(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
     __device__ static constexpr int value_turn(int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); }
+};
+
+// A group of a chunk, kept in LDS: a piece needs the registers, and reading the bounds and
+// lengths again took each piece two round trips to memory.
+struct Group {
+    int per, seen, token, tokens;
+    int64_t tiles;
 };
 
 // Workgroup (block_x, head) of the prefix's many rows.
@@ -90,20 +97,29 @@ __device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_
         for (int i = 0; i < kTurns; ++i) rv[i] = S::kTile + r * S::kRow + (x ^ (4 * i)) * 16 + (lane & 1) * 8;
     }
 
+    __shared__ Group kept[64];
     int first = chunk.first;
+    auto keep = [&]() {
+        __syncthreads();                                     // the chunk before has been read
+        if (wave == 0) kept[lane] = {chunk.per, chunk.seen, chunk.token, chunk.tokens, (int64_t)chunk.tiles};
+        __syncthreads();
+    };
+    keep();
     for (int64_t at = lo; at < hi;) {
-        // Read again for every piece: a piece needs the registers.
-        if (group - first == 64) first = group;
-        if (at != lo || first != chunk.first) chunk = chunk_at<kPrefix>(a, first, lane, 0, kRows);
-        const int at_lane = group - first;
-        const int64_t cells = chunk.read(chunk.tiles, at_lane);
+        if (group - first == 64) {
+            first = group;
+            chunk = chunk_at<kPrefix>(a, first, lane, 0, kRows);
+            keep();
+        }
+        const Group& of = kept[group - first];
+        const int64_t cells = scalar(of.tiles);
         if (cells == 0) {
             ++group;
             continue;
         }
-        const int tiles = __builtin_amdgcn_readlane(chunk.per, at_lane), seen = __builtin_amdgcn_readlane(chunk.seen, at_lane);
-        const int token0 = __builtin_amdgcn_readlane(chunk.token, at_lane);
-        const int rows = __builtin_amdgcn_readlane(chunk.tokens, at_lane) * a.group;
+        const int tiles = __builtin_amdgcn_readfirstlane(of.per), seen = __builtin_amdgcn_readfirstlane(of.seen);
+        const int token0 = __builtin_amdgcn_readfirstlane(of.token);
+        const int rows = __builtin_amdgcn_readfirstlane(of.tokens) * a.group;
         const int64_t span = cells >> 32 ? (at - before) / tiles : (int64_t)((uint32_t)(at - before) / (uint32_t)tiles);
         const int t0 = (int)(at - before - span * tiles), t1 = (int)min(hi - at + t0, (int64_t)tiles);
         const int32_t* table = a.table + (int64_t)(token0 / a.drafts) * a.max_pages;
