@@ -559,7 +559,7 @@ def fp4_attn_shared_mx(q, cache: KvCache, page_table, seq_lens, groups, prefix_l
                        tree_mask=None, scale=None, stream=None):
     """fp4_attn_tree_mx where the sequences [groups[g], groups[g + 1]) (int32
     [num_groups + 1]) share their first prefix_lens[g] (int32 [num_groups]) tokens,
-    which are attended once for all of them."""
+    which are attended once for all of them, from the first sequence's pages."""
     _check("fp4_attn_shared_mx", _binding.fp4_attn_shared_mx(q, cache, page_table, seq_lens, groups, prefix_lens, out, workspace,
                                                              draft_lens, tree_mask, scale, stream))
 

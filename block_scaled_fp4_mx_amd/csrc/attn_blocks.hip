@@ -7,6 +7,15 @@
 // of workgroups of its own.  With one list for all heads the waves of a workgroup stage
 // neighbouring heads of the same rows together; with a list for each, a workgroup has
 // one head.
+//
+// What bounds it: latency for a few queries (lengths, list, page table and tiles are read
+// one after another, and the join waits for the walk), HBM for many.  Calls among others
+// on cold inputs, and kernel + join traced one call after another:
+//   64 sequences, 64 blocks of 64 tokens each, 64 / 8
+//     heads of 128 (290 MB)                            73 us, 4.0 TB/s     56 + 5
+//   one, 32 blocks of 64 tokens, 64 / 8 heads of 128   13 us, latency       9 + 4
+//   16, 4 drafts, 40 blocks of 32 tokens for each of
+//     4 heads of 64, 20 / 4 (20 MB)                    17 us, latency      13 + 4
 #include "attn_cache.h"
 
 namespace fp4 {

@@ -17,6 +17,21 @@
 //   S^T = K Q^T: lane (c = lane % 32, h = lane / 32) ends with row c and tokens
 //   8i + 4h .. 8i + 4h+3 of each 32, and the weights are the B operand of
 //   O^T = V^T P^T as they stand, V^T by transposing LDS reads of 4 tokens of one value.
+//
+// What bounds it: a prefix's bytes are few (51 MB for 64 samples of 16384 tokens, 10 us);
+// products and softmax are 35 GFLOP (30 us at a library product's rate) and as many vector
+// cycles.  A workgroup's tile of 64 tokens of 128 values (128 of 64) by 256 rows takes 2.55
+// us, before which lie 2 to 4 us until the last workgroup starts, 2.8 us of reading lengths
+// and bounds, and 4 us until the first tile is in LDS.  Calls among others, and kernel +
+// join traced one call after another:
+//   64 samples of 16384 tokens and up to 1024 own, 64 / 8 heads of 128     67 us   65 + 10
+//   54 sessions over 6 prefixes of 1000 .. 9000, 3 drafts, 20 / 4 of 64    32 us   26 +  7
+//   4 samples of 1000 tokens, 32 / 8 heads of 128 (by the walk)            16 us   11 +  5
+// Tried and slower: 4 waves to a workgroup (128 rows; 1 to 5%), the prefixes and the own
+// tokens in two launches (68 against 65 us for the first one's kernels), a round of
+// workgroups for each kind with the joins between.  Spans that fill fewer waves cost
+// nearly as much as full ones: 48 sessions, with 120 rows to a group instead of 135, take
+// 24 us, 72, with 180, 28, and 96, with 240, 32.
 #include "attn_cache.h"
 
 namespace fp4 {

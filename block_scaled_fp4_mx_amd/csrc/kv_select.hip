@@ -15,9 +15,9 @@
 // blocks, and what is taken is written in the blocks' order: no order of atomics shows.
 //
 // Bound by latency: the entries of 64 contexts of up to 131072 tokens are 5 MB.  A call
-// among others, on cold inputs: 4 queries for each of these 13.4 us; one query over 1562
-// blocks 8.4 us, of which 4 are the read of its 64-byte entries by one CU; 8 lists over
-// 12 contexts 10.5 us.
+// among others, on cold inputs: 4 queries for each of these 12.0 us (13.4 with neighbouring
+// queries on different XCDs); one query over 1562 blocks 8.3 us, of which 4 are the read of
+// its 64-byte entries by one CU; 8 lists over 12 contexts 8.7 us (10.6).
 #include "fp4_internal.h"
 #include "mma_core.h"
 #include "quant_device.h"
@@ -310,6 +310,12 @@ __device__ __forceinline__ uint32_t sum_upto(uint32_t v) {
 // trip to memory 0.7 to 1.2 us, and the meetings of the waves: so everything that is
 // known at the start is asked for at once, and the entries of all steps together.
 constexpr int kOneWaves = 16, kOneThreads = 64 * kOneWaves, kParts = 256, kNear = 64;
+// Workgroups are dealt to the 8 XCDs in turn: each XCD takes neighbouring queries, which
+// read the same entries (drafted tokens) or parts of the same lines (lists).
+__device__ __forceinline__ int query_of(int block, int blocks) {
+    const int xcd = block % 8;
+    return blocks / 8 * xcd + min(xcd, blocks % 8) + block / 8;
+}
 // kFromScores: the scores are in the workspace already.
 template <int kSteps, bool kFromScores>
 __global__ __launch_bounds__(kOneThreads) void select_one_kernel(const SelectArgs a) {
@@ -318,7 +324,7 @@ __global__ __launch_bounds__(kOneThreads) void select_one_kernel(const SelectArg
     __shared__ int near_block[kNear];
     __shared__ uint32_t all[5];                               // blocks, taken, lowest, highest, near
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row = blockIdx.x;
+    const int64_t row = kFromScores ? blockIdx.x : query_of(blockIdx.x, gridDim.x);
     const int64_t token = row / a.lists;
     const int list = (int)(row - token * a.lists);
     const int b = (int)(token / a.drafts), t = (int)(token - (int64_t)b * a.drafts);
@@ -513,12 +519,13 @@ hipError_t launch_kv_select(const KvSelect& p, hipStream_t s) {
     a.select = p.n_select, a.n_first = p.n_first, a.n_recent = p.n_recent;
     a.ids = p.ids, a.out_scores = p.out_scores, a.scores = static_cast<float*>(p.ws);
     const unsigned rows = (unsigned)(p.batch * p.drafts * p.lists);
-    // One launch where a workgroup has its query's entries in flight at once and every
-    // query a CU: 64 queries over 1000 blocks 8.6 us, in two launches 10.4; over 2000 12.6
-    // and 13.4; one over 4000, with more steps, 16.5 and 13.2; 64 x 8 drafted tokens, which
-    // read their sequence's entries once each, over 2000 27 and 17.
-    if (p.max_pages <= 2 * kOneThreads && p.dim <= 128 && rows <= 256) {
-        if (p.max_pages <= kOneThreads)
+    // One launch where a workgroup has its query's entries in flight at once and a CU has
+    // two workgroups of one step or one of two: one query over 500 blocks 6.6 us, in two
+    // launches 8.7; 64 x 8 drafted tokens over 1000 11.5 and 12.7; 64 x 4 over 2000 12.8 and
+    // 13.7, but 96 x 4 22.4 and 16.9; one over 4000, with more steps, 16.5 and 13.2.
+    const bool one_step = p.max_pages <= kOneThreads;
+    if (p.max_pages <= 2 * kOneThreads && p.dim <= 128 && rows <= (one_step ? 512 : 256)) {
+        if (one_step)
             select_one_kernel<1, false><<<rows, kOneThreads, 0, s>>>(a);
         else
             select_one_kernel<2, false><<<rows, kOneThreads, 0, s>>>(a);

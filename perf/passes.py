@@ -1,5 +1,5 @@
-"""Passes of one listed case of perf/operators.py through the library's kernels, as a
-profiler's target.
+"""Passes of one listed case of perf/operators.py or perf/more_operators.py through the
+library's kernels, as a profiler's target.
 usage: python3 perf/passes.py NAME COUNT
 """
 import os
@@ -11,15 +11,15 @@ sys.path.insert(0, ROOT)
 
 import torch  # noqa: E402
 
-from perf import operators  # noqa: E402
+from perf import more_operators, operators  # noqa: E402
 
 
 def main(name, count):
-    operators.own = True
-    case = next(c for c in operators.listed() if c["name"] == name)
-    state = operators.prepare(case, 1)
+    module, case = next((m, c) for m in (operators, more_operators) for c in m.listed() if c["name"] == name)
+    module.own = True
+    state = module.prepare(case, 1)
     for _ in range(count):
-        operators.run(state)
+        module.run(state)
     torch.cuda.synchronize()
     print(f"{name}: {count} passes")
 

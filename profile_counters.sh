@@ -1,6 +1,6 @@
 #!/bin/bash
 # rocprofv3 profiles of bench.py's stages and of the attention path's cases
-# (perf/operators.py) on an MI355X: kernel durations of
+# (perf/operators.py, perf/more_operators.py) on an MI355X: kernel durations of
 # the whole benchmark, HBM traffic (FETCH_SIZE, then WRITE_SIZE, one counter
 # per pass) of the main stages and of a plain 256 MiB device copy that
 # calibrates the counters, and the matrix-core busy cycles, MFMA operation
@@ -52,12 +52,15 @@ fi
 
 if [[ " $PARTS " == *" attention "* ]]; then
     for case in norm_rope_decode norm_rope_prompt norm_rope_odd prompt_short prompt_packed prompt_long \
-                tree_one_token tree_batch tree_long pages_speculate pages_fork pages_copy; do
+                tree_one_token tree_batch tree_long pages_speculate pages_fork pages_copy \
+                append_decode append_prompt append_odd shared_few shared_samples shared_sessions \
+                select_one select_batch select_heads blocks_one blocks_batch blocks_heads; do
         echo "kernel trace of $case"
         timeout -s KILL 120 rocprofv3 --kernel-trace --stats --output-format csv -d "$OUT/att_$case" -o run -- \
             python3 "$R/perf/passes.py" "$case" 23 > "$OUT/att_$case.log" 2>&1
     done
-    for case in norm_rope_prompt prompt_packed prompt_long tree_batch tree_long pages_copy; do
+    for case in norm_rope_prompt prompt_packed prompt_long tree_batch tree_long pages_copy \
+                append_prompt shared_samples shared_sessions select_batch blocks_batch; do
         for ctrs in "SQ_VALU_MFMA_BUSY_CYCLES SQ_INSTS_VALU SQ_LDS_BANK_CONFLICT SQ_LDS_IDX_ACTIVE GRBM_GUI_ACTIVE" \
                     FETCH_SIZE WRITE_SIZE; do
             echo "counters $ctrs on $case"

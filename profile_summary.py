@@ -11,8 +11,9 @@ Writes into the profiles directory:
                               LDS bank conflicts per launch of the MFMA-bound
                               stages' kernels;
   attention_kernels.txt       durations of the attention path's kernels in each
-                              listed case of perf/operators.py, and counters of
-                              the larger cases;
+                              listed case of perf/operators.py and
+                              perf/more_operators.py, and counters of the larger
+                              cases;
   traffic.json                the traffic and matrix-core figures for bench.py,
                               tagged with the digest of the kernel sources they
                               were taken on.
@@ -84,7 +85,7 @@ ROWS = {
 
 
 def short(name):
-    n = name.replace("(anonymous namespace)::", "").replace("fp4::", "")
+    n = name.replace("(anonymous namespace)::", "").replace("fp4::", "").replace("(Mode)", "")
     return n.split("(")[0][:70]
 
 
@@ -262,7 +263,7 @@ def attention_summary(raw, prof, calibration):
                        r["Workgroup_Size_X"])
                 kernels.setdefault(key, []).append((int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3)
         for (name, grid, group), us in kernels.items():
-            lines.append(f"{case:18s} {name:38s} {grid:>14s} {group:>5s} {len(us):6d} {sorted(us)[len(us) // 2]:10.1f} {min(us):9.1f}")
+            lines.append(f"{case:18s} {name:44s} {grid:>14s} {group:>5s} {len(us):6d} {sorted(us)[len(us) // 2]:10.1f} {min(us):9.1f}")
     if not lines:
         return
     counters = []
@@ -284,20 +285,20 @@ def attention_summary(raw, prof, calibration):
             if len(m) != 7:
                 continue
             busy = m["SQ_VALU_MFMA_BUSY_CYCLES"] / (m["GRBM_GUI_ACTIVE"] / XCCS * SIMDS)
-            counters.append(f"{case:18s} {k:38s} {100 * busy:8.1f}%  {m['SQ_INSTS_VALU']:10.3g}  {m['SQ_LDS_BANK_CONFLICT']:10.3g}"
+            counters.append(f"{case:18s} {k:44s} {100 * busy:8.1f}%  {m['SQ_INSTS_VALU']:10.3g}  {m['SQ_LDS_BANK_CONFLICT']:10.3g}"
                             f" / {m['SQ_LDS_IDX_ACTIVE']:<10.3g} {m['FETCH_SIZE'] * scale['FETCH_SIZE'] / 1e6:9.1f}"
                             f" {m['WRITE_SIZE'] * scale['WRITE_SIZE'] / 1e6:9.1f}")
     with open(os.path.join(prof, "attention_kernels.txt"), "w") as f:
-        f.write("Kernels of the attention path on MI355X: each listed case of perf/operators.py traced by itself.\n")
+        f.write("Kernels of the attention path on MI355X: each listed case of perf/operators.py and perf/more_operators.py\ntraced by itself.\n")
         f.write("command (per case): rocprofv3 --kernel-trace --stats --output-format csv -d <out>/att_<case> -o run -- "
                 "python3 perf/passes.py <case> 23\n")
         f.write(f"kernel sources digest: {source_digest()}\n\n")
-        f.write(f"{'case':18s} {'kernel':38s} {'grid (threads)':>14s} {'group':>5s} {'calls':>6s} {'median us':>10s} {'min us':>9s}\n")
+        f.write(f"{'case':18s} {'kernel':44s} {'grid (threads)':>14s} {'group':>5s} {'calls':>6s} {'median us':>10s} {'min us':>9s}\n")
         f.write("\n".join(lines) + "\n\n")
         f.write("Counters per launch (python3 perf/passes.py <case> 5, one block a run).  MFMA busy: SQ_VALU_MFMA_BUSY_CYCLES of\n"
                 "1024 SIMDs over GRBM_GUI_ACTIVE / 8 XCDs; fetched and written: FETCH_SIZE and WRITE_SIZE, each scaled by what it\n"
                 "reads for a plain 256 MiB device copy.\n\n")
-        f.write(f"{'case':18s} {'kernel':38s} {'MFMA busy':>9s}  {'VALU insts':>10s}  {'LDS conflict / active cycles':>25s} "
+        f.write(f"{'case':18s} {'kernel':44s} {'MFMA busy':>9s}  {'VALU insts':>10s}  {'LDS conflict / active cycles':>25s} "
                 f"{'read MB':>9s} {'wrote MB':>9s}\n")
         f.write("\n".join(counters) + "\n")
     print("\n".join(lines + counters))

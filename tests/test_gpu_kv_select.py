@@ -88,6 +88,11 @@ def test_more_queries_than_compute_units(dim):
     Index(dim, [16 * 90, 16 * 200 + 1, 30, 0, 16 * 130], 30, 2, dim, 16).check(20, draft_lens=[30, 17, 30, 1, 0])
 
 
+@pytest.mark.parametrize("drafts,width", [(64, 0), (41, 0), (31, 1100)])
+def test_more_queries_than_one_launch_takes(drafts, width):
+    Index(drafts, [16 * 90, 16 * 200 + 1, 30, 16 * 130, 16], drafts, 3, 64, 16, width=width).check(20)
+
+
 @pytest.mark.parametrize("blocks", [511, 512, 513, 1024, 1025, 2048, 2049, 4000, 8191])
 def test_many_blocks_in_registers(blocks):
     Index(blocks, [16 * blocks + 5, 100], 2, 1, 64, 16).check(50)
