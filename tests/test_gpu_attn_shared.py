@@ -86,6 +86,16 @@ def test_more_groups_than_lanes(groups):
     Shared(groups, spec, lens, 1, 2, 1, 64, 16).run()
 
 
+@pytest.mark.parametrize("groups", [64, 70, 150])
+def test_many_rows_of_more_groups_than_lanes(groups):
+    rng = np.random.default_rng(groups)
+    sizes = rng.integers(0, 3, groups)
+    sizes[62:66] = 0                                        # none where the lanes' groups end
+    spec = [(int(n), int(p)) for n, p in zip(sizes, rng.integers(0, 200, groups))]
+    lens = [p + int(rng.integers(0, 40)) for n, p in spec for _ in range(n)] + [5]
+    Shared(groups, spec, lens, 50, 4, 2, 64, 16, masks=_tree(1, len(lens), 50)).run()
+
+
 @pytest.mark.parametrize("d,q_heads,kv_heads,drafts", [(64, 8, 2, 1), (128, 16, 2, 3), (128, 8, 1, 1), (256, 4, 2, 1)])
 def test_long_prefixes_split_over_workgroups(d, q_heads, kv_heads, drafts):
     Shared(d, [(5, 6000)], [6000, 6100, 6001, 7200, 6031], drafts, q_heads, kv_heads, d, 64).run()
