@@ -220,3 +220,41 @@ def test_replays_and_the_end_of_the_workspace():
         torch.cuda.synchronize()
         assert torch.equal(a["out"], want)
     assert (ws[-512:] == 0xEE).all()
+
+
+@pytest.mark.parametrize("members", [3, 90])
+def test_an_empty_pool_table_batch_and_no_drafts(members):
+    """By the walk and with many rows."""
+    x = Shared(15, [(members, 64)], [70] * members, 1, 4, 2, 64, 16)
+    a = x.device()
+    F.fp4_attn_shared_mx(**(a | dict(cache=F.KvCache(*(t[:0] for t in a["cache"][:4]), 16))))
+    assert (a["out"] == 0).all()
+    a["out"].fill_(7.0)
+    F.fp4_attn_shared_mx(**(a | dict(page_table=a["page_table"][:, :0])))
+    assert (a["out"] == 0).all()
+    a["out"].fill_(7.0)
+    F.fp4_attn_shared_mx(**(a | dict(draft_lens=_i32([0] * members))))
+    assert (a["out"] == 7.0).all()
+    F.fp4_attn_shared_mx(a["q"][:0], a["cache"], a["page_table"][:0], a["seq_lens"][:0], a["groups"], a["prefix_lens"], a["out"][:0],
+                         a["workspace"])
+
+
+@pytest.mark.parametrize("d,q_heads,kv_heads", [(64, 10, 2), (128, 8, 2), (256, 4, 1)])
+def test_many_rows_replayed_and_the_end_of_the_workspace(d, q_heads, kv_heads):
+    rng = np.random.default_rng(d)
+    lens = (900 + rng.integers(0, 200, 45)).tolist()
+    x = Shared(16, [(40, 900), (5, 333)], lens, 1, q_heads, kv_heads, d, 16, draft_lens=rng.integers(0, 2, 45).tolist())
+    a = x.run()
+    want = a["out"].clone()
+    ws = torch.full((a["workspace"].numel() + 512,), 0xEE, dtype=torch.uint8, device=DEV)
+    args = a | dict(workspace=ws[:-512])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        F.fp4_attn_shared_mx(**args)
+    for _ in range(3):
+        a["out"].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a["out"], want)
+    assert (ws[-512:] == 0xEE).all()
