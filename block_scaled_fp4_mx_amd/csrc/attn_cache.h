@@ -117,11 +117,10 @@ __device__ __forceinline__ T sum_upto(T v) {
     return v + moved<0x143, 0xC>(v);
 }
 
-// Tokens of a group's prefix that are attended once for all: whole tiles, as far as the
-// table's row goes.
-__device__ __forceinline__ int prefix_of(const TreeArgs& a, int g) {
-    return tokens_of(a, max(a.prefix_lens[g], 0), 0) & ~(kTile - 1);
-}
+__device__ __forceinline__ int prefix_of(const TreeArgs& a, int g) { return max(a.prefix_lens[g], 0); }
+// Tokens of a prefix that are attended once for all: whole tiles, as far as the table's
+// row goes.
+__device__ __forceinline__ int shared_of(const TreeArgs& a, int prefix) { return tokens_of(a, prefix, 0) & ~(kTile - 1); }
 // Sequence number i of the bounds of the groups, within the batch.
 __device__ __forceinline__ int bound_of(const TreeArgs& a, int i) { return min(max(a.groups[i], 0), a.batch); }
 // The row tiles (of 16 rows) before a group's, in an order of all groups' rows.
@@ -184,7 +183,7 @@ __device__ __forceinline__ Chunk<kMode> chunk_at(const TreeArgs& a, int first, i
         c.token = bound_of(a, g);
         const int members = max(bound_of(a, g + 1) - c.token, 0);
         c.token *= a.drafts, c.tokens = members * a.drafts;
-        c.len = c.seen = prefix_of(a, g), c.drafts = 0;
+        c.len = c.seen = shared_of(a, prefix_of(a, g)), c.drafts = 0;
         c.per = (c.seen + a.prefix_tile - 1) / a.prefix_tile;
         c.tiles = there ? (uint64_t)(((int64_t)members * a.rows + span - 1) / span) * (uint32_t)c.per : 0;
     } else {
@@ -203,7 +202,8 @@ __device__ __forceinline__ Chunk<kMode> chunk_at(const TreeArgs& a, int first, i
             c.tiles = first + lane < a.batch ? tiles_of(c.seen, c.drafts) : 0;
             if constexpr (kMode == kOwn) {
                 const Member x = member_of(a, b, lane);
-                c.skip = c.len >= x.prefix ? x.prefix / kTile : 0;
+                // A shorter sequence has its own table's rows, also of the tiles that it has whole.
+                c.skip = c.len >= x.prefix ? shared_of(a, x.prefix) / kTile : 0;
                 c.token = c.skip ? x.group : -1, c.tokens = c.skip ? x.first : 0;
                 if (c.tiles) c.tiles = max((int)c.tiles - c.skip, 1);
             }

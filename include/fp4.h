@@ -624,8 +624,8 @@ size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int
  * ascending; values are taken as within [0, batch]), and their first prefix_lens[g]
  * (int32 [num_groups]) tokens are the same: the cache rows that the table of the group's
  * first sequence names for them are read, once for the whole group (that sequence has to
- * hold them, as long as any of the group is longer than they are).  Sequences outside
- * every group, and those shorter than their group's prefix, are attended by their own
+ * hold them while any of the group has prefix_lens[g] tokens or more).  Sequences outside
+ * every group, and those with seq_lens[b] < prefix_lens[g], are attended by their own
  * table alone.  The result is fp4_attn_tree_mx's up to the order of the fp32 sums; the
  * order depends on the shapes, lengths and groups alone.
  * Everything else is as there.  num_groups 0: nothing is shared.
