@@ -711,7 +711,9 @@ __device__ __forceinline__ void walk(const TreeArgs& a, uint8_t* staging, int bl
                     float x = top[n] * a.scale2;
                     x = fmaxf(x, __shfl_xor(x, 16, 64));
                     x = fmaxf(x, __shfl_xor(x, 32, 64));
-                    const float up = fmaxf(m[n], x), alpha = exp2_hw(m[n] - up);
+                    // kPrefix: the others' rows are those of other sequences, or nobody's; a row
+                    // moves when its own scores rise, so that its bits are its own.
+                    const float up = kMode == kPrefix && !(x > m[n] + kSlack) ? m[n] : fmaxf(m[n], x), alpha = exp2_hw(m[n] - up);
                     m[n] = up;
                     sum[n] *= alpha;
 #pragma unroll

@@ -213,7 +213,7 @@ __device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_
             top *= a.scale2;
             if (__any(top > m + kSlack)) {
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float up = fmaxf(m, top);
+                const float up = top > m + kSlack ? top : m;         // each row by its own scores alone
                 const float alpha = exp2_hw(m - up);
                 m = up;
 #pragma unroll

@@ -626,8 +626,10 @@ size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int
  * first sequence names for them are read, once for the whole group (that sequence has to
  * hold them while any of the group has prefix_lens[g] tokens or more).  Sequences outside
  * every group, and those with seq_lens[b] < prefix_lens[g], are attended by their own
- * table alone.  The result is fp4_attn_tree_mx's up to the order of the fp32 sums; the
- * order depends on the shapes, lengths and groups alone.
+ * table alone.  The result is fp4_attn_tree_mx's up to the rounding of the weights (each
+ * relative to its row's running reference) and the order of the fp32 sums; the order
+ * depends on the shapes, lengths and groups alone, and a sequence's bits on no other
+ * sequence's queries, nor on query rows i >= draft_lens[b], which may hold anything.
  * Everything else is as there.  num_groups 0: nothing is shared.
  * workspace: fp4_attn_shared_workspace_bytes(...) bytes; calls (and replays) that share
  * one are ordered by the caller.
