@@ -979,7 +979,7 @@ int fp4_attn_shared_mx(const void* q, int64_t ld_q, const fp4_kv_cache* cache, c
 
 size_t fp4_kv_select_workspace_bytes(int64_t batch, int drafts, int lists, int64_t max_pages) {
     if (batch <= 0 || batch >= 65536 || drafts < 1 || drafts > 64 || lists < 1 || lists > 4096 || max_pages < 0 ||
-        max_pages >= (int64_t)1 << 31)
+        max_pages >= (int64_t)1 << 31 || batch * drafts * lists >= (int64_t)1 << 23)
         return 0;
     return fp4::kv_select_workspace_bytes(batch, drafts, lists, max_pages);
 }

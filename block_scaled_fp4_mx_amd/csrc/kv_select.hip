@@ -42,6 +42,7 @@ struct SelectArgs {
     int32_t* ids;
     float* out_scores;                     // or NULL
     float* scores;
+    int64_t first_row;                     // of a launch that selects from the scores in the workspace
 };
 
 __device__ __forceinline__ int complete_blocks(const SelectArgs& a, int b) {
@@ -194,13 +195,13 @@ __device__ __forceinline__ Threshold threshold_by_bits(uint32_t low, uint32_t hi
     return t;
 }
 
-// Workgroup x: query x (token and list), from its scores in the workspace, which are
-// read again where they are needed.
+// Workgroup x: query first_row + x (token and list), from its scores in the workspace,
+// which are read again where they are needed.
 __global__ __launch_bounds__(kThreads) void select_blocks_kernel(const SelectArgs a) {
     __shared__ uint32_t hist[256], found[3];
     __shared__ int sums[kWaves][4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row = blockIdx.x;
+    const int64_t row = a.first_row + blockIdx.x;
     const int64_t token = row / a.lists;
     const int b = (int)(token / a.drafts), t = (int)(token - (int64_t)b * a.drafts);
     if (a.draft_lens && t >= a.draft_lens[b]) return;
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(kOneThreads) void select_one_kernel(const SelectArg
     __shared__ int near_block[kNear];
     __shared__ uint32_t all[5];                               // blocks, taken, lowest, highest, near
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row = kFromScores ? blockIdx.x : query_of(blockIdx.x, gridDim.x);
+    const int64_t row = kFromScores ? a.first_row + blockIdx.x : query_of(blockIdx.x, gridDim.x);
     const int64_t token = row / a.lists;
     const int list = (int)(row - token * a.lists);
     const int b = (int)(token / a.drafts), t = (int)(token - (int64_t)b * a.drafts);
@@ -503,6 +504,10 @@ __global__ __launch_bounds__(kOneThreads) void select_one_kernel(const SelectArg
     }
 }
 
+// Queries of a launch: a grid has fewer than 2^32 threads.
+constexpr int64_t kMostRows = 1 << 21;
+static_assert(kMostRows * kOneThreads < (int64_t)1 << 32);
+
 int64_t pitch_of(int64_t max_pages) { return (max_pages + 15) / 16 * 16; }
 
 }  // namespace
@@ -518,7 +523,7 @@ hipError_t launch_kv_select(const KvSelect& p, hipStream_t s) {
     a.seq_lens = p.seq_lens, a.draft_lens = p.draft_lens, a.page_size = (int)p.page_size, a.drafts = p.drafts;
     a.select = p.n_select, a.n_first = p.n_first, a.n_recent = p.n_recent;
     a.ids = p.ids, a.out_scores = p.out_scores, a.scores = static_cast<float*>(p.ws);
-    const unsigned rows = (unsigned)(p.batch * p.drafts * p.lists);
+    const int64_t rows = p.batch * p.drafts * p.lists;
     // One launch where a workgroup has its query's entries in flight at once and a CU has
     // two workgroups of one step or one of two: one query over 500 blocks 6.6 us, in two
     // launches 8.7; 64 x 8 drafted tokens over 1000 11.5 and 12.7; 64 x 4 over 2000 12.8 and
@@ -526,9 +531,9 @@ hipError_t launch_kv_select(const KvSelect& p, hipStream_t s) {
     const bool one_step = p.max_pages <= kOneThreads;
     if (p.max_pages <= 2 * kOneThreads && p.dim <= 128 && rows <= (one_step ? 512 : 256)) {
         if (one_step)
-            select_one_kernel<1, false><<<rows, kOneThreads, 0, s>>>(a);
+            select_one_kernel<1, false><<<(unsigned)rows, kOneThreads, 0, s>>>(a);
         else
-            select_one_kernel<2, false><<<rows, kOneThreads, 0, s>>>(a);
+            select_one_kernel<2, false><<<(unsigned)rows, kOneThreads, 0, s>>>(a);
         return hipGetLastError();
     }
     if (p.num_pages && p.max_pages) {
@@ -537,13 +542,18 @@ hipError_t launch_kv_select(const KvSelect& p, hipStream_t s) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (p.max_pages <= 2 * kOneThreads)
-        select_one_kernel<2, true><<<rows, kOneThreads, 0, s>>>(a);
-    else if (p.max_pages <= 8 * kOneThreads)
-        select_one_kernel<8, true><<<rows, kOneThreads, 0, s>>>(a);
-    else
-        select_blocks_kernel<<<rows, kThreads, 0, s>>>(a);
-    return hipGetLastError();
+    for (; a.first_row < rows; a.first_row += kMostRows) {
+        const unsigned n = (unsigned)(rows - a.first_row < kMostRows ? rows - a.first_row : kMostRows);
+        if (p.max_pages <= 2 * kOneThreads)
+            select_one_kernel<2, true><<<n, kOneThreads, 0, s>>>(a);
+        else if (p.max_pages <= 8 * kOneThreads)
+            select_one_kernel<8, true><<<n, kOneThreads, 0, s>>>(a);
+        else
+            select_blocks_kernel<<<n, kThreads, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace fp4
