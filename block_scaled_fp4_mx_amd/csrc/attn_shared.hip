@@ -441,9 +441,8 @@ struct SharedLayout {
     int own_ranges() const { return blocks / own.columns; }
     int prefix_ranges() const { return blocks / prefix_columns; }
 };
-SharedLayout shared_layout(int64_t batch, int drafts, int q_heads, int kv_heads, int head_dim, int groups) {
-    const int own_rows = drafts * (q_heads / kv_heads);
-    const int64_t rows = batch * own_rows / groups;
+// own_rows: of a sequence, rows: of a group.
+SharedLayout shared_layout(int own_rows, int64_t rows, int kv_heads, int head_dim) {
     SharedLayout l;
     l.waves = rows <= 64 ? 0 : kWideWaves;
     l.own = layout_of(l.waves ? own_rows : (int)(rows < own_rows ? own_rows : rows), kv_heads, head_dim);
@@ -469,18 +468,27 @@ int64_t spans(const SharedLayout& l, int64_t batch, int rows, int groups) { retu
 }  // namespace
 
 // In this order: own_pieces, span_pieces, the own tokens' partial results, the prefixes'.
+// The largest of all layouts that up to 64 rows to a group (their row tiles change at 16
+// and 32) and more may get, and of the attention without groups: each grows with the batch
+// and the groups, so that a workspace serves every smaller step.
 size_t attn_shared_workspace_bytes(int64_t batch, int drafts, int q_heads, int head_dim, int kv_heads, int groups) {
-    if (groups == 0) return attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
+    size_t most = attn_tree_workspace_bytes(drafts, q_heads, head_dim, kv_heads);
+    if (groups == 0) return most;
     const int rows = drafts * (q_heads / kv_heads);
-    const SharedLayout l = shared_layout(batch, drafts, q_heads, kv_heads, head_dim, groups);
-    return (size_t)batch * sizeof(int4) + (size_t)((spans(l, batch, rows, groups) + 1) / 2) * sizeof(int4) +
-           part_bytes(own_tiles(l, batch, rows, kv_heads) + prefix_tiles(l, batch, rows, kv_heads, groups), head_dim);
+    for (const int group_rows : {16, 32, 64, 65}) {
+        const SharedLayout l = shared_layout(rows, group_rows, kv_heads, head_dim);
+        const size_t bytes =
+            (size_t)batch * sizeof(int4) + (size_t)((spans(l, batch, rows, groups) + 1) / 2) * sizeof(int4) +
+            part_bytes(own_tiles(l, batch, rows, kv_heads) + prefix_tiles(l, batch, rows, kv_heads, groups), head_dim);
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 hipError_t launch_attn_shared(const AttnTree& p, hipStream_t s) {
     if (p.num_groups == 0) return launch_attn_tree(p, s);
     const int rows = p.drafts * (p.q_heads / p.kv_heads);
-    const SharedLayout l = shared_layout(p.batch, p.drafts, p.q_heads, p.kv_heads, p.head_dim, p.num_groups);
+    const SharedLayout l = shared_layout(rows, p.batch * rows / p.num_groups, p.kv_heads, p.head_dim);
     TreeArgs own = cache_args(p, l.own);
     own.groups = p.groups, own.prefix_lens = p.prefix_lens, own.num_groups = p.num_groups;
     own.own_pieces = static_cast<int4*>(p.ws);

@@ -631,8 +631,8 @@ size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int
  * depends on the shapes, lengths and groups alone, and a sequence's bits on no other
  * sequence's queries, nor on query rows i >= draft_lens[b], which may hold anything.
  * Everything else is as there.  num_groups 0: nothing is shared.
- * workspace: fp4_attn_shared_workspace_bytes(...) bytes; calls (and replays) that share
- * one are ordered by the caller.
+ * workspace: fp4_attn_shared_workspace_bytes(...) bytes, which serve every smaller batch
+ * and num_groups too; calls (and replays) that share one are ordered by the caller.
  * Errors: as there; num_groups negative -> FP4_ERR_INVALID; num_groups of 2^20 or more, or
  * batch * drafts * q_heads / kv_heads of 2^31 or more -> FP4_ERR_SHAPE.
  */
