@@ -15,7 +15,7 @@
 //     heads of 128 (290 MB)                            73 us, 4.0 TB/s     56 + 5
 //   one, 32 blocks of 64 tokens, 64 / 8 heads of 128   13 us, latency       9 + 4
 //   16, 4 drafts, 40 blocks of 32 tokens for each of
-//     4 heads of 64, 20 / 4 (20 MB)                    17 us, latency      13 + 4
+//     4 heads of 64, 20 / 4 (20 MB)             17 .. 18 us, latency      13 + 4
 #include "attn_cache.h"
 
 namespace fp4 {

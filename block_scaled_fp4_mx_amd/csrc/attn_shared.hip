@@ -24,9 +24,15 @@
 // us, before which lie 2 to 4 us until the last workgroup starts, 2.8 us of reading lengths
 // and bounds, and 4 us until the first tile is in LDS.  Calls among others, and kernel +
 // join traced one call after another:
-//   64 samples of 16384 tokens and up to 1024 own, 64 / 8 heads of 128     67 us   65 + 10
+//   64 samples of 16384 tokens and up to 1024 own, 64 / 8 heads of 128     69 us   66 + 10
 //   54 sessions over 6 prefixes of 1000 .. 9000, 3 drafts, 20 / 4 of 64    32 us   26 +  7
-//   4 samples of 1000 tokens, 32 / 8 heads of 128 (by the walk)            16 us   11 +  5
+//   4 samples of 1500 tokens, 32 / 8 heads of 128 (by the walk)            16 us   12 +  5
+//   32 samples of 16384 tokens and up to 1024 own, 32 / 4 heads of 256     79 us
+// (the last one's floor is 15 us, and its kernel spills 37 vector registers).  By the counters of
+// the samples the matrix cores are busy for 22% of the kernel and LDS for about as long, 27% of
+// that in bank conflicts of the widened tiles' stores (512 cycles a tile: value_turn and
+// key_turn serve the reads); a wave does a tile's scores, softmax and second product in turn, so
+// little of this overlaps.
 // Tried and slower: 4 waves to a workgroup (128 rows; 1 to 5%), the prefixes and the own
 // tokens in two launches (68 against 65 us for the first one's kernels), a round of
 // workgroups for each kind with the joins between.  Spans that fill fewer waves cost
@@ -259,7 +265,8 @@ __device__ __forceinline__ void attend_prefix(const TreeArgs& a, uint8_t* tiles_
         if (t0 + 1 < t1) load(t0 + 1);
         // Of the two waves of a SIMD one widens before its products and one behind them, so
         // that the matrix core has work meanwhile.  One copy of the step, not one for each
-        // buffer: at D = 256 two do not fit the registers.
+        // buffer: at D = 128 it takes 220 to 229 of 256 registers, at D = 256 it spills 37 (152
+        // bytes of scratch a lane) as it is.
         const bool early = wave < W / 2;
 #pragma unroll 1
         for (int t = t0; t < t1; ++t) {
@@ -344,7 +351,11 @@ __device__ __forceinline__ int ranges_of(int64_t tiles, int64_t most) {
     return tiles == 0 ? 0 : (int)min(max(tiles / kMinTiles, (int64_t)1), max(most, (int64_t)1));
 }
 // What a tile of the own tokens costs a workgroup, of what one of the prefix does (heads of
-// 128: 1.0 and 2.6 us).  0.33 to 0.5 take 68 to 73 us for 64 samples, 30 to 34 for sessions.
+// 128: 1.0 and 2.6 us).  Calls with 0.3, 0.37, 0.5 and 1:
+//   64 samples of 16384 tokens, up to 1024 own, 64 / 8 heads of 128    70   69   73   81 us
+//   the same, heads of 64                                             49   48   53   56
+//   32 samples, 32 / 4 heads of 256 (tiles of 32 tokens both)          85   79   77   77
+//   54 sessions, 20 / 4 heads of 64 | 128 | 256    32   32   34   36 | 44   42   43   46 | 97   93   91   96
 constexpr double own_cost(int waves) { return waves ? 0.37 : 1.0; }
 
 template <int D, int W>
@@ -433,7 +444,17 @@ __global__ __launch_bounds__(64 * kPer * kTeams) void attn_shared_join_kernel(co
 
 // How the call is laid out, from its shapes alone.  The prefixes are attended by the walk,
 // laid out for as many rows as a group has on average, or by attend_prefix; spans of rows
-// are laid end to end, so that columns are heads alone.
+// are laid end to end, so that columns are heads alone.  Walk and attend_prefix, one group
+// with up to 200 own tokens, 64 / 8 heads of 128 (32 / 4 of 256):
+//   rows of the group                    16        32        64        96       128
+//   prefix of 2000 tokens           17 | 18   19 | 18   22 | 22   24 | 22   26 | 23 us
+//   of 16000                        24 | 29   28 | 29   32 | 33   43 | 36   41 | 40
+//   of 2000, heads of 256           20 | 23   21 | 24   24 | 27   30 | 34   38 | 35
+//   of 16000, heads of 256          28 | 39   42 | 41   51 | 46   72 | 61   74 | 62
+// The average is over num_groups and the whole batch: the bounds are on the device.  Empty
+// groups and sequences outside groups spoil it: the 64 samples above take 69 us alone, 83 as
+// one of 8 groups of which the others are empty and 102 as one of 64; a group of two among 64
+// sequences of 16384 tokens takes 221, the attention without groups 149.
 struct SharedLayout {
     Layout own;
     int waves;                             // of attend_prefix; 0: the walk, laid out as own

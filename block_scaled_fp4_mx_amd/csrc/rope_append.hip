@@ -15,9 +15,10 @@
 // a head; a block of 32 is 4 neighbouring lanes, whose largest magnitude takes two
 // quad exchanges.  A workgroup takes one token: its angles are read once.
 //
-// 64 + 8 + 8 heads of 128 values: 8192 tokens (315 MB) 59 us, 5.3 TB/s, what a large copy
-// reaches; 64 tokens 3.1 us, one round trip to memory.  4097 tokens of 20 + 4 + 4 heads of
-// 96 (41 MB, a quarter of the lanes idle) 8.9 us, 4.6 TB/s.
+// A call among others, 64 + 8 + 8 heads of 128 values: 8192 tokens (315 MB) 59 us, 5.3 TB/s,
+// what a large copy reaches; 64 tokens 3.6 to 4.2 us, 3.2 of them the kernel, one round trip to
+// memory.  4097 tokens of 20 + 4 + 4 heads of 96 (41 MB, a quarter of the lanes idle) 8.9 us,
+// 4.6 TB/s.  With norms 73 us, 4.0 and 11.3.
 #include "fp4_internal.h"
 #include "quant_device.h"
 

@@ -630,7 +630,9 @@ size_t fp4_attn_tree_workspace_bytes(int64_t batch, int drafts, int q_heads, int
  * relative to its row's running reference) and the order of the fp32 sums; the order
  * depends on the shapes, lengths and groups alone, and a sequence's bits on no other
  * sequence's queries, nor on query rows i >= draft_lens[b], which may hold anything.
- * Everything else is as there.  num_groups 0: nothing is shared.
+ * Everything else is as there.  num_groups 0: nothing is shared.  The work is laid out for
+ * batch / num_groups sequences to a group, so empty groups and a batch that is mostly
+ * outside groups cost time, not correctness.
  * workspace: fp4_attn_shared_workspace_bytes(...) bytes, which serve every smaller batch
  * and num_groups too; calls (and replays) that share one are ordered by the caller.
  * Errors: as there; num_groups negative -> FP4_ERR_INVALID; num_groups of 2^20 or more, or
